@@ -16,7 +16,9 @@
 
 #include "hisparse.h"
 #include "hisparse_measure.h"
+#include "hisparse_rows4.h"
 #include "hs_common.cuh"
+#include "rows4.cuh"
 
 // Scratch of the allocation-free swap-in (hisparse_swap_in_noalloc): the miss
 // plan that its resolve grid hands to its copy grid lives in this fixed array
@@ -1122,6 +1124,38 @@ int hisparse_swap_in_noalloc(hisparse_t h, int32_t layer, const int32_t *topk_id
     c.programmatic = true;
     c.only_if = nullptr;
     return cuda_status(hs::launch_replay(c, as_stream(stream)));
+}
+
+// ---- eviction by accumulated weight (the calls without a handle are in rows4.cu) ----
+
+int hisparse_evict(hisparse_t h, int32_t layer, const float *weights, int64_t weights_stride,
+                   int64_t weights_tokens, const int32_t *seq_lens, int32_t keep_recent, int32_t n, const int32_t *want,
+                   int32_t *out_slots, int32_t *out_counts, void *stream)
+{
+    if (!h || (!weights && weights_tokens != 0) || !seq_lens) return HISPARSE_ERR_INVALID_ARG;
+    if (weights_tokens < 0 || weights_stride < weights_tokens || keep_recent < 0 || n < 1 ||
+        n > h->D)
+        return HISPARSE_ERR_INVALID_ARG;
+    if (layer < 0 || layer >= h->L || h->anchor[layer] >= 0) return HISPARSE_ERR_LAYER;
+    if (!on_own_device(h)) return HISPARSE_ERR_INVALID_ARG;
+    hs::EvictLaunch e = {};
+    e.R = h->R;
+    e.D = h->D;
+    e.n = n;
+    e.weights = weights;
+    e.weights_stride = weights_stride;
+    e.weights_tokens = weights_tokens;
+    e.st = h->state[layer];
+    e.slot2tok = e.st.slot2tok;
+    e.seq_lens = seq_lens;
+    e.keep_recent = keep_recent;
+    e.want = want;
+    e.out_slots = out_slots;
+    e.out_counts = out_counts;
+    e.host_off = h->d_off;
+    e.protect_calls = (uint32_t)h->protect_calls;
+    note_launch_layers(h, as_stream(stream), &layer, 1);
+    return cuda_status(hs::launch_evict(e, as_stream(stream)));
 }
 
 // ---- measurement kernels ---------------------------------------------------

@@ -23,6 +23,7 @@ ERR_INVALID_ARG, ERR_LAYOUT, ERR_CAPACITY, ERR_LAYER = -1, -2, -3, -4
 ERR_CUDA, ERR_NO_MEMORY, ERR_UNSUPPORTED, ERR_ALIGNMENT = -5, -6, -7, -8
 STATUS_OK, STATUS_BAD_INDEX, STATUS_DUPLICATE, STATUS_BAD_SEQ_LEN, STATUS_BAD_POSITION = 0, 1, 2, 3, 4
 STATUS_BAD_RESIDENT, STATUS_NO_HOST_ROW, STATUS_CAPACITY, STATUS_COPY_TIMEOUT = 5, 6, 7, 8
+STATUS_ATTEND_TIMEOUT = 9
 
 
 def STATUS_BIT(code: int) -> int:
@@ -33,6 +34,11 @@ def STATUS_BIT(code: int) -> int:
 RESIDENT_FLAG = 1 << 30
 COPY_FUSED, COPY_SPLIT, COPY_AUTO = 1, 2, 3
 NOALLOC_SCRATCH_BYTES = 8 << 20   # HISPARSE_NOALLOC_SCRATCH_BYTES
+
+# 4-bit rows (include/hisparse_rows4.h)
+ROW4_LATENT, ROW4_ROPE, ROW4_VALUES, ROW4_BYTES = 512, 64, 576, 416
+BF16, F16 = 0, 1
+MAX_HEADS = 1024
 
 
 class HiSparseError(RuntimeError):
@@ -52,6 +58,27 @@ class Layout(ctypes.Structure):
 
 class Plan(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_void_p), ("counts", ctypes.c_void_p)]
+
+
+class AttendArgs(ctypes.Structure):
+    _fields_ = [("num_requests", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("q_request_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64),
+                ("rows", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("request_stride", ctypes.c_int64), ("rows_per_request", ctypes.c_int32),
+                ("scale", ctypes.c_float),
+                ("slot_ids", ctypes.c_void_p), ("ids_stride", ctypes.c_int64),
+                ("resident_rows", ctypes.c_void_p), ("resident_stride", ctypes.c_int64),
+                ("resident_count", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_request_stride", ctypes.c_int64),
+                ("out_head_stride", ctypes.c_int64),
+                ("lse", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p), ("weights_stride", ctypes.c_int64),
+                ("weights_tokens", ctypes.c_int64),
+                ("positions", ctypes.c_void_p), ("positions_stride", ctypes.c_int64),
+                ("status", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -102,6 +129,12 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "hisparse_synthetic_compute": [P, I64, I32, I32, P],
         "hisparse_link_probe": [P, P, I64, I32, P],
         "hisparse_link_gather": [P, I64, P, I64, P, I32, P],
+        "hisparse_pack_rows": [P, I64, I32, I64, P, I64, P],
+        "hisparse_unpack_rows": [P, I64, I64, P, I64, I32, P],
+        "hisparse_attend": [P, P],
+        "hisparse_attend_workspace": [I32, I32, I32, I32, P],
+        "hisparse_evict_select": [I32, I32, P, I64, I64, P, P, I32, I32, P, P, P, P],
+        "hisparse_evict": [P, I32, P, I64, I64, P, I32, I32, P, P, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -407,6 +440,31 @@ class HiSparse:
         _check(self.lib.hisparse_set_programmatic_launch(self.h, 1 if on else 0),
                "hisparse_set_programmatic_launch")
 
+    # -- 4-bit rows ---------------------------------------------------------
+    def attend(self, layer: int, q, slot_ids, out, scale: float, lse=None, positions=None,
+               weights=None, resident_rows=None, workspace=None, stream=None) -> None:
+        """attend() over the layer's hot buffer (row_bytes must be
+        ROW4_BYTES); data errors go to this handle's status words."""
+        if self.B != ROW4_BYTES:
+            raise ValueError(f"row_bytes is {self.B}: attention reads {ROW4_BYTES}-byte rows")
+        _attend(q, self.device_buffer_ptr(layer), self.B, self.D * self.B, self.R, self.D, slot_ids,
+                out, scale, lse, positions, weights, resident_rows, self.status_ptr(), workspace,
+                stream)
+
+    def evict(self, layer: int, weights, seq_lens, n: int, keep_recent: int = 0, want=None,
+              out_slots=None, out_counts=None, stream=None) -> None:
+        """hisparse_evict: free, per request, up to n (or want[r]) hot slots
+        of the least accumulated weight (weights: float32 [R][tokens])."""
+        _rows_of(weights, "weights", "torch.float32", self.R)
+        _ints(seq_lens, "seq_lens", (self.R,))
+        _ints(want, "want", (self.R,))
+        _ints(out_slots, "out_slots", (self.R, n))
+        _ints(out_counts, "out_counts", (self.R,))
+        _check(self.lib.hisparse_evict(self.h, layer, _addr(weights),
+                                       _row_stride(weights), weights.shape[1], _addr(seq_lens), keep_recent, n, _addr(want),
+                                       _addr(out_slots), _addr(out_counts), _stream(stream)),
+               "hisparse_evict")
+
     def set_copy_mode(self, mode: int) -> None:
         _check(self.lib.hisparse_set_copy_mode(self.h, mode), "hisparse_set_copy_mode")
 
@@ -421,6 +479,158 @@ class HiSparse:
                                             t2s.ctypes.data, lru.ctypes.data, ticks.ctypes.data,
                                             _stream(stream)), "hisparse_read_state")
         return s2t, lu, t2s, lru, ticks
+
+
+# -- 4-bit rows (include/hisparse_rows4.h) ----------------------------------
+
+def _dtype16(x, what: str) -> int:
+    d = str(x.dtype)
+    if d == "torch.bfloat16":
+        return BF16
+    if d == "torch.float16":
+        return F16
+    raise ValueError(f"{what} must be bfloat16 or float16, not {d}")
+
+
+def _rows_of(x, what: str, dtype: str, n: int) -> None:
+    """x is [n][...] of dtype with contiguous rows."""
+    if str(x.dtype) != dtype or x.dim() != 2 or x.shape[0] != n or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{what} must be {dtype} [{n}][...] with contiguous rows")
+
+
+def _row_stride(x) -> int:
+    """Elements from row to row (a single row has no stride to go by)."""
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def _ints(x, what: str, shape) -> None:
+    """x is None or a contiguous int32 tensor of this shape."""
+    if x is not None and (str(x.dtype) != "torch.int32" or tuple(x.shape) != shape
+                          or not x.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {shape}")
+
+
+def _packed(rows, what: str, dims: int):
+    if (str(rows.dtype) != "torch.uint8" or rows.dim() != dims or rows.shape[-1] != ROW4_BYTES
+            or rows.stride(-1) != 1):
+        raise ValueError(f"{what} must be uint8 [...][{ROW4_BYTES}] with contiguous rows")
+
+
+def _pack_args(values, rows):
+    dt = _dtype16(values, "values")
+    if values.dim() != 2 or values.shape[1] != ROW4_VALUES or values.stride(1) != 1:
+        raise ValueError(f"values must be [n][{ROW4_VALUES}] with contiguous rows")
+    _packed(rows, "rows", 2)
+    n = values.shape[0]
+    if rows.shape[0] != n:
+        raise ValueError("values and rows differ in length")
+    return dt, n, _row_stride(values), _row_stride(rows)
+
+
+def pack_rows(values, rows, stream=None) -> None:
+    """rows (uint8 [n][416], device or pinned) <- values (bf16 or f16
+    [n][576]: 512 latent and 64 rope values) in 4 bits."""
+    dt, n, vs, rs = _pack_args(values, rows)
+    _check(load_library().hisparse_pack_rows(_addr(values), vs, dt, n, _addr(rows), rs,
+                                             _stream(stream)), "hisparse_pack_rows")
+
+
+def unpack_rows(rows, values, stream=None) -> None:
+    """values (bf16 or f16 [n][576]) <- what rows (uint8 [n][416]) stand for."""
+    dt, n, vs, rs = _pack_args(values, rows)
+    _check(load_library().hisparse_unpack_rows(_addr(rows), rs, n, _addr(values), vs, dt,
+                                               _stream(stream)), "hisparse_unpack_rows")
+
+
+def attend_workspace_bytes(num_requests: int, num_heads: int, top_k: int,
+                           weights: bool = False) -> int:
+    """Bytes of workspace that attend() needs for these sizes."""
+    n = ctypes.c_int64()
+    _check(load_library().hisparse_attend_workspace(num_requests, num_heads, top_k,
+                                                    1 if weights else 0, ctypes.byref(n)),
+           "hisparse_attend_workspace")
+    return n.value
+
+
+def attend(q, rows, slot_ids, out, scale: float, lse=None, positions=None, weights=None,
+           resident_rows=None, status=None, workspace=None, stream=None) -> None:
+    """hisparse_attend: one step's sparse attention over 4-bit rows.
+
+    q [R][H][576] and out [R][H][512] in bf16 or f16; rows uint8 [R][D][416];
+    slot_ids int32 [R][k] as swap_in writes them; lse float32 [R][H] or None;
+    weights float32 [R][tokens] (accumulated into at positions, int32 [R][k])
+    or None; resident_rows uint8 [n][416] for flagged ids; status int32 [R]
+    or None; workspace a uint8 tensor of attend_workspace_bytes (None:
+    allocated for this call)."""
+    _packed(rows, "rows", 3)
+    R, D = rows.shape[0], rows.shape[1]
+    _attend(q, rows.data_ptr(), rows.stride(1) if D > 1 else ROW4_BYTES,
+            rows.stride(0) if R > 1 else 0, R, D, slot_ids, out, scale, lse, positions, weights,
+            resident_rows, status, workspace, stream)
+
+
+def _attend(q, rows, row_stride, request_stride, R, D, slot_ids, out, scale, lse, positions,
+            weights, resident_rows, status, workspace, stream) -> None:
+    dt = _dtype16(q, "q")
+    if q.dim() != 3 or q.shape[0] != R or q.shape[2] != ROW4_VALUES or q.stride(2) != 1:
+        raise ValueError(f"q must be [{R}][H][{ROW4_VALUES}] with contiguous heads")
+    H = q.shape[1]
+    if (out.dtype != q.dtype or tuple(out.shape) != (R, H, ROW4_LATENT) or out.stride(2) != 1):
+        raise ValueError(f"out must be [{R}][{H}][{ROW4_LATENT}] of q's type with contiguous heads")
+    _rows_of(slot_ids, "slot_ids", "torch.int32", R)
+    k = slot_ids.shape[1]
+    if lse is not None and (str(lse.dtype) != "torch.float32" or tuple(lse.shape) != (R, H)
+                            or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous float32 tensor of shape ({R}, {H})")
+    a = AttendArgs()
+    if weights is not None:
+        _rows_of(weights, "weights", "torch.float32", R)
+        if positions is None:
+            raise ValueError("weights need positions")
+        _rows_of(positions, "positions", "torch.int32", R)
+        if positions.shape[1] != k:
+            raise ValueError("positions and slot_ids differ in length")
+        a.weights, a.positions = weights.data_ptr(), positions.data_ptr()
+        a.weights_stride, a.weights_tokens = _row_stride(weights), weights.shape[1]
+        a.positions_stride = _row_stride(positions)
+    if resident_rows is not None:
+        _packed(resident_rows, "resident_rows", 2)
+        a.resident_rows = resident_rows.data_ptr()
+        a.resident_count = resident_rows.shape[0]
+        a.resident_stride = resident_rows.stride(0) if a.resident_count > 1 else ROW4_BYTES
+    if workspace is None:
+        import torch
+        workspace = torch.empty(attend_workspace_bytes(R, H, k, weights is not None),
+                                dtype=torch.uint8, device=q.device)
+    a.num_requests, a.num_heads, a.top_k, a.dtype = R, H, k, dt
+    a.q, a.q_request_stride, a.q_head_stride = q.data_ptr(), q.stride(0), q.stride(1)
+    a.rows, a.row_stride, a.request_stride, a.rows_per_request = rows, row_stride, request_stride, D
+    a.scale = scale
+    a.slot_ids, a.ids_stride = slot_ids.data_ptr(), _row_stride(slot_ids)
+    a.out, a.out_request_stride, a.out_head_stride = out.data_ptr(), out.stride(0), out.stride(1)
+    a.lse, a.status = _addr(lse), _addr(status)
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(load_library().hisparse_attend(ctypes.byref(a), _stream(stream)), "hisparse_attend")
+
+
+def evict_select(weights, slot2tok, seq_lens, out_slots, out_counts, keep_recent: int = 0,
+                 want=None, stream=None) -> None:
+    """hisparse_evict_select: the slots of the least accumulated weight
+    (out_slots int32 [R][n], ascending, -1 behind them; out_counts int32 [R])
+    of slot2tok int32 [R][D]; weights float32 [R][tokens]."""
+    R, D = slot2tok.shape
+    _rows_of(weights, "weights", "torch.float32", R)
+    _ints(slot2tok, "slot2tok", (R, D))
+    _ints(seq_lens, "seq_lens", (R,))
+    n = out_slots.shape[1]
+    _ints(out_slots, "out_slots", (R, n))
+    _ints(out_counts, "out_counts", (R,))
+    _ints(want, "want", (R,))
+    _check(load_library().hisparse_evict_select(R, D, weights.data_ptr(),
+                                                _row_stride(weights), weights.shape[1], slot2tok.data_ptr(), seq_lens.data_ptr(),
+                                                keep_recent, n, _addr(want), out_slots.data_ptr(),
+                                                out_counts.data_ptr(), _stream(stream)),
+           "hisparse_evict_select")
 
 
 # -- measurement kernels (include/hisparse_measure.h) -----------------------
