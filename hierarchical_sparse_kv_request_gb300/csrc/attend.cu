@@ -16,16 +16,19 @@
 // enter the second product as f16 (relative step 2^-11).
 //
 // One CTA takes up to 64 heads of one request over a range of its rows, 64
-// rows a tile, two tiles in flight:
-//   warps 4-11   fetch the tile's packed rows into registers one tile ahead,
+// rows a tile, three tiles in flight:
+//   warps 4-19   fetch a tile's packed rows into registers one tile ahead,
 //                decode them to f16 in shared memory (128-byte swizzle);
-//   warp 12      one thread issues the MMAs (M = 64 heads): S = Q K^T into
-//                tensor memory, then O += P V, the same tile read as V with
-//                the rows as the k dimension;
+//   warp 20      issues the MMAs (M = 64 heads): S = Q K^T, then O += P V of
+//                the tile before, its rows now the k dimension;
 //   warps 0-3    softmax: read S, move the reference, write P as f16 over the
 //                tile's rope part (S no longer needs it), keep l.
-// O takes 256 columns of tensor memory: M = 64 uses 16 of each warp's 32
-// lanes, so values 0-255 sit in the lower and 256-511 in the upper 16.
+// M = 64 uses 16 of the 32 lanes of each warp's part of tensor memory: O fills
+// the upper 16 (512 columns), S (two tiles) and the queries the lower.  With
+// the queries there, an MMA of the first product reads 2 KB of shared memory
+// in its 32 cycles instead of 4 KB, which would take all of its bandwidth and
+// leave the decoding warps none (measured: 45.9 -> XX us for 32 requests, 128
+// heads, 2,048 rows).
 //
 // The rows of a request are split over several CTAs when there are few
 // (request, head tile) pairs; a second launch joins the parts.  With weights,
@@ -42,22 +45,24 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int TILE = 64;          // rows a tile
 constexpr int HEADS = 64;         // heads a CTA
-constexpr int AT_NT = 416;        // 4 softmax, 8 decode warps and the MMA warp
-constexpr int SOFTMAX_WARPS = 4, DECODE_WARPS = 8, MMA_WARP = 12;
+constexpr int SOFTMAX_WARPS = 4, DECODE_WARPS = 16, MMA_WARP = SOFTMAX_WARPS + DECODE_WARPS;
+constexpr int AT_NT = (MMA_WARP + 1) * 32;
 constexpr uint32_t BLOCK = 64 * 128;             // 64 values of 64 rows, swizzled
 constexpr uint32_t OPERAND = 9 * BLOCK;          // 576 values of 64 rows
 constexpr uint32_t ROPE_BLOCK = 8 * BLOCK;
-constexpr uint32_t TMEM_S = 256;                 // column of S; 64 columns a stage
+constexpr int STAGES = 3;                        // tiles in shared memory
+constexpr uint32_t TMEM_UPPER = 16u << 16;       // O: the upper lanes, column = value
+constexpr uint32_t TMEM_Q = 2 * TILE;            // lower lanes: S of two tiles, then the queries
 constexpr float kMoveAbove = 8.0f;               // base-2 growth that moves the reference
 
 struct AttendSmem {
-    uint64_t full[2], empty[2], scored[2], weighed[2], drained;
+    uint64_t full[STAGES], empty[STAGES], scored[2], weighed[2], queries, drained;
     uint32_t tmem;
     int gave_up;
-    uint64_t valid[2];        // bit i: row i of the stage's tile is named
+    __align__(16) uint8_t valid[STAGES][16];   // bit b of byte n: row 4 n + b of the stage's tile is named
     float factor[HEADS];      // scale * log2(e) * the query's power of two
 };
-constexpr size_t AT_SMEM = 3 * OPERAND + sizeof(AttendSmem);
+constexpr size_t AT_SMEM = STAGES * OPERAND + sizeof(AttendSmem);
 
 // Row that an id names, or null (nothing, or an id out of range, whose status
 // bit is set in *bad).
@@ -81,7 +86,7 @@ __device__ __forceinline__ const uint8_t *row_of(const AttendLaunch &a, int r, i
 __device__ __forceinline__ uint4 ld_row_v4(const void *p)
 {
     uint4 v;
-    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
@@ -90,13 +95,20 @@ __device__ __forceinline__ uint4 ld_row_v4(const void *p)
 __device__ __forceinline__ uint32_t ld_row_u16(const void *p)
 {
     uint16_t v;
-    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p));
     return v;
 }
 
 __device__ __forceinline__ void st_smem_v4(uint32_t at, uint4 v)
 {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_smem_v4(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ void st_smem_u32(uint32_t at, uint32_t v)
@@ -126,46 +138,61 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, __half2 scale)
     return make_uint4(pair(w << 12, w << 9), pair(w << 8, w << 5), pair(w << 4, w << 1), pair(w, w >> 3));
 }
 
-// A thread's share of a packed row: a quarter of its 16-byte chunks.
+// A decode warp's four rows, as its threads hold them: half a warp takes the
+// 256 bytes of codes of one row (chunk c = lane % 16; two loads for four
+// rows), a quarter the rope part of one, so every load is whole sectors of a
+// few rows.
 struct RowPart {
-    uint4 codes[4], rope[2];
-    uint32_t scales[4];
+    uint4 codes[2], rope;
+    uint32_t scales[2];
 };
 
-__device__ __forceinline__ void fetch(RowPart &p, const uint8_t *row, int quarter)
+// row: this lane's rope row (lane / 8 of the warp's four), or null.
+__device__ __forceinline__ void fetch(RowPart &p, const uint8_t *row, int lane)
 {
-    if (row) {
+    const int c = lane & 15;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p.codes[j] = ld_row_v4(row + (j * 4 + quarter) * 16);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) p.scales[j] = ld_row_u16(row + kScaleAt + (j * 4 + quarter) * 2);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) p.rope[j] = ld_row_v4(row + kRopeAt + (j * 4 + quarter) * 16);
-    } else {     // zeros: nothing of it reaches a result
-#pragma unroll
-        for (int j = 0; j < 4; ++j) p.codes[j] = make_uint4(0, 0, 0, 0), p.scales[j] = 0;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) p.rope[j] = make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < 2; ++j) {
+        const uint8_t *src = reinterpret_cast<const uint8_t *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), (2 * j + (lane >> 4)) * 8));
+        p.codes[j] = make_uint4(0, 0, 0, 0);     // of no row: nothing of it reaches a result
+        p.scales[j] = 0;
+        if (src) {
+            p.codes[j] = ld_row_v4(src + c * 16);
+            p.scales[j] = ld_row_u16(src + kScaleAt + c * 2);
+        }
     }
+    p.rope = make_uint4(0, 0, 0, 0);
+    if (row) p.rope = ld_row_v4(row + kRopeAt + (lane & 7) * 16);
 }
 
-__device__ __forceinline__ void decode(const RowPart &p, uint32_t stage, int i, int quarter)
+// i0: the warp's first row in the tile.  A thread's four words go to four
+// units of one row and block; lanes start at different words, so that the 8
+// lanes that store at once go to 8 different units.
+__device__ __forceinline__ void decode(const RowPart &p, uint32_t stage, int i0, int lane)
 {
+    const int c = lane & 15, turn = (c >> 1) & 3;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
+        const int i = i0 + 2 * j + (lane >> 4);
         uint32_t s2;
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"((uint16_t)p.scales[j]));
-        const __half2 s = __hmul2(*reinterpret_cast<__half2 *>(&s2), __half2half2(__ushort_as_half(0x5800)));  // 2^7
+        const __half2 s = __hmul2(*reinterpret_cast<__half2 *>(&s2), __half2half2(__ushort_as_half(0x5800)));   // 2^7
         const __half2 lo = __low2half2(s), hi = __high2half2(s);
-        const uint32_t block = stage + (2 * j + (quarter >> 1)) * BLOCK;
-        const int u = (quarter & 1) * 4;
-        st_smem_v4(swizzled(block, i, u), decode8(p.codes[j].x, lo));
-        st_smem_v4(swizzled(block, i, u + 1), decode8(p.codes[j].y, lo));
-        st_smem_v4(swizzled(block, i, u + 2), decode8(p.codes[j].z, hi));
-        st_smem_v4(swizzled(block, i, u + 3), decode8(p.codes[j].w, hi));
+        const uint4 v = p.codes[j];
+        uint4 a = (turn & 1) ? make_uint4(v.y, v.z, v.w, v.x) : v;
+        a = (turn & 2) ? make_uint4(a.z, a.w, a.x, a.y) : a;       // word (w + turn) % 4 in place w
+        const uint32_t row = stage + (c >> 1) * BLOCK + i * 128;
+        auto put = [&](uint32_t word, int w) {
+            const int n = (w + turn) & 3;
+            st_smem_v4(row + ((((c & 1) * 4 + n) ^ (i & 7)) << 4), decode8(word, n & 2 ? hi : lo));
+        };
+        put(a.x, 0);
+        put(a.y, 1);
+        put(a.z, 2);
+        put(a.w, 3);
     }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) st_smem_v4(swizzled(stage + ROPE_BLOCK, i, j * 4 + quarter), p.rope[j]);
+    st_smem_v4(swizzled(stage + ROPE_BLOCK, i0 + (lane >> 3), lane & 7), p.rope);
 }
 
 template <int DT>
@@ -189,57 +216,61 @@ __device__ __forceinline__ uint32_t floats_to_pair(float x, float y)
 // A power of two as float
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// Query rows [h0, h0 + 64) into shared memory, by whole warps; rows past H
-// are zero.
+// Query rows [h0, h0 + 64) into shared memory, by whole warps (QROWS rows
+// each, all their loads in flight); rows past H are zero.
+constexpr int QROWS = (HEADS + AT_NT / 32 - 1) / (AT_NT / 32);
+
 template <int DT>
 __device__ __forceinline__ void stage_queries(const AttendLaunch &a, int r, int h0, uint32_t dst, float *factor,
                                               int warp, int lane)
 {
-    for (int i = warp; i < HEADS; i += AT_NT / 32) {
-        const int h = h0 + i;
-        uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, rope = make_uint4(0, 0, 0, 0);
-        if (h < a.H) {
+    uint4 v[QROWS][2], rope[QROWS];
+#pragma unroll
+    for (int n = 0; n < QROWS; ++n) {
+        const int i = warp + n * (AT_NT / 32), h = h0 + i;
+        v[n][0] = v[n][1] = rope[n] = make_uint4(0, 0, 0, 0);
+        if (i < HEADS && h < a.H) {
             const uint8_t *q = a.q + (int64_t)r * a.q_rs + (int64_t)h * a.q_hs;
-            v[0] = ld_dev_v4(q + lane * 16);
-            v[1] = ld_dev_v4(q + 512 + lane * 16);
-            if (lane < 8) rope = ld_dev_v4(q + kLatent * 2 + lane * 16);
+            v[n][0] = ld_row_v4(q + lane * 16);
+            v[n][1] = ld_row_v4(q + 512 + lane * 16);
+            if (lane < 8) rope[n] = ld_row_v4(q + kLatent * 2 + lane * 16);
         }
+    }
+#pragma unroll
+    for (int n = 0; n < QROWS; ++n) {
+        const int i = warp + n * (AT_NT / 32);
+        if (i >= HEADS) break;
         uint32_t m = 0;   // magnitudes compare as integers
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
-            m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[half].x & 0x7FFF7FFFu, v[half].y & 0x7FFF7FFFu),
-                                     __vmaxu2(v[half].z & 0x7FFF7FFFu, v[half].w & 0x7FFF7FFFu)));
-        m = __vmaxu2(m, __vmaxu2(__vmaxu2(rope.x & 0x7FFF7FFFu, rope.y & 0x7FFF7FFFu),
-                                 __vmaxu2(rope.z & 0x7FFF7FFFu, rope.w & 0x7FFF7FFFu)));
-        uint32_t top = max(m >> 16, m & 0xFFFFu);
-        top = __reduce_max_sync(0xffffffffu, top);
+        for (int part = 0; part < 3; ++part) {
+            const uint4 x = part < 2 ? v[n][part] : rope[n];
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                     __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+        }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xFFFFu));
         // exponent of the largest value; 0 for none and for infinities and
         // NaN, which pass through as they are
         int e = (int)(__float_as_uint(pair_to_float<DT>(top).x) >> 23) - 127;
         if (top == 0 || e == 128) e = 0;
         e = max(e, -119);
-        const float up = exp2i(7 - e), up_rope = exp2i(-e);
+        const float up = exp2i(-e), u7 = exp2i(7 - e);    // the latter: decode8's 2^7
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const float2 x0 = pair_to_float<DT>(v[half].x), x1 = pair_to_float<DT>(v[half].y);
-            const float2 x2 = pair_to_float<DT>(v[half].z), x3 = pair_to_float<DT>(v[half].w);
+            const float2 x0 = pair_to_float<DT>(v[n][half].x), x1 = pair_to_float<DT>(v[n][half].y);
+            const float2 x2 = pair_to_float<DT>(v[n][half].z), x3 = pair_to_float<DT>(v[n][half].w);
             // the order of decode8
-            const uint4 h = make_uint4(floats_to_pair<kF16>(x0.x * up, x2.x * up), floats_to_pair<kF16>(x0.y * up, x2.y * up),
-                                       floats_to_pair<kF16>(x1.x * up, x3.x * up), floats_to_pair<kF16>(x1.y * up, x3.y * up));
+            const uint4 h = make_uint4(floats_to_pair<kF16>(x0.x * u7, x2.x * u7), floats_to_pair<kF16>(x0.y * u7, x2.y * u7),
+                                       floats_to_pair<kF16>(x1.x * u7, x3.x * u7), floats_to_pair<kF16>(x1.y * u7, x3.y * u7));
             const int unit = half * 32 + lane;
             st_smem_v4(swizzled(dst + (unit >> 3) * BLOCK, i, unit & 7), h);
         }
         if (lane < 8) {
-            uint4 h;
-            float2 x = pair_to_float<DT>(rope.x);
-            h.x = floats_to_pair<DT>(x.x * up_rope, x.y * up_rope);
-            x = pair_to_float<DT>(rope.y);
-            h.y = floats_to_pair<DT>(x.x * up_rope, x.y * up_rope);
-            x = pair_to_float<DT>(rope.z);
-            h.z = floats_to_pair<DT>(x.x * up_rope, x.y * up_rope);
-            x = pair_to_float<DT>(rope.w);
-            h.w = floats_to_pair<DT>(x.x * up_rope, x.y * up_rope);
-            st_smem_v4(swizzled(dst + ROPE_BLOCK, i, lane), h);
+            auto scaled = [&](uint32_t w) {
+                const float2 x = pair_to_float<DT>(w);
+                return floats_to_pair<DT>(x.x * up, x.y * up);
+            };
+            st_smem_v4(swizzled(dst + ROPE_BLOCK, i, lane),
+                       make_uint4(scaled(rope[n].x), scaled(rope[n].y), scaled(rope[n].z), scaled(rope[n].w)));
         }
         if (lane == 0) factor[i] = a.scale * kLog2e * exp2i(e);
     }
@@ -254,22 +285,16 @@ struct AttendParts {
     float *scores;    // [R][H][k] base-2 scores, for the weights
 };
 
-// The warp's 16 heads' value, kept by the threads of a 16x256b fragment
-// (rows lane / 4 and lane / 4 + 8), for the head of lane % 16.
-__device__ __forceinline__ float by_lane(float a, float b, int lane)
-{
-    const float x = __shfl_sync(0xffffffffu, a, (lane & 7) * 4), y = __shfl_sync(0xffffffffu, b, (lane & 7) * 4);
-    return (lane & 8) ? y : x;
-}
-
 template <int DT>
 __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant__ AttendLaunch a,
                                                           const __grid_constant__ AttendParts w)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    AttendSmem &sm = *reinterpret_cast<AttendSmem *>(smem + 3 * OPERAND);
-    const uint32_t q_at = smem_u32(smem);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // this call's own next launch may be placed now; it waits for this grid
+    if (w.splits > 1 || a.weights) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    AttendSmem &sm = *reinterpret_cast<AttendSmem *>(smem + STAGES * OPERAND);
+    const uint32_t stages = smem_u32(smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int head_tiles = (a.H + HEADS - 1) / HEADS;
     const int ht = blockIdx.x % head_tiles;
     const int split = (blockIdx.x / head_tiles) % w.splits;
@@ -279,105 +304,143 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
     const int rows = min(a.k - k0, w.tiles_per_split * TILE);
     const int tiles = (rows + TILE - 1) / TILE;
 
+    const bool decodes = warp >= SOFTMAX_WARPS && warp < MMA_WARP;
+    const int dw = warp - SOFTMAX_WARPS;      // its rows of a tile: 4 dw to 4 dw + 3
+    const int32_t *ids = a.ids + (int64_t)r * a.ids_stride + k0;
+    auto id_at = [&](int t) {
+        const int n = t * TILE + dw * 4 + (lane >> 3);
+        return n < rows ? ids[n] : -1;
+    };
+    RowPart next;
+    const uint8_t *row = nullptr;
+    int32_t id = -1;
+    int bad = 0;
+    if (decodes) {       // the first tile's rows are on their way while the queries are staged
+        row = row_of(a, r, id_at(0), &bad);
+        id = id_at(1);
+        fetch(next, row, lane);
+    }
+    const uint32_t q_at = stages + (STAGES - 1) * OPERAND;   // the queries, until they are in tensor memory
     if (tid == 0) {
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&sm.full[s]), DECODE_WARPS);
             mbar_init(smem_u32(&sm.empty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&sm.scored[s]), 1);
             mbar_init(smem_u32(&sm.weighed[s]), SOFTMAX_WARPS);
         }
+        mbar_init(smem_u32(&sm.queries), SOFTMAX_WARPS);
         mbar_init(smem_u32(&sm.drained), 1);
         sm.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == MMA_WARP) tmem_alloc_all(smem_u32(&sm.tmem));
     stage_queries<DT>(a, r, h0, q_at, sm.factor, warp, lane);
-    fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
     volatile int *gave_up = &sm.gave_up;
+    auto all = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
 
-    if (warp >= SOFTMAX_WARPS && warp < MMA_WARP) {
+    if (decodes) {
         // ---- fetch and decode -----------------------------------------------
-        const int dw = warp - SOFTMAX_WARPS, i = dw * 8 + (lane & 7), quarter = lane >> 3;
-        const int32_t *ids = a.ids + (int64_t)r * a.ids_stride + k0;
-        auto id_at = [&](int t) { return t * TILE + i < rows ? ids[t * TILE + i] : -1; };
-        RowPart next;
-        int bad = 0;
-        const uint8_t *row = row_of(a, r, id_at(0), &bad);
-        fetch(next, row, quarter);
-        int32_t id = id_at(1);
+        int s = 0, phase = 1;     // the phase whose end frees stage s
+#pragma unroll 2
         for (int t = 0; t < tiles; ++t) {
-            const RowPart part = next;
-            const uint32_t named = __ballot_sync(0xffffffffu, row != nullptr) & 0xFFu;
+            const RowPart now = next;
+            const uint32_t named = __ballot_sync(0xffffffffu, row != nullptr);    // lanes 0, 8, 16, 24
             row = row_of(a, r, id, &bad);
-            fetch(next, row, quarter);
+            fetch(next, row, lane);
             id = id_at(t + 2);
-            const int s = t & 1;
-            const bool free = t < 2 || mbar_wait(smem_u32(&sm.empty[s]), ((t >> 1) - 1) & 1, gave_up);
-            if (!__all_sync(0xffffffffu, free)) break;
-            decode(part, q_at + (1 + s) * OPERAND, i, quarter);
-            if (lane == 0) reinterpret_cast<uint8_t *>(&sm.valid[s])[dw] = (uint8_t)named;
+            const bool free = t < STAGES - 1    ? true
+                              : t == STAGES - 1 ? mbar_wait(smem_u32(&sm.queries), 0, gave_up)
+                                                : mbar_wait(smem_u32(&sm.empty[s]), phase, gave_up);
+            if (!all(free)) break;
+            decode(now, stages + s * OPERAND, dw * 4, lane);
+            if (lane == 0)
+                sm.valid[s][dw] = (uint8_t)((named & 1u) | (named >> 7 & 2u) | (named >> 14 & 4u) | (named >> 21 & 8u));
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.full[s]));
+            if (++s == STAGES) s = 0, phase ^= 1;
         }
         if (bad && a.status) atomicOr(a.status + r, bad);
     } else if (warp == MMA_WARP) {
         // ---- MMA issue -----------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t qk = mma_desc(HEADS, TILE, false, false);
-            constexpr uint32_t qk_rope = mma_desc(HEADS, TILE, DT == kBf16, false);
-            constexpr uint32_t pv = mma_desc(HEADS, 256, false, true);
-            const uint64_t q_desc = smem_desc(q_at, 16, 1024);
-            bool ok = true;
-            for (int t0 = 0; ok && t0 < tiles; t0 += 2) {
-                const int n = min(2, tiles - t0);
-                for (int s = 0; ok && s < n; ++s) {       // S = Q K^T
-                    ok = mbar_wait(smem_u32(&sm.full[s]), (t0 >> 1) & 1, gave_up);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t k_desc = smem_desc(q_at + (1 + s) * OPERAND, 16, 1024);
-                    const uint32_t d = tmem + TMEM_S + s * TILE;
+        constexpr uint32_t qk = mma_desc(HEADS, TILE, false, false);
+        constexpr uint32_t qk_rope = mma_desc(HEADS, TILE, DT == kBf16, false);
+        constexpr uint32_t pv = mma_desc(HEADS, 256, false, true);
+        bool ok = all(mbar_wait(smem_u32(&sm.queries), 0, gave_up));
+        int s = 0, s_pv = 0, phase = 0;
+        for (int t = 0; ok && t <= tiles; ++t) {
+            if (t < tiles) {            // S(t) = Q K^T
+                if (!(ok = all(mbar_wait(smem_u32(&sm.full[s]), phase, gave_up)))) break;
+                tc_fence_after();
+                const uint64_t k_desc = smem_desc(stages + s * OPERAND, 16, 1024);
+                const uint32_t d = tmem + (t & 1) * TILE;
+                if (elect_one()) {
 #pragma unroll
                     for (int b = 0; b < 9; ++b)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {     // 16 values a step: 32 bytes
-                            const uint64_t off = (b * BLOCK + x * 32) >> 4;
-                            mma_f16(d, q_desc + off, k_desc + off, b < 8 ? qk : qk_rope, b + x > 0);
-                        }
-                    mma_commit(smem_u32(&sm.scored[s]));
+                        for (int x = 0; x < 4; ++x)      // 16 values a step: 32 bytes, 8 columns
+                            mma_f16_ts(d, tmem + TMEM_Q + (b * 4 + x) * 8, k_desc + ((b * BLOCK + x * 32) >> 4),
+                                       b < 8 ? qk : qk_rope, b + x > 0);
+                    mma_commit(smem_u32(&sm.scored[t & 1]));
                 }
-                for (int s = 0; ok && s < n; ++s) {       // O += P V
-                    ok = mbar_wait(smem_u32(&sm.weighed[s]), (t0 >> 1) & 1, gave_up);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t stage = q_at + (1 + s) * OPERAND;
-                    const uint64_t p_desc = smem_desc(stage + ROPE_BLOCK, 16, 1024);
+                __syncwarp();
+                if (++s == STAGES) s = 0, phase ^= 1;
+            }
+            if (t > 0) {                // O += P(t - 1) V
+                if (!(ok = all(mbar_wait(smem_u32(&sm.weighed[(t - 1) & 1]), ((t - 1) >> 1) & 1, gave_up)))) break;
+                tc_fence_after();
+                const uint32_t stage = stages + s_pv * OPERAND;
+                const uint64_t p_desc = smem_desc(stage + ROPE_BLOCK, 16, 1024);
+                if (elect_one()) {
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const uint64_t v_desc = smem_desc(stage + half * 4 * BLOCK, BLOCK, 1024);
 #pragma unroll
                         for (int x = 0; x < 4; ++x)       // 16 rows a step
-                            mma_f16(tmem + (half ? 16u << 16 : 0u), p_desc + ((x * 32) >> 4),
-                                    v_desc + ((x * 2048) >> 4), pv, t0 + s + x > 0);
+                            mma_f16(tmem + TMEM_UPPER + half * 256, p_desc + ((x * 32) >> 4),
+                                    v_desc + ((x * 2048) >> 4), pv, t - 1 + x > 0);
                     }
-                    mma_commit(smem_u32(&sm.empty[s]));
+                    mma_commit(smem_u32(&sm.empty[s_pv]));
                 }
+                __syncwarp();
+                if (++s_pv == STAGES) s_pv = 0;
             }
-            if (!ok) {     // let what was issued end before the CTA goes
-                mma_commit(smem_u32(&sm.drained));
-                const uint32_t bar = smem_u32(&sm.drained);
-                for (int i = 0; i < (1 << 20) && !mbar_try(bar, 0); ++i) {}
-            }
+        }
+        if (!ok) {     // let what was issued end before the CTA goes
+            if (elect_one()) mma_commit(smem_u32(&sm.drained));
+            const uint32_t bar = smem_u32(&sm.drained);
+            for (int i = 0; i < (1 << 20) && !mbar_try(bar, 0); ++i) {}
         }
         __syncwarp();
     } else {
         // ---- softmax --------------------------------------------------------------
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        {   // the queries of this warp's 16 heads: 16 columns (32 values) at a time
+            const int i = warp * 16 + (lane & 15);
+#pragma unroll 2
+            for (int c = 0; c < 18; ++c) {
+                uint32_t v[16];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint4 x = ld_smem_v4(swizzled(q_at + (c >> 1) * BLOCK, i, (c & 1) * 4 + u));
+                    v[4 * u] = x.x, v[4 * u + 1] = x.y, v[4 * u + 2] = x.z, v[4 * u + 3] = x.w;
+                }
+                // (the upper lanes get them too: O starts there later)
+                tmem_st_32x16(lanes + TMEM_Q + c * 16, v);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.queries));
+        }
         const int g = lane >> 2, c2 = (lane & 3) * 2;     // fragment row and column
+        const int vs = (c2 >> 2) * 8 + (c2 & 3);          // its bit in valid's 16-bit pieces
         const int i0 = warp * 16 + g, i1 = i0 + 8;
         const float f0 = sm.factor[i0], f1 = sm.factor[i1];
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
@@ -388,26 +451,26 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
             if (h0 + i1 < a.H) sc1 = w.scores + at + (int64_t)i1 * a.k;
         }
         bool ok = true;
+        int s = 0, phase = 0, s_before = 0, phase_before = 0;     // of tile t, of tile t - 1
         for (int t = 0; t < tiles; ++t) {
-            const int s = t & 1;
-            const uint32_t parity = (t >> 1) & 1;
-            ok = mbar_wait(smem_u32(&sm.full[s]), parity, gave_up) &&
-                 mbar_wait(smem_u32(&sm.scored[s]), parity, gave_up);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            ok = all(mbar_wait(smem_u32(&sm.full[s]), phase, gave_up) &&
+                     mbar_wait(smem_u32(&sm.scored[t & 1]), (t >> 1) & 1, gave_up));
+            if (!ok) break;
             tc_fence_after();
             uint32_t v[32];
-            tmem_ld_16x64(lanes + TMEM_S + s * TILE, v);
-            const uint64_t named = sm.valid[s] >> c2;
+            tmem_ld_16x64(lanes + (t & 1) * TILE, v);
+            const uint4 valid = *reinterpret_cast<const uint4 *>(sm.valid[s]);
+            const uint32_t named[4] = {valid.x >> vs, valid.y >> vs, valid.z >> vs, valid.w >> vs};
             tmem_wait_ld();
-            float x[32];
+            float (&x)[32] = reinterpret_cast<float (&)[32]>(v);
             float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const bool on = (named >> (8 * j + b)) & 1u;
-                    x[4 * j + b] = on ? __uint_as_float(v[4 * j + b]) * f0 : -INFINITY;
-                    x[4 * j + 2 + b] = on ? __uint_as_float(v[4 * j + 2 + b]) * f1 : -INFINITY;
+                    const bool on = (named[j >> 1] >> ((j & 1) * 16 + b)) & 1u;
+                    x[4 * j + b] = on ? x[4 * j + b] * f0 : -INFINITY;
+                    x[4 * j + 2 + b] = on ? x[4 * j + 2 + b] * f1 : -INFINITY;
                     top0 = fmaxf(top0, x[4 * j + b]);
                     top1 = fmaxf(top1, x[4 * j + 2 + b]);
                 }
@@ -435,23 +498,24 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
                 l0 *= d0;
                 l1 *= d1;
                 if (t > 0) {      // O so far, once the product before this one is done
-                    const float d = by_lane(d0, d1, lane);
-                    ok = mbar_wait(smem_u32(&sm.empty[s ^ 1]), ((t - 1) >> 1) & 1, gave_up);
-                    if (!__all_sync(0xffffffffu, ok)) break;
+                    ok = all(mbar_wait(smem_u32(&sm.empty[s_before]), phase_before, gave_up));
+                    if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < 256; c += 32) {
-                        tmem_ld_32x32(lanes + c, v);
+                    for (int c = 0; c < kLatent; c += 64) {
+                        uint32_t o[32];
+                        tmem_ld_16x64(lanes + TMEM_UPPER + c, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * d);
-                        tmem_st_32x32(lanes + c, v);
+                        for (int j = 0; j < 32; ++j)
+                            o[j] = __float_as_uint(__uint_as_float(o[j]) * (j & 2 ? d1 : d0));
+                        tmem_st_16x64(lanes + TMEM_UPPER + c, o);
                     }
                     tmem_wait_st();
                 }
             }
             const float r0 = m0 == -INFINITY ? 0.0f : m0, r1 = m1 == -INFINITY ? 0.0f : m1;
-            const uint32_t p_at = q_at + (1 + s) * OPERAND + ROPE_BLOCK;
+            const uint32_t p_at = stages + s * OPERAND + ROPE_BLOCK;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float p00 = exp2f(x[4 * j] - r0), p01 = exp2f(x[4 * j + 1] - r0);
@@ -464,57 +528,62 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
             fence_async_smem();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.weighed[s]));
+            if (lane == 0) mbar_arrive(smem_u32(&sm.weighed[t & 1]));
+            s_before = s, phase_before = phase;
+            if (++s == STAGES) s = 0, phase ^= 1;
         }
         // the last product, then O / l or this part's O, m and l
-        if (__all_sync(0xffffffffu, ok))
-            ok = mbar_wait(smem_u32(&sm.empty[(tiles - 1) & 1]), ((tiles - 1) >> 1) & 1, gave_up);
-        if (__all_sync(0xffffffffu, ok)) {
+        if (ok) ok = all(mbar_wait(smem_u32(&sm.empty[s_before]), phase_before, gave_up));
+        if (ok) {
             tc_fence_after();
             l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
             l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
             l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
             l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-            const int h = h0 + warp * 16 + (lane & 15), d0 = (lane >> 4) * 256;
-            const float l = by_lane(l0, l1, lane), m = by_lane(m0, m1, lane);
-            const int64_t rh = (int64_t)r * a.H + h;
-            const bool whole = w.splits == 1;
-            float *part = w.o + ((int64_t)split * a.R * a.H + rh) * kLatent + d0;
-            uint8_t *out = a.out + (int64_t)r * a.out_rs + (int64_t)h * a.out_hs + d0 * 2;
-            const float inv = l == 0.0f ? 0.0f : 128.0f / l;
-            if (lane < 16 && h < a.H) {
+            const bool whole = w.splits == 1, odd = lane & 1;
+            // columns hold values in decode8's order: after an exchange with
+            // its neighbour, this thread holds values d, d + 1 of each eight
+            const int d = (lane & 2) + (odd ? 4 : 0);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int h = h0 + (half ? i1 : i0);
+                const float l = half ? l1 : l0, m = half ? m1 : m0;
+                if ((lane & 3) || h >= a.H) continue;
+                const int64_t rh = (int64_t)r * a.H + h;
                 if (whole) {
                     const float l2 = l == 0.0f ? -INFINITY : m + log2f(l);
                     if (a.lse) a.lse[rh] = l2 * kLn2;
                     if (a.weights) w.lse2[rh] = l2;
                 } else {
-                    float *ml = w.ml + ((int64_t)split * a.R * a.H + rh) * 2;
-                    ml[0] = m;
-                    ml[1] = l;
+                    *reinterpret_cast<float2 *>(w.ml + ((int64_t)split * a.R * a.H + rh) * 2) = make_float2(m, l);
                 }
             }
+            const float inv0 = l0 == 0.0f ? 0.0f : 128.0f / l0, inv1 = l1 == 0.0f ? 0.0f : 128.0f / l1;
+            const bool on0 = h0 + i0 < a.H, on1 = h0 + i1 < a.H;
+            const int64_t rh0 = (int64_t)r * a.H + h0 + i0;
+            float *o0 = w.o + ((int64_t)split * a.R * a.H + rh0) * kLatent + d, *o1 = o0 + 8 * kLatent;
+            uint8_t *out0 = a.out + (int64_t)r * a.out_rs + (int64_t)(h0 + i0) * a.out_hs + d * 2, *out1 = out0 + 8 * a.out_hs;
 #pragma unroll 1
-            for (int c = 0; c < 256; c += 32) {
+            for (int c = 0; c < kLatent; c += 64) {
                 uint32_t v[32];
-                tmem_ld_32x32(lanes + c, v);
+                tmem_ld_16x64(lanes + TMEM_UPPER + c, v);
                 tmem_wait_ld();
-                if (h < a.H) {
 #pragma unroll
-                    for (int u = 0; u < 32; u += 8) {     // back to value order
-                        const float y0 = __uint_as_float(v[u]), y4 = __uint_as_float(v[u + 1]);
-                        const float y1 = __uint_as_float(v[u + 2]), y5 = __uint_as_float(v[u + 3]);
-                        const float y2 = __uint_as_float(v[u + 4]), y6 = __uint_as_float(v[u + 5]);
-                        const float y3 = __uint_as_float(v[u + 6]), y7 = __uint_as_float(v[u + 7]);
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const float x = __uint_as_float(v[4 * j + 2 * half]), y = __uint_as_float(v[4 * j + 2 * half + 1]);
+                        const float got = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
+                        const float lo = odd ? got : x, hi = odd ? y : got;
+                        if (!(half ? on1 : on0)) continue;
                         if (whole) {
-                            st_v4(out + (c + u) * 2,
-                                  make_uint4(floats_to_pair<DT>(y0 * inv, y1 * inv), floats_to_pair<DT>(y2 * inv, y3 * inv),
-                                             floats_to_pair<DT>(y4 * inv, y5 * inv), floats_to_pair<DT>(y6 * inv, y7 * inv)));
+                            const float inv = half ? inv1 : inv0;
+                            *reinterpret_cast<uint32_t *>((half ? out1 : out0) + (c + 8 * j) * 2) =
+                                floats_to_pair<DT>(lo * inv, hi * inv);
                         } else {
-                            *reinterpret_cast<float4 *>(part + c + u) = make_float4(y0, y1, y2, y3);
-                            *reinterpret_cast<float4 *>(part + c + u + 4) = make_float4(y4, y5, y6, y7);
+                            *reinterpret_cast<float2 *>((half ? o1 : o0) + c + 8 * j) = make_float2(lo, hi);
                         }
                     }
-                }
             }
             tc_fence_before();
         }
@@ -526,35 +595,52 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
 
 // ---- joining the parts -------------------------------------------------------------
 
-constexpr int JN_NT = 128;     // 4 values a thread
+// out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.  A CTA joins one
+// (request, head), 4 values a thread; lane s of each warp holds part s's
+// factor.  Bound by latency: the references, then all of the parts at once.
+constexpr int JN_NT = 128;
+constexpr int MAX_SPLITS = 32;     // one lane each
 
 template <int DT>
 __global__ void __launch_bounds__(JN_NT) join_kernel(const __grid_constant__ AttendLaunch a,
                                                      const __grid_constant__ AttendParts w)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t rh = blockIdx.x, RH = (int64_t)a.R * a.H;
-    const int r = (int)(rh / a.H), h = (int)(rh - (int64_t)r * a.H), tid = threadIdx.x;
-    float top = -INFINITY;
-    for (int s = 0; s < w.splits; ++s) top = fmaxf(top, w.ml[(s * RH + rh) * 2]);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    float l = 0.0f;
+    const int r = (int)(rh / a.H), h = (int)(rh - (int64_t)r * a.H), tid = threadIdx.x, lane = tid & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (lane < w.splits) ml = *reinterpret_cast<const float2 *>(w.ml + (lane * RH + rh) * 2);
+    const float *o_part = w.o + rh * kLatent + tid * 4;
+    constexpr int AHEAD = 8;
+    float4 p[AHEAD];
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s)
+        if (s < w.splits) p[s] = *reinterpret_cast<const float4 *>(o_part + s * RH * kLatent);
+    float top = ml.x;
+    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float factor = exp2f(ml.x - (top == -INFINITY ? 0.0f : top));
+    float l = factor * ml.y;
+    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int s = 0; s < w.splits; ++s) {
-        const float f = exp2f(w.ml[(s * RH + rh) * 2] - ref);
-        l = fmaf(f, w.ml[(s * RH + rh) * 2 + 1], l);
-        const float4 p = *reinterpret_cast<const float4 *>(w.o + (s * RH + rh) * kLatent + tid * 4);
-        o.x = fmaf(f, p.x, o.x);
-        o.y = fmaf(f, p.y, o.y);
-        o.z = fmaf(f, p.z, o.z);
-        o.w = fmaf(f, p.w, o.w);
+    for (int s0 = 0; s0 < w.splits; s0 += AHEAD) {
+#pragma unroll
+        for (int s = 0; s < AHEAD; ++s) {
+            if (s0 + s >= w.splits) break;
+            const float f = __shfl_sync(0xffffffffu, factor, s0 + s);
+            o.x = fmaf(f, p[s].x, o.x);
+            o.y = fmaf(f, p[s].y, o.y);
+            o.z = fmaf(f, p[s].z, o.z);
+            o.w = fmaf(f, p[s].w, o.w);
+            if (s0 + s + AHEAD < w.splits)
+                p[s] = *reinterpret_cast<const float4 *>(o_part + (s0 + s + AHEAD) * RH * kLatent);
+        }
     }
     const float inv = l == 0.0f ? 0.0f : 128.0f / l;
     uint8_t *out = a.out + (int64_t)r * a.out_rs + (int64_t)h * a.out_hs;
     *reinterpret_cast<uint2 *>(out + tid * 8) =
         make_uint2(floats_to_pair<DT>(o.x * inv, o.y * inv), floats_to_pair<DT>(o.z * inv, o.w * inv));
     if (tid == 0) {
-        const float l2 = l == 0.0f ? -INFINITY : ref + log2f(l);
+        const float l2 = l == 0.0f ? -INFINITY : top + log2f(l);
         if (a.lse) a.lse[rh] = l2 * kLn2;
         if (a.weights) w.lse2[rh] = l2;
     }
@@ -562,14 +648,34 @@ __global__ void __launch_bounds__(JN_NT) join_kernel(const __grid_constant__ Att
 
 // ---- weights -----------------------------------------------------------------------
 
-constexpr int WT_NT = 128;
+// weights[position] += sum over the heads of 2^(score - lse2).  A CTA takes 64
+// rows of a request: a warp reads 64 scores of a head (256 bytes) at a time,
+// the 8 warps take the heads in turn, and their sums meet in shared memory in
+// a fixed order.  Bound by reading the scores once.
+constexpr int WT_NT = 256, WT_ROWS = 64, WT_WARPS = WT_NT / 32;
 
 __global__ void __launch_bounds__(WT_NT) weights_kernel(const __grid_constant__ AttendLaunch a,
                                                         const __grid_constant__ AttendParts w)
 {
+    __shared__ float sums[WT_WARPS][WT_ROWS];
+    const int r = blockIdx.y, i0 = blockIdx.x * WT_ROWS, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c0 = i0 + lane, c1 = c0 + 32;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int r = blockIdx.y, i = blockIdx.x * WT_NT + threadIdx.x;
-    if (i >= a.k) return;
+    const float *s = w.scores + (int64_t)r * a.H * a.k, *lse2 = w.lse2 + (int64_t)r * a.H;
+    const bool on0 = c0 < a.k, on1 = c1 < a.k;
+    float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll 8
+    for (int h = warp; h < a.H; h += WT_WARPS) {
+        const float ref = lse2[h];
+        const float x0 = on0 ? s[(int64_t)h * a.k + c0] : -INFINITY, x1 = on1 ? s[(int64_t)h * a.k + c1] : -INFINITY;
+        sum0 += exp2f(x0 - ref);
+        sum1 += exp2f(x1 - ref);
+    }
+    sums[warp][lane] = sum0;
+    sums[warp][lane + 32] = sum1;
+    __syncthreads();
+    const int i = i0 + threadIdx.x;
+    if (threadIdx.x >= WT_ROWS || i >= a.k) return;
     int bad = 0;
     if (!row_of(a, r, a.ids[(int64_t)r * a.ids_stride + i], &bad)) return;
     const int64_t pos = a.positions[(int64_t)r * a.positions_stride + i];
@@ -577,10 +683,9 @@ __global__ void __launch_bounds__(WT_NT) weights_kernel(const __grid_constant__ 
         if (a.status) record_status(a.status, r, kStatusBadPosition);
         return;
     }
-    const float *s = w.scores + (int64_t)r * a.H * a.k + i, *lse2 = w.lse2 + (int64_t)r * a.H;
     float sum = 0.0f;
-#pragma unroll 8
-    for (int h = 0; h < a.H; ++h) sum += exp2f(s[(int64_t)h * a.k] - lse2[h]);
+#pragma unroll
+    for (int x = 0; x < WT_WARPS; ++x) sum += sums[x][threadIdx.x];
     atomicAdd(a.weights + (int64_t)r * a.weights_stride + pos, sum);
 }
 
@@ -591,7 +696,7 @@ int choose_splits(int64_t units, int tiles, int num_sms)
 {
     int best = 1;
     int64_t best_cost = INT64_MAX;
-    for (int s = 1; s <= tiles && s <= 64; ++s) {
+    for (int s = 1; s <= tiles && s <= MAX_SPLITS; ++s) {
         const int per = (tiles + s - 1) / s;
         if ((tiles + per - 1) / per != s) continue;       // the same parts as a smaller s
         const int64_t waves = (units * s + num_sms - 1) / num_sms;
@@ -651,7 +756,7 @@ cudaError_t launch_dt(const AttendLaunch &a, const AttendParts &w, cudaStream_t 
     if (e == cudaSuccess && w.splits > 1)
         e = launch_after(join_kernel<DT>, dim3((unsigned)(a.R * a.H)), JN_NT, s, a, w);
     if (e == cudaSuccess && a.weights)
-        e = launch_after(weights_kernel, dim3((a.k + WT_NT - 1) / WT_NT, a.R), WT_NT, s, a, w);
+        e = launch_after(weights_kernel, dim3((a.k + WT_ROWS - 1) / WT_ROWS, a.R), WT_NT, s, a, w);
     return e;
 }
 

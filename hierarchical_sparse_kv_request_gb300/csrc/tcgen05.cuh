@@ -12,6 +12,21 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p)
     return (uint32_t)__cvta_generic_to_shared(p);
 }
 
+// One thread of a converged warp, always the same.  MMAs are issued under this
+// rather than under a lane test: the compiler then keeps their descriptors in
+// uniform registers (measured, M = N = 64: 32 cycles an MMA against 45).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile("{\n"
+                 ".reg .pred p;\n"
+                 "elect.sync _|p, 0xffffffff;\n"
+                 "selp.u32 %0, 1, 0, p;\n"
+                 "}"
+                 : "=r"(ok));
+    return ok != 0;
+}
+
 // ---- mbarriers ---------------------------------------------------------------
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
@@ -97,19 +112,18 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t at, uint32_t (&v)[32])
                  : "r"(at));
 }
 
-// 32 lanes x 32 columns: v[c] is the thread's own lane, column c.
-__device__ __forceinline__ void tmem_ld_32x32(uint32_t at, uint32_t (&v)[32])
+__device__ __forceinline__ void tmem_st_16x64(uint32_t at, const uint32_t (&v)[32])
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 " HS_REGS32 ", [%32];"
-                 : HS_R4(v, 0), HS_R4(v, 4), HS_R4(v, 8), HS_R4(v, 12), HS_R4(v, 16), HS_R4(v, 20),
-                   HS_R4(v, 24), HS_R4(v, 28)
-                 : "r"(at));
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x8.b32 [%32], " HS_REGS32 ";" ::HS_I4(v, 0), HS_I4(v, 4),
+                 HS_I4(v, 8), HS_I4(v, 12), HS_I4(v, 16), HS_I4(v, 20), HS_I4(v, 24), HS_I4(v, 28), "r"(at)
+                 : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_32x32(uint32_t at, const uint32_t (&v)[32])
+// 32 lanes x 16 columns: v[c] goes to the thread's own lane, column c.
+__device__ __forceinline__ void tmem_st_32x16(uint32_t at, const uint32_t (&v)[16])
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], " HS_REGS32 ";" ::HS_I4(v, 0), HS_I4(v, 4),
-                 HS_I4(v, 8), HS_I4(v, 12), HS_I4(v, 16), HS_I4(v, 20), HS_I4(v, 24), HS_I4(v, 28), "r"(at)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+                 ::HS_I4(v, 0), HS_I4(v, 4), HS_I4(v, 8), HS_I4(v, 12), "r"(at)
                  : "memory");
 }
 
@@ -143,6 +157,19 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
                  "}" ::"r"(d),
                  "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+                 : "memory");
+}
+
+// The same with A in tensor memory: for M = 64, row i in lane 32 (i / 16) + i %
+// 16, columns of two 16-bit values each.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile("{\n"
+                 ".reg .pred p;\n"
+                 "setp.ne.u32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+                 "}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
                  : "memory");
 }
 

@@ -455,15 +455,15 @@ class HiSparse:
               out_slots=None, out_counts=None, stream=None) -> None:
         """hisparse_evict: free, per request, up to n (or want[r]) hot slots
         of the least accumulated weight (weights: float32 [R][tokens])."""
-        _rows_of(weights, "weights", "torch.float32", self.R)
+        _rows_of(weights, "weights", "float32", self.R)
         _ints(seq_lens, "seq_lens", (self.R,))
         _ints(want, "want", (self.R,))
         _ints(out_slots, "out_slots", (self.R, n))
         _ints(out_counts, "out_counts", (self.R,))
-        _check(self.lib.hisparse_evict(self.h, layer, _addr(weights),
-                                       _row_stride(weights), weights.shape[1], _addr(seq_lens), keep_recent, n, _addr(want),
-                                       _addr(out_slots), _addr(out_counts), _stream(stream)),
-               "hisparse_evict")
+        _check(self.lib.hisparse_evict(self.h, layer, _addr(weights), _row_stride(weights),
+                                       weights.shape[1], _addr(seq_lens), keep_recent, n,
+                                       _addr(want), _addr(out_slots), _addr(out_counts),
+                                       _stream(stream)), "hisparse_evict")
 
     def set_copy_mode(self, mode: int) -> None:
         _check(self.lib.hisparse_set_copy_mode(self.h, mode), "hisparse_set_copy_mode")
@@ -483,18 +483,30 @@ class HiSparse:
 
 # -- 4-bit rows (include/hisparse_rows4.h) ----------------------------------
 
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _dtype16(x, what: str) -> int:
-    d = str(x.dtype)
-    if d == "torch.bfloat16":
+    t = _torch or _load_torch()
+    if x.dtype is t.bfloat16:
         return BF16
-    if d == "torch.float16":
+    if x.dtype is t.float16:
         return F16
-    raise ValueError(f"{what} must be bfloat16 or float16, not {d}")
+    raise ValueError(f"{what} must be bfloat16 or float16, not {x.dtype}")
 
 
 def _rows_of(x, what: str, dtype: str, n: int) -> None:
     """x is [n][...] of dtype with contiguous rows."""
-    if str(x.dtype) != dtype or x.dim() != 2 or x.shape[0] != n or (x.shape[1] > 1 and x.stride(1) != 1):
+    if (x.dtype is not getattr(_torch or _load_torch(), dtype) or x.dim() != 2 or x.shape[0] != n
+            or (x.stride(1) != 1 and x.shape[1] > 1)):
         raise ValueError(f"{what} must be {dtype} [{n}][...] with contiguous rows")
 
 
@@ -505,14 +517,14 @@ def _row_stride(x) -> int:
 
 def _ints(x, what: str, shape) -> None:
     """x is None or a contiguous int32 tensor of this shape."""
-    if x is not None and (str(x.dtype) != "torch.int32" or tuple(x.shape) != shape
+    if x is not None and (x.dtype is not (_torch or _load_torch()).int32 or x.shape != shape
                           or not x.is_contiguous()):
         raise ValueError(f"{what} must be a contiguous int32 tensor of shape {shape}")
 
 
 def _packed(rows, what: str, dims: int):
-    if (str(rows.dtype) != "torch.uint8" or rows.dim() != dims or rows.shape[-1] != ROW4_BYTES
-            or rows.stride(-1) != 1):
+    if (rows.dtype is not (_torch or _load_torch()).uint8 or rows.dim() != dims
+            or rows.shape[-1] != ROW4_BYTES or rows.stride(-1) != 1):
         raise ValueError(f"{what} must be uint8 [...][{ROW4_BYTES}] with contiguous rows")
 
 
@@ -531,15 +543,17 @@ def pack_rows(values, rows, stream=None) -> None:
     """rows (uint8 [n][416], device or pinned) <- values (bf16 or f16
     [n][576]: 512 latent and 64 rope values) in 4 bits."""
     dt, n, vs, rs = _pack_args(values, rows)
-    _check(load_library().hisparse_pack_rows(_addr(values), vs, dt, n, _addr(rows), rs,
-                                             _stream(stream)), "hisparse_pack_rows")
+    _check((_lib or load_library()).hisparse_pack_rows(values.data_ptr(), vs, dt, n,
+                                                       rows.data_ptr(), rs, _stream(stream)),
+           "hisparse_pack_rows")
 
 
 def unpack_rows(rows, values, stream=None) -> None:
     """values (bf16 or f16 [n][576]) <- what rows (uint8 [n][416]) stand for."""
     dt, n, vs, rs = _pack_args(values, rows)
-    _check(load_library().hisparse_unpack_rows(_addr(rows), rs, n, _addr(values), vs, dt,
-                                               _stream(stream)), "hisparse_unpack_rows")
+    _check((_lib or load_library()).hisparse_unpack_rows(rows.data_ptr(), rs, n, values.data_ptr(),
+                                                         vs, dt, _stream(stream)),
+           "hisparse_unpack_rows")
 
 
 def attend_workspace_bytes(num_requests: int, num_heads: int, top_k: int,
@@ -575,19 +589,19 @@ def _attend(q, rows, row_stride, request_stride, R, D, slot_ids, out, scale, lse
     if q.dim() != 3 or q.shape[0] != R or q.shape[2] != ROW4_VALUES or q.stride(2) != 1:
         raise ValueError(f"q must be [{R}][H][{ROW4_VALUES}] with contiguous heads")
     H = q.shape[1]
-    if (out.dtype != q.dtype or tuple(out.shape) != (R, H, ROW4_LATENT) or out.stride(2) != 1):
+    if out.dtype is not q.dtype or out.shape != (R, H, ROW4_LATENT) or out.stride(2) != 1:
         raise ValueError(f"out must be [{R}][{H}][{ROW4_LATENT}] of q's type with contiguous heads")
-    _rows_of(slot_ids, "slot_ids", "torch.int32", R)
+    _rows_of(slot_ids, "slot_ids", "int32", R)
     k = slot_ids.shape[1]
-    if lse is not None and (str(lse.dtype) != "torch.float32" or tuple(lse.shape) != (R, H)
+    if lse is not None and (lse.dtype is not _torch.float32 or lse.shape != (R, H)
                             or not lse.is_contiguous()):
         raise ValueError(f"lse must be a contiguous float32 tensor of shape ({R}, {H})")
     a = AttendArgs()
     if weights is not None:
-        _rows_of(weights, "weights", "torch.float32", R)
+        _rows_of(weights, "weights", "float32", R)
         if positions is None:
             raise ValueError("weights need positions")
-        _rows_of(positions, "positions", "torch.int32", R)
+        _rows_of(positions, "positions", "int32", R)
         if positions.shape[1] != k:
             raise ValueError("positions and slot_ids differ in length")
         a.weights, a.positions = weights.data_ptr(), positions.data_ptr()
@@ -599,9 +613,8 @@ def _attend(q, rows, row_stride, request_stride, R, D, slot_ids, out, scale, lse
         a.resident_count = resident_rows.shape[0]
         a.resident_stride = resident_rows.stride(0) if a.resident_count > 1 else ROW4_BYTES
     if workspace is None:
-        import torch
-        workspace = torch.empty(attend_workspace_bytes(R, H, k, weights is not None),
-                                dtype=torch.uint8, device=q.device)
+        workspace = _torch.empty(attend_workspace_bytes(R, H, k, weights is not None),
+                                dtype=_torch.uint8, device=q.device)
     a.num_requests, a.num_heads, a.top_k, a.dtype = R, H, k, dt
     a.q, a.q_request_stride, a.q_head_stride = q.data_ptr(), q.stride(0), q.stride(1)
     a.rows, a.row_stride, a.request_stride, a.rows_per_request = rows, row_stride, request_stride, D
@@ -610,7 +623,7 @@ def _attend(q, rows, row_stride, request_stride, R, D, slot_ids, out, scale, lse
     a.out, a.out_request_stride, a.out_head_stride = out.data_ptr(), out.stride(0), out.stride(1)
     a.lse, a.status = _addr(lse), _addr(status)
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(load_library().hisparse_attend(ctypes.byref(a), _stream(stream)), "hisparse_attend")
+    _check((_lib or load_library()).hisparse_attend(ctypes.byref(a), _stream(stream)), "hisparse_attend")
 
 
 def evict_select(weights, slot2tok, seq_lens, out_slots, out_counts, keep_recent: int = 0,
@@ -619,18 +632,17 @@ def evict_select(weights, slot2tok, seq_lens, out_slots, out_counts, keep_recent
     (out_slots int32 [R][n], ascending, -1 behind them; out_counts int32 [R])
     of slot2tok int32 [R][D]; weights float32 [R][tokens]."""
     R, D = slot2tok.shape
-    _rows_of(weights, "weights", "torch.float32", R)
+    _rows_of(weights, "weights", "float32", R)
     _ints(slot2tok, "slot2tok", (R, D))
     _ints(seq_lens, "seq_lens", (R,))
     n = out_slots.shape[1]
     _ints(out_slots, "out_slots", (R, n))
     _ints(out_counts, "out_counts", (R,))
     _ints(want, "want", (R,))
-    _check(load_library().hisparse_evict_select(R, D, weights.data_ptr(),
-                                                _row_stride(weights), weights.shape[1], slot2tok.data_ptr(), seq_lens.data_ptr(),
-                                                keep_recent, n, _addr(want), out_slots.data_ptr(),
-                                                out_counts.data_ptr(), _stream(stream)),
-           "hisparse_evict_select")
+    _check((_lib or load_library()).hisparse_evict_select(
+        R, D, weights.data_ptr(), _row_stride(weights), weights.shape[1], slot2tok.data_ptr(),
+        seq_lens.data_ptr(), keep_recent, n, _addr(want), out_slots.data_ptr(),
+        out_counts.data_ptr(), _stream(stream)), "hisparse_evict_select")
 
 
 # -- measurement kernels (include/hisparse_measure.h) -----------------------
