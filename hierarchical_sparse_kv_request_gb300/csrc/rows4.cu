@@ -266,10 +266,7 @@ int hisparse_attend_workspace(int32_t num_requests, int32_t num_heads, int32_t t
     *bytes = 0;
     const int rc = check_attend_sizes(num_requests, num_heads, top_k);
     if (rc != HISPARSE_OK) return rc;
-    const int sms = current_sms();
-    if (!sms) return HISPARSE_ERR_CUDA;
-    *bytes = hs::attend_workspace_bytes(num_requests, num_heads, top_k, with_weights != 0, sms);
-    return HISPARSE_OK;
+    return cuda_status(hs::attend_workspace_bytes(num_requests, num_heads, top_k, with_weights != 0, bytes));
 }
 
 int hisparse_attend(const hisparse_attend_args *p, void *stream)
@@ -296,11 +293,7 @@ int hisparse_attend(const hisparse_attend_args *p, void *stream)
     if (!aligned16(a.q) || !aligned16(a.rows) || !aligned16(a.resident_rows) || !aligned16(a.out) ||
         !aligned16(a.workspace))
         return HISPARSE_ERR_ALIGNMENT;
-    const int sms = current_sms();
-    if (!sms) return HISPARSE_ERR_CUDA;
-    if (a.workspace_bytes <
-        hs::attend_workspace_bytes(a.num_requests, a.num_heads, a.top_k, a.weights != nullptr, sms))
-        return HISPARSE_ERR_CAPACITY;
+    if (a.workspace_bytes < 16) return HISPARSE_ERR_CAPACITY;
     hs::AttendLaunch l;
     l.R = a.num_requests;
     l.H = a.num_heads;
@@ -330,7 +323,9 @@ int hisparse_attend(const hisparse_attend_args *p, void *stream)
     l.positions_stride = a.positions_stride;
     l.status = a.status;
     l.workspace = static_cast<uint8_t *>(a.workspace);
-    return cuda_status(hs::launch_attend(l, sms, static_cast<cudaStream_t>(stream)));
+    bool too_small = false;
+    const cudaError_t e = hs::launch_attend(l, a.workspace_bytes, &too_small, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess && too_small ? HISPARSE_ERR_CAPACITY : cuda_status(e);
 }
 
 int hisparse_evict_select(int32_t num_requests, int32_t rows_per_request, const float *weights,

@@ -67,8 +67,11 @@ struct AttendLaunch {
     int32_t *status;
     uint8_t *workspace;
 };
-int64_t attend_workspace_bytes(int32_t R, int32_t H, int32_t k, bool weights, int num_sms);
-cudaError_t launch_attend(const AttendLaunch &a, int num_sms, cudaStream_t s);
+// Workspace of a call on the current device.  The first call on a device also
+// loads the attention kernels and finds how many of their clusters it holds.
+cudaError_t attend_workspace_bytes(int32_t R, int32_t H, int32_t k, bool weights, int64_t *bytes);
+// Launches nothing and sets *too_small if the workspace is too small.
+cudaError_t launch_attend(const AttendLaunch &a, int64_t workspace_bytes, bool *too_small, cudaStream_t s);
 
 // Arguments of the eviction kernel.  With st.tok2slot the chosen slots are
 // freed in that hot state (slot2tok is then st.slot2tok); without, slot2tok

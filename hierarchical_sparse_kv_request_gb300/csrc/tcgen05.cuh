@@ -53,14 +53,14 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-// Wait for the phase with this parity, for at most about a second; false if
-// it did not come or another thread of the CTA gave up (*gave_up).
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up)
+// The long part of a wait, kept out of line: the attention kernel's loops have
+// to stay in the instruction cache.
+__device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int *gave_up)
 {
-    if (mbar_try(bar, parity)) return true;
     uint64_t t0, t;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
     for (;;) {
+#pragma unroll 1
         for (int i = 0; i < 64; ++i)
             if (mbar_try(bar, parity)) return true;
         asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
@@ -69,6 +69,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
             return false;
         }
     }
+}
+
+// Wait for the phase with this parity, for at most about a second; false if
+// it did not come or another thread of the CTA gave up (*gave_up).
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up)
+{
+    return mbar_try(bar, parity) || mbar_wait_long(bar, parity, gave_up);
 }
 
 // This thread's shared-memory writes become visible to the tensor core.
@@ -119,10 +126,10 @@ __device__ __forceinline__ void tmem_st_16x64(uint32_t at, const uint32_t (&v)[3
                  : "memory");
 }
 
-// 32 lanes x 16 columns: v[c] goes to the thread's own lane, column c.
-__device__ __forceinline__ void tmem_st_32x16(uint32_t at, const uint32_t (&v)[16])
+// The same for 32 columns.
+__device__ __forceinline__ void tmem_st_16x32(uint32_t at, const uint32_t (&v)[16])
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
                  ::HS_I4(v, 0), HS_I4(v, 4), HS_I4(v, 8), HS_I4(v, 12), "r"(at)
                  : "memory");
 }
