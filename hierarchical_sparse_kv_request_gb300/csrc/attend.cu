@@ -61,11 +61,11 @@ constexpr uint32_t TMEM_Q = 2 * TILE;            // lower lanes: S of two tiles,
 constexpr float kMoveAbove = 8.0f;               // base-2 growth that moves the reference
 
 constexpr int MAX_SPLITS = 16;                   // CTAs a cluster
-// At the end, where the tiles were: a part of a head's O a slot (no bank
-// conflict between 8 slots).
-constexpr int SLOTS = HEADS + MAX_SPLITS - 1;
-constexpr uint32_t O_STRIDE = (kLatent + 8) * 4;
-static_assert(SLOTS * O_STRIDE <= STAGES * OPERAND, "O fits where the tiles were");
+// At the end a part of a head's O takes a slot where the tiles were (the stride
+// keeps the bank conflicts of a 16x256b fragment to two ways).
+constexpr uint32_t O_STRIDE = (kLatent + 4) * 4;
+constexpr int SLOTS = (STAGES * OPERAND + HEADS * 64) / O_STRIDE;
+static_assert(SLOTS >= HEADS + MAX_SPLITS - 1, "the parts that a CTA joins");
 
 struct AttendSmem {
     uint64_t full[STAGES], empty[STAGES], scored[2], weighed[2], fetched[SOFTMAX_WARPS], queries, drained;
@@ -73,30 +73,34 @@ struct AttendSmem {
     int gave_up;
     __align__(16) uint8_t valid[STAGES][16];   // bit b of byte n: row 4 n + b of the stage's tile is named
     float factor[HEADS];      // |scale| * log2(e) * the query's power of two, > 0
-    float2 ml[SLOTS];         // at the end: reference and sum of each slot (see join)
+    float2 ml[HEADS + MAX_SPLITS];   // at the end: reference and sum of each part of the CTA's
+                                     // heads, then its factor
+    uint32_t top[HEADS];      // largest magnitude in each query, as its 16 bits
 };
 // Queries on their way to tensor memory start at the last stage and reach a
 // little past it.
-constexpr uint32_t Q_AT = (STAGES - 1) * OPERAND, MISC_AT = STAGES * OPERAND + HEADS * 16;
+constexpr uint32_t Q_AT = (STAGES - 1) * OPERAND, MISC_AT = STAGES * OPERAND + HEADS * 64;
 constexpr size_t AT_SMEM = MISC_AT + sizeof(AttendSmem);
 
-// Row that an id names, or null (nothing, or an id out of range, whose status
+// An id as it is, or -1 if it names nothing or is out of range (then its status
 // bit is set in *bad).
-__device__ __forceinline__ const uint8_t *row_of(const AttendLaunch &a, int r, int32_t id, int *bad)
+__device__ __forceinline__ int32_t checked_id(const AttendLaunch &a, int32_t id, int *bad)
 {
-    if (id < 0) {
-        if (id != -1) *bad |= 1 << kStatusBadIndex;
-        return nullptr;
-    }
-    if (id & kResidentFlag) {
-        const int64_t n = id & (kResidentFlag - 1);
-        if (n < a.res_count) return a.res + n * a.res_stride;
-        *bad |= 1 << kStatusBadResident;
-        return nullptr;
-    }
-    if (id < a.D) return a.rows + (int64_t)r * a.req_stride + (int64_t)id * a.row_stride;
-    *bad |= 1 << kStatusBadIndex;
-    return nullptr;
+    if (id == -1) return -1;
+    const int64_t n = id & (kResidentFlag - 1);
+    const bool resident = id >= 0 && (id & kResidentFlag);
+    if (id >= 0 && n < (resident ? a.res_count : a.D)) return id;
+    *bad |= 1 << (resident ? kStatusBadResident : kStatusBadIndex);
+    return -1;
+}
+
+// The row that a checked id names; for -1, the request's row 0 (hot), which is
+// there too.
+__device__ __forceinline__ const uint8_t *row_of(const AttendLaunch &a, const uint8_t *hot, int32_t id)
+{
+    if (a.res_count > 0 && id >= 0 && (id & kResidentFlag))
+        return a.res + (int64_t)(id & (kResidentFlag - 1)) * a.res_stride;
+    return hot + (int64_t)max(id, 0) * a.row_stride;
 }
 
 __device__ __forceinline__ uint4 ld_row_v4(const void *p)
@@ -134,6 +138,11 @@ __device__ __forceinline__ uint2 ld_smem_v2(uint32_t at)
     return v;
 }
 
+__device__ __forceinline__ void st_smem_v2(uint32_t at, uint32_t x, uint32_t y)
+{
+    asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(x), "r"(y) : "memory");
+}
+
 __device__ __forceinline__ void st_smem_u32(uint32_t at, uint32_t v)
 {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
@@ -163,61 +172,48 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, __half2 scale)
     return make_uint4(pair(even, 0x1404), pair(even, 0x3424), pair(odd, 0x1404), pair(odd, 0x3424));
 }
 
-// A decode warp's four rows, as its threads hold them: half a warp takes the
-// 256 bytes of codes of one row (chunk c = lane % 16; two loads for four
-// rows), a quarter the rope part of one, so every load is whole sectors of a
-// few rows.
+// A decode warp has four rows of a tile.  Lane: bit 0 and bits 4-3 are a
+// number c of 0-7, bits 2-1 the row; the thread takes 16-byte chunks c and c + 8
+// of the row's codes and c of its rope part.  So a load of the warp is 128
+// contiguous bytes of each row, and the 8 lanes that store at once (four rows,
+// two chunks) go to 8 different swizzled units: no bank conflict.
 struct RowPart {
     uint4 codes[2], rope;
-    uint32_t scales[2];
+    uint32_t scales;     // of the two chunks, two e4m3 each
 };
 
-// row: this lane's rope row (lane / 8 of the warp's four), or null.
-__device__ __forceinline__ void fetch(RowPart &p, const uint8_t *row, int lane)
+__device__ __forceinline__ int lane_row(int lane) { return (lane >> 1) & 3; }
+__device__ __forceinline__ int lane_chunk(int lane) { return (lane & 1) + ((lane >> 3) << 1); }
+
+// id: of the lane's row, checked.  For no row (-1) the scales become 0, and with
+// them the values of the second product; its scores are masked.
+__device__ __forceinline__ void fetch(RowPart &p, const AttendLaunch &a, const uint8_t *hot, int32_t id, int lane)
 {
-    const int c = lane & 15;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const uint8_t *src = reinterpret_cast<const uint8_t *>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), (2 * j + (lane >> 4)) * 8));
-        p.codes[j] = make_uint4(0, 0, 0, 0);     // of no row: nothing of it reaches a result
-        p.scales[j] = 0;
-        if (src) {
-            p.codes[j] = ld_row_v4(src + c * 16);
-            p.scales[j] = ld_row_u16(src + kScaleAt + c * 2);
-        }
-    }
-    p.rope = make_uint4(0, 0, 0, 0);
-    if (row) p.rope = ld_row_v4(row + kRopeAt + (lane & 7) * 16);
+    const int c = lane_chunk(lane);
+    const uint8_t *row = row_of(a, hot, id), *src = row + c * 16;
+    p.codes[0] = ld_row_v4(src);
+    p.codes[1] = ld_row_v4(src + 128);
+    p.rope = ld_row_v4(src + kRopeAt);
+    const uint32_t s0 = ld_row_u16(row + kScaleAt + c * 2), s1 = ld_row_u16(row + kScaleAt + 16 + c * 2);
+    p.scales = id >= 0 ? s0 | (s1 << 16) : 0u;
 }
 
-// i0: the warp's first row in the tile.  A thread's four words go to four
-// units of one row and block; lanes start at different words, so that the 8
-// lanes that store at once go to 8 different units.
-__device__ __forceinline__ void decode(const RowPart &p, uint32_t stage, int i0, int lane)
+// at: where the first word goes (see decode_at).
+__device__ __forceinline__ void decode(const RowPart &p, uint32_t at, uint32_t rope_at)
 {
-    const int c = lane & 15, turn = (c >> 1) & 3;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const int i = i0 + 2 * j + (lane >> 4);
         uint32_t s2;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"((uint16_t)p.scales[j]));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"((uint16_t)(p.scales >> (16 * j))));
         const __half2 s = __hmul2(*reinterpret_cast<__half2 *>(&s2), __half2half2(__ushort_as_half(0x5800)));   // 2^7
         const __half2 lo = __low2half2(s), hi = __high2half2(s);
-        const uint4 v = p.codes[j];
-        uint4 a = (turn & 1) ? make_uint4(v.y, v.z, v.w, v.x) : v;
-        a = (turn & 2) ? make_uint4(a.z, a.w, a.x, a.y) : a;       // word (w + turn) % 4 in place w
-        const uint32_t row = stage + (c >> 1) * BLOCK + i * 128;
-        auto put = [&](uint32_t word, int w) {
-            const int n = (w + turn) & 3;
-            st_smem_v4(row + ((((c & 1) * 4 + n) ^ (i & 7)) << 4), decode8(word, n & 2 ? hi : lo));
-        };
-        put(a.x, 0);
-        put(a.y, 1);
-        put(a.z, 2);
-        put(a.w, 3);
+        const uint32_t to = at + j * 4 * BLOCK;
+        st_smem_v4(to, decode8(p.codes[j].x, lo));
+        st_smem_v4(to ^ 16, decode8(p.codes[j].y, lo));
+        st_smem_v4(to ^ 32, decode8(p.codes[j].z, hi));
+        st_smem_v4(to ^ 48, decode8(p.codes[j].w, hi));
     }
-    st_smem_v4(swizzled(stage + ROPE_BLOCK, i0 + (lane >> 3), lane & 7), p.rope);
+    st_smem_v4(rope_at, p.rope);
 }
 
 template <int DT>
@@ -251,10 +247,12 @@ __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t
 
 // ---- queries -------------------------------------------------------------------------
 
-// A softmax warp brings its 16 heads' queries into shared memory (as they
-// are; the last stage is still free) and writes them, scaled, to tensor
-// memory in the fragments of a 16x256b store.
-constexpr uint32_t Q_STRIDE = kRowValues * 2 + 16;     // no bank conflict between 8 heads
+// A softmax warp has its 16 heads' queries copied to shared memory (as they
+// are; the last stage is still free).  Then the warps of each quarter of tensor
+// memory (warp % 4), five of them, find the heads' largest magnitudes and write
+// the queries, scaled, in the fragments of a 16x256b store.
+constexpr uint32_t Q_STRIDE = kRowValues * 2 + 64;     // no bank conflict between neighbours
+constexpr int QUARTER_WARPS = MMA_WARP / 4;
 
 __device__ __forceinline__ void fetch_queries(const AttendLaunch &a, int r, int h0, uint32_t dst, uint32_t bar,
                                               int warp, int lane)
@@ -278,89 +276,127 @@ __device__ __forceinline__ void fetch_queries(const AttendLaunch &a, int r, int 
 
 // Largest magnitudes, by halves, of m and 8 values (NaN does not count).
 template <int DT>
-__device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y)
+__device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y)      // (the signs mean nothing)
 {
     uint32_t z;
     if (DT == kBf16)
-        asm("max.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+        asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
     else
-        asm("max.f16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+        asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
     return z;
 }
 
 template <int DT>
 __device__ __forceinline__ uint32_t magnitude(uint32_t m, uint4 x)
 {
-    return max2<DT>(m, max2<DT>(max2<DT>(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), max2<DT>(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+    return max2<DT>(m, max2<DT>(max2<DT>(x.x, x.y), max2<DT>(x.z, x.w)));
 }
 
+// The largest magnitudes (see top) of heads lane / 4 and lane / 4 + 8 of the
+// quarter; share: the warp's part of the values.
 template <int DT>
-__device__ __forceinline__ void place_queries(const AttendLaunch &a, int h0, uint32_t src, uint32_t tmem, float *factor,
-                                              int warp, int lane)
+__device__ __forceinline__ void measure_queries(uint32_t src, uint32_t *top, int quarter, int share, int lane)
 {
-    const int g = lane >> 2, q = lane & 3, i0 = warp * 16 + g;
-    const uint32_t at[2] = {src + i0 * Q_STRIDE, src + (i0 + 8) * Q_STRIDE};
-    const bool on[2] = {h0 + i0 < a.H, h0 + i0 + 8 < a.H};
+    const int i0 = quarter * 16 + (lane >> 2);
+    const uint32_t at = src + i0 * Q_STRIDE + (lane & 3) * 16;
     uint32_t m[2] = {0, 0};      // (of no head: of whatever is there, and not used)
 #pragma unroll 1
-    for (int n = 0; n < kRowValues / 32; n += 3) {
-        uint4 x[6];
+    for (int n = share; n < kRowValues / 32; n += QUARTER_WARPS)
 #pragma unroll
-        for (int j = 0; j < 6; ++j) x[j] = ld_smem_v4(at[j & 1] + ((n + (j >> 1)) * 4 + q) * 16);
-#pragma unroll
-        for (int j = 0; j < 6; ++j) m[j & 1] = magnitude<DT>(m[j & 1], x[j]);
-    }
-    float up[2], u7[2];
+        for (int half = 0; half < 2; ++half)
+            m[half] = magnitude<DT>(m[half], ld_smem_v4(at + half * 8 * Q_STRIDE + n * 64));
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        uint32_t x = m[half];
-        x = max2<DT>(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        uint32_t x = max2<DT>(m[half], __shfl_xor_sync(0xffffffffu, m[half], 1));
         x = max2<DT>(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        const uint32_t top = max(x >> 16, x & 0xFFFFu);
+        x &= 0x7FFF7FFFu;
+        if ((lane & 3) == 0) atomicMax(top + i0 + 8 * half, max(x >> 16, x & 0xFFFFu));
+    }
+}
+
+// Two values times a power of two, exactly: 2^n for bf16, 2^n in two steps for
+// f16, whose own powers reach 2^15.
+template <int DT>
+struct PowerOfTwo {
+    uint32_t f[2];
+    __device__ __forceinline__ PowerOfTwo(int n, bool negative)
+    {
+        const float s = negative ? -1.0f : 1.0f;
+        if (DT == kBf16) {
+            f[0] = floats_to_pair<DT>(s * exp2i(n), s * exp2i(n));
+        } else {
+            const int a = max(min(n, 15), -14);
+            f[0] = floats_to_pair<DT>(s * exp2i(a), s * exp2i(a));
+            f[1] = floats_to_pair<DT>(exp2i(n - a), exp2i(n - a));
+        }
+    }
+    __device__ __forceinline__ uint32_t times(uint32_t x) const
+    {
+        uint32_t y;
+        if (DT == kBf16) {
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(f[0]));
+        } else {
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(f[0]));
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(y), "r"(f[1]));
+        }
+        return y;
+    }
+};
+
+template <int DT>
+__device__ __forceinline__ void place_queries(const AttendLaunch &a, int h0, uint32_t src, uint32_t tmem, const uint32_t *top,
+                                              float *factor, int quarter, int share, int lane)
+{
+    const int q = lane & 3, i0 = quarter * 16 + (lane >> 2);
+    const uint32_t at = src + i0 * Q_STRIDE;
+    int e[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int i = i0 + 8 * half;
         // exponent of the largest value; 0 for none and for infinities, which
         // pass through as they are (as NaN does)
-        int e = (int)(__float_as_uint(pair_to_float<DT>(top).x) >> 23) - 127;
-        if (top == 0 || e == 128) e = 0;
-        e = max(e, -119);      // (2^(7 - e) is a float)
-        // with the sign of the scale, so that the factor of the scores is
-        // positive; u7: decode8's 2^7
-        up[half] = copysignf(exp2i(-e), a.scale);
-        u7[half] = 128.0f * up[half];
-        if (q == 0) factor[i0 + 8 * half] = fmaxf(fabsf(a.scale) * kLog2e * exp2i(e), FLT_MIN);
+        e[half] = (int)(__float_as_uint(pair_to_float<DT>(top[i]).x) >> 23) - 127;
+        if (top[i] == 0 || e[half] == 128) e[half] = 0;
+        // (2^(7 - e) is representable, in one step or two)
+        e[half] = max(e[half], DT == kBf16 ? -119 : -23);
+        if (q == 0 && share == 0) factor[i] = fmaxf(fabsf(a.scale) * kLog2e * exp2i(e[half]), FLT_MIN);
     }
-    // Latent columns 8 j + 2 q and + 1 hold the even (q even) or the odd
-    // values of the eight at 16 j + 8 (q / 2): the order of decode8.
+    // with the sign of the scale, so that the factor of the scores is positive
+    const bool neg = a.scale < 0.0f;
+    const bool on[2] = {h0 + i0 < a.H, h0 + i0 + 8 < a.H};
+    // 8 columns a time.  Latent columns 8 j + 2 q and + 1 hold the even (q
+    // even) or the odd values of the eight at 16 j + 8 (q / 2), the order of
+    // decode8, with its 2^7; rope columns their values in order.
+    const PowerOfTwo<DT> up7[2] = {{7 - e[0], neg}, {7 - e[1], neg}};
     const uint32_t pick = q & 1 ? 0x7632 : 0x5410;
 #pragma unroll 1
-    for (int c = 0; c < kLatent / 2; c += 64) {
-        uint32_t v[32];
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            uint4 x[4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) x[n] = ld_smem_v4(at[n & 1] + (c + 8 * (j + (n >> 1))) * 4 + (q >> 1) * 16);
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int half = n & 1, to = 4 * (j + (n >> 1)) + 2 * half;
-                const float2 y = pair_to_float<DT>(__byte_perm(x[n].x, x[n].y, pick));
-                const float2 z = pair_to_float<DT>(__byte_perm(x[n].z, x[n].w, pick));
-                v[to] = on[half] ? floats_to_pair<kF16>(y.x * u7[half], y.y * u7[half]) : 0u;
-                v[to + 1] = on[half] ? floats_to_pair<kF16>(z.x * u7[half], z.y * u7[half]) : 0u;
-            }
-        }
-        tmem_st_16x64(tmem + c, v);
-    }
-    uint32_t v[16];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = share; j < kLatent / 16; j += QUARTER_WARPS) {
+        uint32_t v[4];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const uint2 x = ld_smem_v2(at[half] + kLatent * 2 + (8 * j + 2 * q) * 4);
-            const float2 y = pair_to_float<DT>(x.x), z = pair_to_float<DT>(x.y);
-            v[4 * j + 2 * half] = on[half] ? floats_to_pair<DT>(y.x * up[half], y.y * up[half]) : 0u;
-            v[4 * j + 2 * half + 1] = on[half] ? floats_to_pair<DT>(z.x * up[half], z.y * up[half]) : 0u;
+            const uint4 x = ld_smem_v4(at + half * 8 * Q_STRIDE + j * 32 + (q >> 1) * 16);
+            uint32_t lo = up7[half].times(__byte_perm(x.x, x.y, pick)), hi = up7[half].times(__byte_perm(x.z, x.w, pick));
+            if (DT == kBf16) {
+                const float2 y = pair_to_float<DT>(lo), z = pair_to_float<DT>(hi);
+                lo = floats_to_pair<kF16>(y.x, y.y);
+                hi = floats_to_pair<kF16>(z.x, z.y);
+            }
+            v[2 * half] = on[half] ? lo : 0u;
+            v[2 * half + 1] = on[half] ? hi : 0u;
         }
-    tmem_st_16x32(tmem + kLatent / 2, v);
+        tmem_st_16x8(tmem + j * 8, v);
+    }
+    if (share < 4) {
+        const PowerOfTwo<DT> up[2] = {{-e[0], neg}, {-e[1], neg}};
+        uint32_t v[4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint2 x = ld_smem_v2(at + half * 8 * Q_STRIDE + kLatent * 2 + share * 32 + q * 8);
+            v[2 * half] = on[half] ? up[half].times(x.x) : 0u;
+            v[2 * half + 1] = on[half] ? up[half].times(x.y) : 0u;
+        }
+        tmem_st_16x8(tmem + kLatent / 2 + share * 8, v);
+    }
     tmem_wait_st();
 }
 
@@ -368,8 +404,12 @@ __device__ __forceinline__ void place_queries(const AttendLaunch &a, int h0, uin
 struct AttendParts {
     int splits, tiles_per_split;
     float *lse2;            // [R][H] log2 of the sums, for the weights
-    float *scores;          // [R][H][score_stride] base-2 scores, for the weights
-    int64_t score_stride;   // whole tiles
+    // Base-2 scores, for the weights: [R][head_blocks][tiles] blocks of 16 heads
+    // by 64 rows, each as a softmax warp holds it: [8][32 lanes][4], the
+    // fragments of a 16x256b load.
+    float4 *scores;
+    int64_t head_blocks;
+    int tiles;
 };
 
 // This CTA's shared-memory address `at` in CTA `rank` of the cluster.
@@ -385,10 +425,13 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t at, uint32_t x, uint32_t 
     asm volatile("st.shared::cluster.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(x), "r"(y) : "memory");
 }
 
-__device__ __forceinline__ void cluster_sync_all()
+__device__ __forceinline__ void st_cluster_v4(uint32_t at, uint4 v)
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <int DT>
 __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant__ AttendLaunch a,
@@ -413,18 +456,18 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
     const int dw = warp - SOFTMAX_WARPS;      // its rows of a tile: 4 dw to 4 dw + 3
     const int32_t *ids = a.ids + (int64_t)r * a.ids_stride + k0;
     auto id_at = [&](int t) {
-        const int n = t * TILE + dw * 4 + (lane >> 3);
+        const int n = t * TILE + dw * 4 + lane_row(lane);
         return n < rows ? ids[n] : -1;
     };
-    RowPart next;
-    const uint8_t *row = nullptr;
-    int32_t id = -1;
+    const uint8_t *hot = a.rows + (int64_t)r * a.req_stride;
+    RowPart part[2];                      // of tiles t (even) and t + 1
+    int32_t id[2] = {-1, -1}, id2 = -1;   // theirs (checked), and of tile t + 2
     int bad = 0;
+    const int heads = min(HEADS, a.H - h0);
     if (decodes) {
-        const int32_t id0 = id_at(0);
-        id = id_at(1);
-        row = row_of(a, r, id0, &bad);
-        fetch(next, row, lane);
+        id[0] = id_at(0);
+        id[1] = id_at(1);
+        id2 = id_at(2);
     } else if (warp < SOFTMAX_WARPS) {
         fetch_queries(a, r, h0, stages + Q_AT, smem_u32(&sm.fetched[warp]), warp, lane);
     } else {
@@ -437,11 +480,12 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
                 mbar_init(smem_u32(&sm.scored[s]), 1);
                 mbar_init(smem_u32(&sm.weighed[s]), SOFTMAX_WARPS);
             }
-            mbar_init(smem_u32(&sm.queries), SOFTMAX_WARPS);
+            mbar_init(smem_u32(&sm.queries), MMA_WARP);
             mbar_init(smem_u32(&sm.drained), 1);
             sm.gave_up = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
+        sm.top[lane] = sm.top[lane + 32] = 0;
         __syncwarp();
         tmem_alloc_all(smem_u32(&sm.tmem));
     }
@@ -451,31 +495,63 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
     const uint32_t tmem = sm.tmem;
     volatile int *gave_up = &sm.gave_up;
     auto all = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
+    bool ok = true;
 
+    // ---- the queries, while the first tiles' rows are on their way -----------------
+    if (decodes) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            id[u] = checked_id(a, id[u], &bad);
+            fetch(part[u], a, hot, id[u], lane);
+        }
+    }
+    const int quarter = warp & 3, share = warp >> 2;
+    const bool serves = warp < MMA_WARP && quarter * 16 < heads;     // the quarter has heads
+    if (serves) {
+        ok = all(mbar_wait(smem_u32(&sm.fetched[quarter]), 0, gave_up));
+        for (int i = 0; !ok && i < (1 << 20) && !mbar_try(smem_u32(&sm.fetched[quarter]), 0); ++i) {}
+        measure_queries<DT>(stages + Q_AT, sm.top, quarter, share, lane);
+    }
+    __syncthreads();
+    if (warp < MMA_WARP) {
+        // (the rows of a quarter without heads stay as they are: what they give
+        // stays in that quarter)
+        if (serves)
+            place_queries<DT>(a, h0, stages + Q_AT, tmem + ((uint32_t)(quarter * 32) << 16) + TMEM_Q, sm.top, sm.factor,
+                              quarter, share, lane);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.queries));
+    }
     // softmax threads: reference and sum of heads lane / 4 and lane / 4 + 8 of
     // the warp's 16
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
     if (decodes) {
         // ---- fetch and decode -----------------------------------------------
         int s = 0, phase = 1;     // the phase whose end frees stage s
-#pragma unroll 1
-        for (int t = 0; t < tiles; ++t) {
-            const RowPart now = next;
-            const uint32_t named = __ballot_sync(0xffffffffu, row != nullptr);    // lanes 0, 8, 16, 24
-            row = row_of(a, r, id, &bad);
-            fetch(next, row, lane);
-            id = id_at(t + 2);
-            const bool free = t < STAGES - 1    ? true
-                              : t == STAGES - 1 ? mbar_wait(smem_u32(&sm.queries), 0, gave_up)
-                                                : mbar_wait(smem_u32(&sm.empty[s]), phase, gave_up);
-            if (!all(free)) break;
-            decode(now, stages + s * OPERAND, dw * 4, lane);
-            if (lane == 0)
-                sm.valid[s][dw] = (uint8_t)((named & 1u) | (named >> 7 & 2u) | (named >> 14 & 4u) | (named >> 21 & 8u));
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.full[s]));
-            if (++s == STAGES) s = 0, phase ^= 1;
+        const int i = dw * 4 + lane_row(lane), c = lane_chunk(lane);
+        const uint32_t at = stages + (c >> 1) * BLOCK + i * 128 + ((((c & 1) * 4) ^ (i & 7)) << 4);
+        const uint32_t rope_at = swizzled(stages + ROPE_BLOCK, i, c);
+        for (int t = 0; ok && t < tiles; t += 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (t + u >= tiles) break;
+                ok = all(t + u < STAGES - 1    ? true
+                         : t + u == STAGES - 1 ? mbar_wait(smem_u32(&sm.queries), 0, gave_up)
+                                               : mbar_wait(smem_u32(&sm.empty[s]), phase, gave_up));
+                if (!ok) break;
+                decode(part[u], at + s * OPERAND, rope_at + s * OPERAND);
+                const uint32_t named = __ballot_sync(0xffffffffu, id[u] >= 0);      // rows: lanes 0, 2, 4, 6
+                if (lane == 0)
+                    sm.valid[s][dw] = (uint8_t)((named & 1u) | (named >> 1 & 2u) | (named >> 2 & 4u) | (named >> 3 & 8u));
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.full[s]));
+                if (++s == STAGES) s = 0, phase ^= 1;
+                id[u] = checked_id(a, id2, &bad);
+                if (t + u + 2 < tiles) fetch(part[u], a, hot, id[u], lane);
+                id2 = id_at(t + u + 3);
+            }
         }
         if (bad && a.status) atomicOr(a.status + r, bad);
     } else if (warp == MMA_WARP) {
@@ -483,7 +559,7 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
         constexpr uint32_t qk = mma_desc(HEADS, TILE, false, false);
         constexpr uint32_t qk_rope = mma_desc(HEADS, TILE, DT == kBf16, false);
         constexpr uint32_t pv = mma_desc(HEADS, 256, false, true);
-        bool ok = all(mbar_wait(smem_u32(&sm.queries), 0, gave_up));
+        ok = all(mbar_wait(smem_u32(&sm.queries), 0, gave_up));
         int s = 0, s_pv = 0, phase = 0;
         for (int t = 0; ok && t <= tiles; ++t) {
             if (t < tiles) {            // S(t) = Q K^T
@@ -534,28 +610,26 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
     } else {
         // ---- softmax --------------------------------------------------------------
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-        bool ok = all(mbar_wait(smem_u32(&sm.fetched[warp]), 0, gave_up));
-        for (int i = 0; !ok && i < (1 << 20) && !mbar_try(smem_u32(&sm.fetched[warp]), 0); ++i) {}
-        place_queries<DT>(a, h0, stages + Q_AT, lanes + TMEM_Q, sm.factor, warp, lane);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.queries));
+        ok = ok && all(mbar_wait(smem_u32(&sm.queries), 0, gave_up));     // for the factors
         const int g = lane >> 2, c2 = (lane & 3) * 2;     // fragment row and column
         const int vs = (c2 >> 2) * 8 + (c2 & 3);          // its bit in valid's 16-bit pieces
         const int i0 = warp * 16 + g, i1 = i0 + 8;
         const float f0 = sm.factor[i0], f1 = sm.factor[i1];
-        float *sc0 = nullptr, *sc1 = nullptr;
-        if (a.weights) {
-            float *at = w.scores + ((int64_t)r * a.H + h0) * w.score_stride + k0 + c2;
-            if (h0 + i0 < a.H) sc0 = at + (int64_t)i0 * w.score_stride;
-            if (h0 + i1 < a.H) sc1 = at + (int64_t)i1 * w.score_stride;
-        }
+        float4 *sc = nullptr;       // this thread's place in the warp's score blocks
+        if (a.weights && h0 + warp * 16 < a.H)
+            sc = w.scores + (((int64_t)r * w.head_blocks + h0 / 16 + warp) * w.tiles + split * w.tiles_per_split) * 256 + lane;
         int s = 0, phase = 0, s_before = 0, phase_before = 0;     // of tile t, of tile t - 1
         for (int t = 0; ok && t < tiles; ++t) {
             ok = all(mbar_wait(smem_u32(&sm.full[s]), phase, gave_up) &&
                      mbar_wait(smem_u32(&sm.scored[t & 1]), (t >> 1) & 1, gave_up));
             if (!ok) break;
             tc_fence_after();
+            if (!serves) {          // no head to weigh
+                if (lane == 0) mbar_arrive(smem_u32(&sm.weighed[t & 1]));
+                s_before = s, phase_before = phase;
+                if (++s == STAGES) s = 0, phase ^= 1;
+                continue;
+            }
             uint32_t v[32];
             tmem_ld_16x64(lanes + (t & 1) * TILE, v);
             const uint4 valid = *reinterpret_cast<const uint4 *>(sm.valid[s]);
@@ -569,13 +643,11 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
                     for (int b = 0; b < 2; ++b)
                         if (!((named[j >> 1] >> ((j & 1) * 16 + b)) & 1u)) x[4 * j + b] = x[4 * j + 2 + b] = -INFINITY;
             }
-            if (a.weights) {
+            if (sc) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int c = t * TILE + 8 * j;
-                    if (sc0) *reinterpret_cast<float2 *>(sc0 + c) = make_float2(x[4 * j] * f0, x[4 * j + 1] * f0);
-                    if (sc1) *reinterpret_cast<float2 *>(sc1 + c) = make_float2(x[4 * j + 2] * f1, x[4 * j + 3] * f1);
-                }
+                for (int j = 0; j < 8; ++j)
+                    sc[j * 32] = make_float4(x[4 * j] * f0, x[4 * j + 1] * f0, x[4 * j + 2] * f1, x[4 * j + 3] * f1);
+                sc += 256;
             }
             float top0 = fmaxf(x[0], x[1]), top1 = fmaxf(x[2], x[3]);
 #pragma unroll
@@ -639,78 +711,136 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
     }
 
     // ---- join ----------------------------------------------------------------------
-    // Head i is joined by CTA i % splits.  Part p of its m-th head (head p' + m
-    // splits, p' its own rank) comes to slot p + m splits of its shared memory,
-    // once every CTA's last product is done and the tiles are free.
-    const int last = tiles - 1, heads = min(HEADS, a.H - h0);
+    // Head i is joined by CTA i % splits (its `mine` heads: split + m splits).
+    // O goes from tensor memory to slot i of this CTA's shared memory, where
+    // the tiles were, and the other CTAs' heads from there to slots behind the
+    // owner's own, 512 bytes a store; or, where these do not all fit, straight
+    // from tensor memory to slot p + m splits of the owner (part p), which
+    // takes twice as long (32 bytes of a row at a time: 64 KB to a neighbour
+    // 7.9 thousand cycles against 4).
+    const int last = tiles - 1, mine = (heads - split + w.splits - 1) / w.splits;
+    const bool staged = w.splits > 1 && heads + (w.splits - 1) * ((heads + w.splits - 1) / w.splits) <= SLOTS;
+    auto part_slot = [&](int owner, int m, int p) {      // part p of the owner's m-th head
+        return !staged        ? p + m * w.splits
+               : p == owner   ? owner + m * w.splits
+                              : heads + m * (w.splits - 1) + (p < owner ? p : p - 1);
+    };
     const bool done = all(mbar_wait(smem_u32(&sm.empty[last % STAGES]), (last / STAGES) & 1, gave_up));
     tc_fence_after();
-    if (w.splits > 1) cluster_sync_all();
-    if (done && warp < MMA_WARP && (warp & 3) * 16 < heads) {
-        const int i0 = (warp & 3) * 16 + (lane >> 2), i1 = i0 + 8;
-        const int to0 = i0 % w.splits, to1 = i1 % w.splits;
-        const int slot0 = i0 - to0 + split, slot1 = i1 - to1 + split;
-        if (warp < SOFTMAX_WARPS && (lane & 3) == 0) {
-            if (i0 < heads) st_cluster_v2(in_cta(smem_u32(&sm.ml[slot0]), to0), __float_as_uint(m0), __float_as_uint(l0));
-            if (i1 < heads) st_cluster_v2(in_cta(smem_u32(&sm.ml[slot1]), to1), __float_as_uint(m1), __float_as_uint(l1));
+    if (w.splits > 1) cluster_arrive();       // this CTA's tiles are free
+    if (w.splits > 1 && !staged) cluster_wait();
+    if (done && serves) {
+        const uint32_t upper = tmem + ((uint32_t)(quarter * 32) << 16) + TMEM_UPPER;
+        uint32_t at[2];
+        bool on[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int i = quarter * 16 + (lane >> 2) + 8 * half, owner = i % w.splits;
+            on[half] = i < heads;
+            at[half] = stages + (staged ? i : part_slot(owner, i / w.splits, split)) * O_STRIDE + (lane & 3) * 8;
+            if (!staged) at[half] = in_cta(at[half], owner);
         }
-        const uint32_t upper = tmem + ((uint32_t)((warp & 3) * 32) << 16) + TMEM_UPPER;
-        const uint32_t at0 = in_cta(stages + slot0 * O_STRIDE + (lane & 3) * 8, to0);
-        const uint32_t at1 = in_cta(stages + slot1 * O_STRIDE + (lane & 3) * 8, to1);
 #pragma unroll 1
-        for (int c = (warp >> 2) * 64; c < kLatent; c += (MMA_WARP / 4) * 64) {
-            uint32_t v[32];
-            tmem_ld_16x64(upper + c, v);
+        for (int c = share; c < kLatent / 32; c += QUARTER_WARPS) {
+            uint32_t v[16];
+            tmem_ld_16x32(upper + c * 32, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (i0 < heads) st_cluster_v2(at0 + (c + 8 * j) * 4, v[4 * j], v[4 * j + 1]);
-                if (i1 < heads) st_cluster_v2(at1 + (c + 8 * j) * 4, v[4 * j + 2], v[4 * j + 3]);
-            }
+            for (int half = 0; half < 2; ++half)
+                if (on[half]) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (staged)
+                            st_smem_v2(at[half] + c * 128 + j * 32, v[4 * j + 2 * half], v[4 * j + 2 * half + 1]);
+                        else
+                            st_cluster_v2(at[half] + c * 128 + j * 32, v[4 * j + 2 * half], v[4 * j + 2 * half + 1]);
+                    }
+                }
         }
         tc_fence_before();
     }
-    if (w.splits > 1)
-        cluster_sync_all();
-    else
+    if (staged) {
         __syncthreads();
-    // out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p, half a head's values a warp
-    const int mine = (heads - split + w.splits - 1) / w.splits;
-    for (int n = warp; n < 2 * mine; n += AT_NT / 32) {
-        const int slot = (n >> 1) * w.splits, d = (n & 1) * 256 + lane * 8;
-        float2 ml = make_float2(-INFINITY, 0.0f);      // lane p: part p
-        if (lane < w.splits) ml = sm.ml[slot + lane];
-        float top = ml.x;
-        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        float factor = ex2(ml.x - (top == -INFINITY ? 0.0f : top));
-        float l = factor * ml.y;
-        for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-        factor *= l == 0.0f ? 0.0f : 128.0f / l;       // decode8's 2^7
-        float o[8] = {};
-        const uint32_t at = stages + slot * O_STRIDE + d * 4;
-#pragma unroll 2
-        for (int p = 0; p < w.splits; ++p) {
-            const uint4 x = ld_smem_v4(at + p * O_STRIDE), y = ld_smem_v4(at + p * O_STRIDE + 16);
-            const float f = __shfl_sync(0xffffffffu, factor, p);
-            // columns are in decode8's order: the even values, then the odd
-            o[0] = fmaf(f, __uint_as_float(x.x), o[0]);
-            o[2] = fmaf(f, __uint_as_float(x.y), o[2]);
-            o[4] = fmaf(f, __uint_as_float(x.z), o[4]);
-            o[6] = fmaf(f, __uint_as_float(x.w), o[6]);
-            o[1] = fmaf(f, __uint_as_float(y.x), o[1]);
-            o[3] = fmaf(f, __uint_as_float(y.y), o[3]);
-            o[5] = fmaf(f, __uint_as_float(y.z), o[5]);
-            o[7] = fmaf(f, __uint_as_float(y.w), o[7]);
+        cluster_wait();
+#pragma unroll 1
+        for (int n = warp; n < heads * 2; n += AT_NT / 32) {       // half a head's values a warp
+            const int i = n >> 1, owner = i % w.splits;
+            if (owner == split) continue;
+            const uint32_t src = stages + i * O_STRIDE + (n & 1) * 1024 + lane * 16;
+            const uint32_t dst = in_cta(stages + part_slot(owner, i / w.splits, split) * O_STRIDE + (n & 1) * 1024 + lane * 16, owner);
+            const uint4 x = ld_smem_v4(src), y = ld_smem_v4(src + 512);
+            st_cluster_v4(dst, x);
+            st_cluster_v4(dst + 512, y);
         }
-        const int h = h0 + split + slot;
-        st_v4(a.out + (int64_t)r * a.out_rs + (int64_t)h * a.out_hs + d * 2,
-              make_uint4(floats_to_pair<DT>(o[0], o[1]), floats_to_pair<DT>(o[2], o[3]),
-                         floats_to_pair<DT>(o[4], o[5]), floats_to_pair<DT>(o[6], o[7])));
-        if (lane == 0 && !(n & 1)) {
-            const int64_t rh = (int64_t)r * a.H + h;
+    }
+    if (warp < SOFTMAX_WARPS && (lane & 3) == 0) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int i = warp * 16 + (lane >> 2) + 8 * half, owner = i % w.splits;
+            if (i < heads)
+                st_cluster_v2(in_cta(smem_u32(&sm.ml[i - owner + split]), owner), __float_as_uint(half ? m1 : m0),
+                              __float_as_uint(half ? l1 : l0));
+        }
+    }
+    if (w.splits > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    // out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p: first the parts'
+    // factors, a thread a part, then the sums, half a head's values a warp
+    int group = 1;       // threads a head
+    while (group < w.splits) group *= 2;
+    if (tid < (mine * group + 31) / 32 * 32) {
+        const int m = tid / group, p = tid % group;
+        const bool on = m < mine && p < w.splits;
+        float2 ml = on ? sm.ml[m * w.splits + p] : make_float2(-INFINITY, 0.0f);
+        float top = ml.x;
+#pragma unroll 1
+        for (int x = 1; x < group; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float f = ex2(ml.x - (top == -INFINITY ? 0.0f : top));
+        float l = f * ml.y;
+#pragma unroll 1
+        for (int x = 1; x < group; x *= 2) l += __shfl_xor_sync(0xffffffffu, l, x);
+        if (on) sm.ml[m * w.splits + p].x = l == 0.0f ? 0.0f : f * (128.0f / l);        // decode8's 2^7
+        if (on && p == 0) {
+            const int64_t rh = (int64_t)r * a.H + h0 + split + m * w.splits;
             const float l2 = l == 0.0f ? -INFINITY : top + log2f(l);
             if (a.lse) a.lse[rh] = l2 * kLn2;
             if (a.weights) w.lse2[rh] = l2;
+        }
+    }
+    __syncthreads();
+    // Columns are in decode8's order: of eight values the even in one 16-byte
+    // unit, the odd in the next, here in neighbouring lanes.
+#pragma unroll 1
+    for (int n = warp; n < 2 * mine; n += AT_NT / 32) {
+        const int m = n >> 1, d = (n & 1) * 256 + lane * 4;      // its place in the slot, and 128 on
+        float o[2][4] = {};
+#pragma unroll 2
+        for (int p = 0; p < w.splits; ++p) {
+            const uint32_t at = stages + part_slot(split, m, p) * O_STRIDE + d * 4;
+            const float f = sm.ml[m * w.splits + p].x;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint4 x = ld_smem_v4(at + u * 512);
+                o[u][0] = fmaf(f, __uint_as_float(x.x), o[u][0]);
+                o[u][1] = fmaf(f, __uint_as_float(x.y), o[u][1]);
+                o[u][2] = fmaf(f, __uint_as_float(x.z), o[u][2]);
+                o[u][3] = fmaf(f, __uint_as_float(x.w), o[u][3]);
+            }
+        }
+        uint8_t *out = a.out + (int64_t)r * a.out_rs + (int64_t)(h0 + split + m * w.splits) * a.out_hs + d * 2;
+        const bool odd = lane & 1;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            // even lane: values 0-3 of its eight; odd lane: 4-7
+            const float g0 = __shfl_xor_sync(0xffffffffu, odd ? o[u][0] : o[u][2], 1);
+            const float g1 = __shfl_xor_sync(0xffffffffu, odd ? o[u][1] : o[u][3], 1);
+            *reinterpret_cast<uint2 *>(out + u * 256) =
+                odd ? make_uint2(floats_to_pair<DT>(g0, o[u][2]), floats_to_pair<DT>(g1, o[u][3]))
+                    : make_uint2(floats_to_pair<DT>(o[u][0], g0), floats_to_pair<DT>(o[u][1], g1));
         }
     }
     if (tid == 0 && sm.gave_up && a.status) record_status(a.status, r, kStatusAttendTimeout);
@@ -719,42 +849,48 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
 
 // ---- weights -----------------------------------------------------------------------
 
-// weights[position] += sum over the heads of 2^(score - lse2).  A CTA takes 64
-// rows of a request: a warp reads 64 scores of a head (256 bytes) at a time,
-// the 8 warps take the heads in turn, and their sums meet in shared memory in
-// a fixed order.  Bound by reading the scores once.
-constexpr int WT_NT = 256, WT_ROWS = TILE, WT_WARPS = WT_NT / 32;
+// weights[position] += sum over the heads of 2^(score - lse2).  A CTA takes the
+// 64 rows of a tile, warp j eight of them: it reads the j-th 512 bytes of every
+// block of 16 heads, a thread two rows by two heads at a time; then the 8
+// threads of a row meet, always in the same order.  Bound by reading the
+// scores once.
+constexpr int WT_NT = 256;
 
 __global__ void __launch_bounds__(WT_NT) weights_kernel(const __grid_constant__ AttendLaunch a,
                                                         const __grid_constant__ AttendParts w)
 {
-    __shared__ float sums[WT_WARPS][WT_ROWS];
-    const int r = blockIdx.y, i0 = blockIdx.x * WT_ROWS, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const float *s = w.scores + (int64_t)r * a.H * w.score_stride, *lse2 = w.lse2 + (int64_t)r * a.H;
-    float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll 8
-    for (int h = warp; h < a.H; h += WT_WARPS) {
-        const float ref = lse2[h];
-        const float2 x = *reinterpret_cast<const float2 *>(s + h * w.score_stride + i0 + 2 * lane);
-        sum.x += ex2(x.x - ref);
-        sum.y += ex2(x.y - ref);
+    const int t = blockIdx.x, r = blockIdx.y, j = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
+    const int i = t * TILE + 8 * j + 2 * (lane & 3) + (g & 1);      // this thread's row in the end (g < 2)
+    int32_t pos = -1;
+    bool on = g < 2 && i < a.k;
+    if (on) {     // (inputs: they do not wait for the launch before)
+        int bad = 0;
+        on = checked_id(a, a.ids[(int64_t)r * a.ids_stride + i], &bad) >= 0;
+        if (on) pos = a.positions[(int64_t)r * a.positions_stride + i];
     }
-    *reinterpret_cast<float2 *>(&sums[warp][2 * lane]) = sum;
-    __syncthreads();
-    const int i = i0 + threadIdx.x;
-    if (threadIdx.x >= WT_ROWS || i >= a.k) return;
-    int bad = 0;
-    if (!row_of(a, r, a.ids[(int64_t)r * a.ids_stride + i], &bad)) return;
-    const int64_t pos = a.positions[(int64_t)r * a.positions_stride + i];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float4 *s = w.scores + ((int64_t)r * w.head_blocks * w.tiles + t) * 256 + j * 32 + lane;
+    const float *lse2 = w.lse2 + (int64_t)r * a.H;
+    float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll 8
+    for (int b = 0; b < (int)w.head_blocks; ++b) {
+        const float4 x = s[(int64_t)b * w.tiles * 256];
+        const int h = b * 16 + g;
+        const float ref0 = h < a.H ? lse2[h] : INFINITY, ref1 = h + 8 < a.H ? lse2[h + 8] : INFINITY;
+        sum0 += ex2(x.x - ref0) + ex2(x.z - ref1);
+        sum1 += ex2(x.y - ref0) + ex2(x.w - ref1);
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+        sum0 += __shfl_xor_sync(0xffffffffu, sum0, o);
+        sum1 += __shfl_xor_sync(0xffffffffu, sum1, o);
+    }
+    if (!on) return;
     if (pos < 0 || pos >= a.weights_tokens) {
         if (a.status) record_status(a.status, r, kStatusBadPosition);
         return;
     }
-    float total = 0.0f;
-#pragma unroll
-    for (int x = 0; x < WT_WARPS; ++x) total += sums[x][threadIdx.x];
-    atomicAdd(a.weights + (int64_t)r * a.weights_stride + pos, total);
+    atomicAdd(a.weights + (int64_t)r * a.weights_stride + pos, g & 1 ? sum1 : sum0);
 }
 
 // ---- host ----------------------------------------------------------------------------
@@ -851,13 +987,14 @@ AttendParts lay_out(int32_t R, int32_t H, int32_t k, bool weights, const Capacit
     const int tiles = (k + TILE - 1) / TILE;
     p.splits = choose_splits((int64_t)R * ((H + HEADS - 1) / HEADS), tiles, cap);
     p.tiles_per_split = (tiles + p.splits - 1) / p.splits;
-    p.score_stride = (int64_t)tiles * TILE;
+    p.tiles = tiles;
+    p.head_blocks = (H + 15) / 16;
     float *f = reinterpret_cast<float *>(ws);
     int64_t n = 4;          // never empty
     p.lse2 = f + n;
     n += weights ? up4(RH) : 0;
-    p.scores = f + n;
-    n += weights ? RH * p.score_stride : 0;
+    p.scores = reinterpret_cast<float4 *>(f + n);
+    n += weights ? R * p.head_blocks * tiles * 1024 : 0;
     *bytes = n * 4;
     return p;
 }
@@ -871,7 +1008,7 @@ cudaError_t launch_dt(const AttendLaunch &a, const AttendParts &w, cudaStream_t 
     cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel<DT>, a, w);
     if (e == cudaSuccess && a.weights) {
         cfg = {};
-        cfg.gridDim = dim3((unsigned)(w.score_stride / WT_ROWS), (unsigned)a.R);
+        cfg.gridDim = dim3((unsigned)w.tiles, (unsigned)a.R);
         cfg.blockDim = dim3(WT_NT);
         cfg.stream = s;
         attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

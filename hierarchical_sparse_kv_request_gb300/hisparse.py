@@ -165,10 +165,24 @@ def _addr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+_torch = _raw_stream = None
+
+
+def _load_torch():
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _torch = torch
+    return _torch
+
+
 def _stream(s) -> Optional[int]:
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        t = _torch or _load_torch()
+        if _raw_stream is not None:     # the same without a Stream object (2.9 -> 0.4 us)
+            return _raw_stream(t.cuda.current_device())
+        return t.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -482,17 +496,6 @@ class HiSparse:
 
 
 # -- 4-bit rows (include/hisparse_rows4.h) ----------------------------------
-
-_torch = None
-
-
-def _load_torch():
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return _torch
-
 
 def _dtype16(x, what: str) -> int:
     t = _torch or _load_torch()
