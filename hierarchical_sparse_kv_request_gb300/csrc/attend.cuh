@@ -1,0 +1,348 @@
+// attend.cuh -- the parts of the attention kernel (attend.cu) that stand for
+// themselves: ids and rows, decoding, queries as f16, and the join of what the
+// CTAs of a cluster have worked on.
+#pragma once
+
+#include <cfloat>
+
+#include "rows4.cuh"
+#include "tcgen05.cuh"
+
+namespace hs {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int TILE = 64;          // rows a tile
+constexpr float kMoveAbove = 8.0f;               // base-2 growth that moves the softmax's reference
+constexpr int MAX_SPLITS = 16;                   // CTAs a cluster
+
+// An id as it is, or -1 if it names nothing or is out of range (then its status
+// bit is set in *bad).
+__device__ __forceinline__ int32_t checked_id(const AttendLaunch &a, int32_t id, int *bad)
+{
+    if (id == -1) return -1;
+    const int64_t n = id & (kResidentFlag - 1);
+    const bool resident = id >= 0 && (id & kResidentFlag);
+    if (id >= 0 && n < (resident ? a.res_count : a.D)) return id;
+    *bad |= 1 << (resident ? kStatusBadResident : kStatusBadIndex);
+    return -1;
+}
+
+// The row that a checked id names; for -1, the request's row 0 (hot), which is
+// there too.
+__device__ __forceinline__ const uint8_t *row_of(const AttendLaunch &a, const uint8_t *hot, int32_t id)
+{
+    if (a.res_count > 0 && id >= 0 && (id & kResidentFlag))
+        return a.res + (int64_t)(id & (kResidentFlag - 1)) * a.res_stride;
+    return hot + (int64_t)max(id, 0) * a.row_stride;
+}
+
+__device__ __forceinline__ uint4 ld_row_v4(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// (straight into 32 bits: widening it would wait for it)
+__device__ __forceinline__ uint32_t ld_row_u16(const void *p)
+{
+    uint32_t v;
+    asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void st_smem_v4(uint32_t at, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_smem_v4(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint2 ld_smem_v2(uint32_t at)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_smem_v2(uint32_t at, uint32_t x, uint32_t y)
+{
+    asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(x), "r"(y) : "memory");
+}
+
+__device__ __forceinline__ void st_smem_u32(uint32_t at, uint32_t v)
+{
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
+template <int DT>
+__device__ __forceinline__ float2 pair_to_float(uint32_t w)
+{
+    if (DT == kBf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t floats_to_pair(float x, float y)
+{
+    if (DT == kBf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    const __half2 v = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// 2^x; less than 2^-126 is 0
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A power of two as float
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Eight codes (a 32-bit word of a row) times scale, as f16, in the order 0 2 4
+// 6 1 3 5 7.  The high byte of an f16 holds its sign, exponent and two bits of
+// mantissa: a code's sign in bit 7 and its other bits in 3-1 read as its value
+// times 2^-14, subnormal included, and four codes (the even, the odd) are
+// placed so at once.  The scale comes with 2^7 of that, the result keeps
+// 2^-7.  Exact: at most six significant bits, at least 2^-17.
+__device__ __forceinline__ uint4 decode8(uint32_t w, __half2 scale)
+{
+    const uint32_t even = ((w << 4) & 0x80808080u) | ((w << 1) & 0x0E0E0E0Eu);
+    const uint32_t odd = (w & 0x80808080u) | ((w >> 3) & 0x0E0E0E0Eu);
+    auto pair = [&](uint32_t bytes, uint32_t select) {
+        const uint32_t b = __byte_perm(bytes, 0, select);     // bytes 4-7 are 0
+        const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&b), scale);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    };
+    return make_uint4(pair(even, 0x1404), pair(even, 0x3424), pair(odd, 0x1404), pair(odd, 0x3424));
+}
+
+// Largest magnitudes, by halves, of m and 8 values (NaN does not count).
+template <int DT>
+__device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y)      // (the signs mean nothing)
+{
+    uint32_t z;
+    if (DT == kBf16)
+        asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+    else
+        asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+    return z;
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t magnitude(uint32_t m, uint4 x)
+{
+    return max2<DT>(m, max2<DT>(max2<DT>(x.x, x.y), max2<DT>(x.z, x.w)));
+}
+
+// Two values times a power of two, exactly: 2^n for bf16, 2^n in two steps for
+// f16, whose own powers reach 2^15.
+template <int DT>
+struct PowerOfTwo {
+    uint32_t f[2];
+    __device__ __forceinline__ PowerOfTwo(int n, bool negative)
+    {
+        const float s = negative ? -1.0f : 1.0f;
+        if (DT == kBf16) {
+            f[0] = floats_to_pair<DT>(s * exp2i(n), s * exp2i(n));
+        } else {
+            const int a = max(min(n, 15), -14);
+            f[0] = floats_to_pair<DT>(s * exp2i(a), s * exp2i(a));
+            f[1] = floats_to_pair<DT>(exp2i(n - a), exp2i(n - a));
+        }
+    }
+    __device__ __forceinline__ uint32_t times(uint32_t x) const
+    {
+        uint32_t y;
+        if (DT == kBf16) {
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(f[0]));
+        } else {
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(f[0]));
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(y), "r"(f[1]));
+        }
+        return y;
+    }
+};
+
+// A query is multiplied by 2^-e (latent: 2^(7 - e), decode8's 2^7) and the sign
+// of the scale; top: the 16 bits of its largest magnitude.  e is that one's
+// exponent, or 0 where there is none and for infinities, which pass through as
+// they are (as NaN does); 2^(7 - e) has to be representable, in one step or two.
+template <int DT>
+__device__ __forceinline__ int query_exponent(uint32_t top)
+{
+    const int e = (int)(__float_as_uint(pair_to_float<DT>(top).x) >> 23) - 127;
+    return max(top == 0 || e == 128 ? 0 : e, DT == kBf16 ? -119 : -23);
+}
+
+// What the products of such a query have to be multiplied by to be base-2
+// scores; positive.
+__device__ __forceinline__ float query_factor(const AttendLaunch &a, int e)
+{
+    return fmaxf(fabsf(a.scale) * kLog2e * exp2i(e), FLT_MIN);
+}
+
+// How a call is cut up, and its workspace.
+struct AttendParts {
+    int splits;             // CTAs a request's (or head tile's) rows are split over: a cluster
+    int rows_per_split;
+    float *lse2;            // [R][H] log2 of the sums, for the weights
+    // Base-2 scores, for the weights: [R][head_blocks][tiles] blocks of 16 heads
+    // by 64 rows, each as a warp holds it: [8][32 lanes][4], where lane's four
+    // are head lane / 4 by rows 8 j + 2 (lane % 4) and + 1, then head lane / 4 + 8
+    // by the same rows.
+    float4 *scores;
+    int64_t head_blocks;
+    int tiles;
+};
+
+// This CTA's shared-memory address `at` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t at, int rank)
+{
+    uint32_t y;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"(at), "r"(rank));
+    return y;
+}
+
+__device__ __forceinline__ void st_cluster_v2(uint32_t at, uint32_t x, uint32_t y)
+{
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(x), "r"(y) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_v4(uint32_t at, uint4 v)
+{
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// ---- join ------------------------------------------------------------------------
+//
+// Every CTA of a cluster has, for each of its heads, a part of O and its
+// reference and sum; head i is joined by CTA i % splits, whose m-th head is its
+// rank + m splits.  Parts are slots of 512 floats in shared memory, values in
+// decode8's order.  `staged`: a CTA's own parts are in slots 0 to heads - 1, and
+// what the others send goes behind them; else part p of head m comes to slot p
+// + m splits of its owner.
+constexpr uint32_t O_STRIDE = (kLatent + 4) * 4;     // (keeps a fragment's bank conflicts to two ways)
+
+// Slots that a staged join of so many heads and CTAs takes at most.
+__host__ __device__ constexpr int staged_slots(int heads, int splits)
+{
+    return heads + (splits - 1) * ((heads + splits - 1) / splits);
+}
+
+struct Join {
+    uint32_t slots;      // shared-memory address of slot 0
+    float2 *ml;          // [mine][splits] reference and sum of each part
+    int heads, splits, rank;
+    bool staged;
+
+    __device__ __forceinline__ int mine() const { return (heads - rank + splits - 1) / splits; }
+    __device__ __forceinline__ uint32_t part(int owner, int m, int p) const
+    {
+        const int slot = !staged      ? p + m * splits
+                         : p == owner ? owner + m * splits
+                                      : heads + m * (splits - 1) + (p < owner ? p : p - 1);
+        return slots + slot * O_STRIDE;
+    }
+    // Staged parts to their owners, 512 bytes a store (64 KB to a neighbour: 3.8
+    // thousand cycles; 32 bytes of a row at a time, straight from fragments,
+    // 7.9).  Every CTA's slots must be free to take them.
+    __device__ __forceinline__ void send(int warp, int warps, int lane) const
+    {
+#pragma unroll 1
+        for (int n = warp; n < heads * 2; n += warps) {       // half a head's values a warp
+            const int i = n >> 1, owner = i % splits;
+            if (owner == rank) continue;
+            const uint32_t off = (n & 1) * 1024 + lane * 16;
+            const uint32_t src = slots + i * O_STRIDE + off, dst = in_cta(part(owner, i / splits, rank) + off, owner);
+            const uint4 x = ld_smem_v4(src), y = ld_smem_v4(src + 512);
+            st_cluster_v4(dst, x);
+            st_cluster_v4(dst + 512, y);
+        }
+    }
+    // A head's reference and sum to its owner.
+    __device__ __forceinline__ void send_ml(int i, float m, float l) const
+    {
+        const int owner = i % splits;
+        st_cluster_v2(in_cta(smem_u32(&ml[i - owner + rank]), owner), __float_as_uint(m), __float_as_uint(l));
+    }
+    // Once all parts are here: out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p
+    // and lse, of heads h0 + ... of request r.  The whole CTA.
+    template <int DT>
+    __device__ __forceinline__ void finish(const AttendLaunch &a, const AttendParts &w, int r, int h0, int tid, int threads) const
+    {
+        const int lane = tid & 31, warp = tid >> 5;
+        const int mine = this->mine();
+        // the parts' factors, a thread a part
+        int group = 1;       // threads a head
+        while (group < splits) group *= 2;
+        for (int n = tid; n < (mine * group + 31) / 32 * 32; n += threads) {
+            const int m = n / group, p = n % group;
+            const bool on = m < mine && p < splits;
+            const float2 x = on ? ml[m * splits + p] : make_float2(-INFINITY, 0.0f);
+            float top = x.x;
+#pragma unroll 1
+            for (int o = 1; o < group; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float f = ex2(x.x - (top == -INFINITY ? 0.0f : top));
+            float l = f * x.y;
+#pragma unroll 1
+            for (int o = 1; o < group; o *= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (on) ml[m * splits + p].x = l == 0.0f ? 0.0f : f * (128.0f / l);        // decode8's 2^7
+            if (on && p == 0) {
+                const int64_t rh = (int64_t)r * a.H + h0 + rank + m * splits;
+                const float l2 = l == 0.0f ? -INFINITY : top + log2f(l);
+                if (a.lse) a.lse[rh] = l2 * kLn2;
+                if (a.weights) w.lse2[rh] = l2;
+            }
+        }
+        __syncthreads();
+        // The sums, half a head's values a warp.  Of eight values the even are
+        // in one 16-byte unit and the odd in the next, here in neighbouring lanes.
+#pragma unroll 1
+        for (int n = warp; n < 2 * mine; n += threads / 32) {
+            const int m = n >> 1, d = (n & 1) * 256 + lane * 4;      // its place in the slot, and 128 on
+            float o[2][4] = {};
+#pragma unroll 2
+            for (int p = 0; p < splits; ++p) {
+                const uint32_t at = part(rank, m, p) + d * 4;
+                const float f = ml[m * splits + p].x;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint4 x = ld_smem_v4(at + u * 512);
+                    o[u][0] = fmaf(f, __uint_as_float(x.x), o[u][0]);
+                    o[u][1] = fmaf(f, __uint_as_float(x.y), o[u][1]);
+                    o[u][2] = fmaf(f, __uint_as_float(x.z), o[u][2]);
+                    o[u][3] = fmaf(f, __uint_as_float(x.w), o[u][3]);
+                }
+            }
+            uint8_t *out = a.out + (int64_t)r * a.out_rs + (int64_t)(h0 + rank + m * splits) * a.out_hs + d * 2;
+            const bool odd = lane & 1;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                // even lane: values 0-3 of its eight; odd lane: 4-7
+                const float g0 = __shfl_xor_sync(0xffffffffu, odd ? o[u][0] : o[u][2], 1);
+                const float g1 = __shfl_xor_sync(0xffffffffu, odd ? o[u][1] : o[u][3], 1);
+                *reinterpret_cast<uint2 *>(out + u * 256) =
+                    odd ? make_uint2(floats_to_pair<DT>(g0, o[u][2]), floats_to_pair<DT>(g1, o[u][3]))
+                        : make_uint2(floats_to_pair<DT>(o[u][0], g0), floats_to_pair<DT>(o[u][1], g1));
+            }
+        }
+    }
+};
+
+}  // namespace hs
