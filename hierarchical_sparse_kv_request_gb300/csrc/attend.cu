@@ -81,59 +81,54 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t block, int i, int u)
 }
 
 // A decode warp has four rows of a tile.  Half a warp takes the 256 bytes of
-// codes of one row (chunk c = lane % 16; two loads for four rows), a quarter the
-// rope part of one.  (Loads of 128 bytes of each of the four rows, which need no
-// shuffles and no turned words: 39.7 against 35.9 us for 32 requests, 128 heads,
-// 2,048 rows.)
+// codes of a row (16 bytes a thread; rows lane / 16 and + 2), a quarter the rope
+// part of one of its two.  So eight neighbouring threads load 128 contiguous
+// bytes (32 bytes of each of four rows, measured: 39.7 against 35.9 us for 32
+// requests, 128 heads, 2,048 rows) and store eight units of a row and block.
 struct RowPart {
     uint4 codes[2], rope;
     uint32_t scales[2];  // two e4m3 each
 };
 
-// id: of row lane / 8, checked.  Nothing here waits for what it loads.
-__device__ __forceinline__ void fetch(RowPart &p, const AttendLaunch &a, const uint8_t *hot, int32_t id, int lane)
+__device__ __forceinline__ const uint8_t *shfl_ptr(const uint8_t *p, int lane)
 {
-    const int c = lane & 15;
-    const uint8_t *row = row_of(a, hot, id);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const uint8_t *src = reinterpret_cast<const uint8_t *>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), (2 * j + (lane >> 4)) * 8));
-        p.codes[j] = ld_row_v4(src + c * 16);
-        p.scales[j] = ld_row_u16(src + kScaleAt + c * 2);
-    }
-    p.rope = ld_row_v4(row + kRopeAt + (lane & 7) * 16);
+    return reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), lane));
 }
 
-// i0: the warp's first row in the tile; named: bit 8 i is set if its row i is
-// one.  The values of no row are 0 (by its scales) for the second product; its
-// scores are masked.  A thread's four words go to four units of one row and
-// block; lanes start at different words, so that the 8 lanes that store at once
-// go to 8 different units.
-__device__ __forceinline__ void decode(const RowPart &p, uint32_t named, uint32_t stage, int i0, int lane)
+// row: of the warp's n-th, in lane first + n.  Nothing here waits for what it
+// loads.
+__device__ __forceinline__ void fetch(RowPart &p, const uint8_t *row, int first, int lane)
 {
-    const int c = lane & 15, turn = (c >> 1) & 3;
+    const int c = lane & 15;
+    const uint8_t *src[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const int n = 2 * j + (lane >> 4), i = i0 + n;
+        src[j] = shfl_ptr(row, first + (lane >> 4) + 2 * j);
+        p.codes[j] = ld_row_v4(src[j] + c * 16);
+    }
+    p.rope = ld_row_v4((lane & 8 ? src[1] : src[0]) + kRopeAt + (lane & 7) * 16);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) p.scales[j] = ld_row_u16(src[j] + kScaleAt + c * 2);
+}
+
+// named: bit n is set if the warp's row n is one.  The values of no row are 0 (by
+// its scales) for the second product; its scores are masked.  at: where the
+// thread's first word goes, for each of its rows.
+__device__ __forceinline__ void decode(const RowPart &p, uint32_t named, const uint32_t (&at)[2], uint32_t rope_at, int lane)
+{
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
         uint32_t s2;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"((uint16_t)(named >> (n * 8) & 1u ? p.scales[j] : 0u)));
+        const bool on = named >> ((lane >> 4) + 2 * j) & 1u;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"((uint16_t)(on ? p.scales[j] : 0u)));
         const __half2 s = __hmul2(*reinterpret_cast<__half2 *>(&s2), __half2half2(__ushort_as_half(0x5800)));   // 2^7
         const __half2 lo = __low2half2(s), hi = __high2half2(s);
-        const uint4 v = p.codes[j];
-        uint4 x = (turn & 1) ? make_uint4(v.y, v.z, v.w, v.x) : v;
-        x = (turn & 2) ? make_uint4(x.z, x.w, x.x, x.y) : x;       // word (w + turn) % 4 in place w
-        const uint32_t row = stage + (c >> 1) * BLOCK + i * 128;
-        auto put = [&](uint32_t word, int w) {
-            const int u = (w + turn) & 3;
-            st_smem_v4(row + ((((c & 1) * 4 + u) ^ (i & 7)) << 4), decode8(word, u & 2 ? hi : lo));
-        };
-        put(x.x, 0);
-        put(x.y, 1);
-        put(x.z, 2);
-        put(x.w, 3);
+        st_smem_v4(at[j], decode8(p.codes[j].x, lo));
+        st_smem_v4(at[j] + 2 * BLOCK, decode8(p.codes[j].y, lo));
+        st_smem_v4(at[j] + 4 * BLOCK, decode8(p.codes[j].z, hi));
+        st_smem_v4(at[j] + 6 * BLOCK, decode8(p.codes[j].w, hi));
     }
-    st_smem_v4(swizzled(stage + ROPE_BLOCK, i0 + (lane >> 3), lane & 7), p.rope);
+    st_smem_v4(rope_at, p.rope);
 }
 
 // ---- queries -------------------------------------------------------------------------
@@ -142,7 +137,7 @@ __device__ __forceinline__ void decode(const RowPart &p, uint32_t named, uint32_
 // are; the last stage is still free).  Then the warps of each quarter of tensor
 // memory (warp % 4), five of them, find the heads' largest magnitudes and write
 // the queries, scaled, in the fragments of a 16x256b store.
-constexpr uint32_t Q_STRIDE = kRowValues * 2 + 64;     // no bank conflict between neighbours
+constexpr uint32_t Q_STRIDE = kRowValues * 2 + 32;     // no bank conflict between neighbours
 constexpr int QUARTER_WARPS = MMA_WARP / 4;
 
 __device__ __forceinline__ void fetch_queries(const AttendLaunch &a, int r, int h0, uint32_t dst, uint32_t bar,
@@ -171,13 +166,15 @@ template <int DT>
 __device__ __forceinline__ void measure_queries(uint32_t src, uint32_t *top, int quarter, int share, int lane)
 {
     const int i0 = quarter * 16 + (lane >> 2);
-    const uint32_t at = src + i0 * Q_STRIDE + (lane & 3) * 16;
+    const uint32_t at = src + i0 * Q_STRIDE + (lane & 1) * 16 + (lane & 2) * 32;     // 32 bytes of 128
     uint32_t m[2] = {0, 0};      // (of no head: of whatever is there, and not used)
 #pragma unroll 1
-    for (int n = share; n < kRowValues / 32; n += QUARTER_WARPS)
+    for (int n = share; n < kRowValues / 64; n += QUARTER_WARPS)
 #pragma unroll
         for (int half = 0; half < 2; ++half)
-            m[half] = magnitude<DT>(m[half], ld_smem_v4(at + half * 8 * Q_STRIDE + n * 64));
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                m[half] = magnitude<DT>(m[half], ld_smem_v4(at + half * 8 * Q_STRIDE + n * 128 + u * 32));
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         uint32_t x = max2<DT>(m[half], __shfl_xor_sync(0xffffffffu, m[half], 1));
@@ -204,7 +201,7 @@ __device__ __forceinline__ void place_queries(const AttendLaunch &a, int h0, uin
     const bool neg = a.scale < 0.0f;
     const bool on[2] = {h0 + i0 < a.H, h0 + i0 + 8 < a.H};
     // 8 columns a time.  Latent columns 8 j + 2 q and + 1 hold the even (q
-    // even) or the odd values of the eight at 16 j + 8 (q / 2), the order of
+    // even) or the odd values of the eight in unit 2 j + q / 2, the order of
     // decode8, with its 2^7; rope columns their values in order.
     const PowerOfTwo<DT> up7[2] = {{7 - e[0], neg}, {7 - e[1], neg}};
     const uint32_t pick = q & 1 ? 0x7632 : 0x5410;
@@ -213,7 +210,7 @@ __device__ __forceinline__ void place_queries(const AttendLaunch &a, int h0, uin
         uint32_t v[4];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const uint4 x = ld_smem_v4(at + half * 8 * Q_STRIDE + j * 32 + (q >> 1) * 16);
+            const uint4 x = ld_smem_v4(at + half * 8 * Q_STRIDE + unit_values(2 * j + (q >> 1)) * 2);
             uint32_t lo = up7[half].times(__byte_perm(x.x, x.y, pick)), hi = up7[half].times(__byte_perm(x.z, x.w, pick));
             if (DT == kBf16) {
                 const float2 y = pair_to_float<DT>(lo), z = pair_to_float<DT>(hi);
@@ -260,19 +257,21 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
 
     const bool decodes = warp >= SOFTMAX_WARPS && warp < MMA_WARP;
     const int dw = warp - SOFTMAX_WARPS;      // its rows of a tile: 4 dw to 4 dw + 3
+    // Decode warps take the ids of eight tiles at once: lane has row lane % 4 of
+    // the warp's in tile lane / 4 of the eight.
     const int32_t *ids = a.ids + (int64_t)r * a.ids_stride + k0;
-    auto id_at = [&](int t) {
-        const int n = t * TILE + dw * 4 + (lane >> 3);
+    auto ids_at = [&](int t) {
+        const int n = (t + (lane >> 2)) * TILE + dw * 4 + (lane & 3);
         return n < rows ? ids[n] : -1;
     };
-    const uint8_t *hot = a.rows + (int64_t)r * a.req_stride;
+    const uint8_t *hot = a.rows + (int64_t)r * a.req_stride, *row = hot;
     RowPart next;               // of tile t + 1
-    int32_t id = -1, id2 = -1;  // its id (checked), and that of tile t + 2
+    uint32_t named = 0;         // bit n: lane n's id names a row
+    int32_t id = -1;            // of the next eight tiles
     int bad = 0;
     const int heads = min(HEADS, a.H - h0);
     if (decodes) {
-        id = id_at(0);
-        id2 = id_at(1);
+        id = ids_at(0);
     } else if (warp < SOFTMAX_WARPS) {
         fetch_queries(a, r, h0, stages + Q_AT, smem_u32(&sm.fetched[warp]), warp, lane);
     } else {
@@ -303,9 +302,15 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
     bool ok = true;
 
     // ---- the queries, while the first tile's rows are on their way -----------------
-    if (decodes) {
+    auto name_rows = [&](int t) {      // of the eight tiles from t on; their ids are in id
         id = checked_id(a, id, &bad);
-        fetch(next, a, hot, id, lane);
+        row = row_of(a, hot, id);
+        named = __ballot_sync(0xffffffffu, id >= 0);
+        id = ids_at(t + 8);
+    };
+    if (decodes) {
+        name_rows(0);
+        fetch(next, row, 0, lane);
     }
     const int quarter = warp & 3, share = warp >> 2;
     const bool serves = warp < MMA_WARP && quarter * 16 < heads;     // the quarter has heads
@@ -331,20 +336,23 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
     if (decodes) {
         // ---- fetch and decode -----------------------------------------------
         int s = 0, phase = 1;     // the phase whose end frees stage s
+        // word w of a row's 16-byte chunk c is unit c % 8 of block 2 w + c / 8
+        const int c = lane & 15, i = dw * 4 + (lane >> 4);
+        const uint32_t to0 = swizzled(stages + (c >> 3) * BLOCK, i, c & 7), to1 = swizzled(stages + (c >> 3) * BLOCK, i + 2, c & 7);
+        const uint32_t rope_to = swizzled(stages + ROPE_BLOCK, i + (lane & 8 ? 2 : 0), lane & 7);
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
             const RowPart now = next;
-            const uint32_t named = __ballot_sync(0xffffffffu, id >= 0);    // rows: lanes 0, 8, 16, 24
-            id = checked_id(a, id2, &bad);
-            fetch(next, a, hot, id, lane);      // (of the last tile: row 0)
-            id2 = id_at(t + 2);
+            const uint32_t now_named = named >> ((t & 7) * 4) & 15u;
+            if (((t + 1) & 7) == 0) name_rows(t + 1);
+            fetch(next, row, ((t + 1) & 7) * 4, lane);      // (after the last tile: row 0)
             ok = ok && all(t < STAGES - 1    ? true
                            : t == STAGES - 1 ? mbar_wait(smem_u32(&sm.queries), 0, gave_up)
                                              : mbar_wait(smem_u32(&sm.empty[s]), phase, gave_up));
             if (!ok) break;
-            decode(now, named, stages + s * OPERAND, dw * 4, lane);
-            if (lane == 0)
-                sm.valid[s][dw] = (uint8_t)((named & 1u) | (named >> 7 & 2u) | (named >> 14 & 4u) | (named >> 21 & 8u));
+            const uint32_t to[2] = {to0 + s * OPERAND, to1 + s * OPERAND};
+            decode(now, now_named, to, rope_to + s * OPERAND, lane);
+            if (lane == 0) sm.valid[s][dw] = (uint8_t)now_named;
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.full[s]));
@@ -440,12 +448,6 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
                     for (int b = 0; b < 2; ++b)
                         if (!((named[j >> 1] >> ((j & 1) * 16 + b)) & 1u)) x[4 * j + b] = x[4 * j + 2 + b] = -INFINITY;
             }
-            if (sc) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    sc[j * 32] = make_float4(x[4 * j] * f0, x[4 * j + 1] * f0, x[4 * j + 2] * f1, x[4 * j + 3] * f1);
-                sc += 256;
-            }
             float top0 = fmaxf(x[0], x[1]), top1 = fmaxf(x[2], x[3]);
 #pragma unroll
             for (int j = 1; j < 8; ++j) {
@@ -498,6 +500,12 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.weighed[t & 1]));
+            if (sc) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    sc[j * 32] = make_float4(x[4 * j] * f0, x[4 * j + 1] * f0, x[4 * j + 2] * f1, x[4 * j + 3] * f1);
+                sc += 256;
+            }
             s_before = s, phase_before = phase;
             if (++s == STAGES) s = 0, phase ^= 1;
         }

@@ -129,6 +129,14 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, __half2 scale)
     return make_uint4(pair(even, 0x1404), pair(even, 0x3424), pair(odd, 0x1404), pair(odd, 0x3424));
 }
 
+// The first of the eight values that unit u (8 columns) of a decoded row holds:
+// units are numbered so that a row's 16-byte pieces, which have four times eight
+// values, go to neighbouring units, one word of each at a time.
+__host__ __device__ constexpr int unit_values(int u)
+{
+    return ((u >> 3 & 1) * 8 + (u & 7)) * 32 + (u >> 4) * 8;
+}
+
 // Largest magnitudes, by halves, of m and 8 values (NaN does not count).
 template <int DT>
 __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y)      // (the signs mean nothing)
@@ -234,7 +242,7 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // Every CTA of a cluster has, for each of its heads, a part of O and its
 // reference and sum; head i is joined by CTA i % splits, whose m-th head is its
 // rank + m splits.  Parts are slots of 512 floats in shared memory, values in
-// decode8's order.  `staged`: a CTA's own parts are in slots 0 to heads - 1, and
+// the columns' order (unit_values, decode8).  `staged`: a CTA's own parts are in slots 0 to heads - 1, and
 // what the others send goes behind them; else part p of head m comes to slot p
 // + m splits of its owner.
 constexpr uint32_t O_STRIDE = (kLatent + 4) * 4;     // (keeps a fragment's bank conflicts to two ways)
@@ -311,26 +319,29 @@ struct Join {
             }
         }
         __syncthreads();
-        // The sums, half a head's values a warp.  Of eight values the even are
-        // in one 16-byte unit and the odd in the next, here in neighbouring lanes.
+        // The sums, half a head's values a warp: 32 units, two threads a unit and
+        // 16 units at a time, whose values are 256 neighbours of out.  Of eight
+        // values the even are in one 16-byte piece and the odd in the next, here
+        // in neighbouring lanes.
 #pragma unroll 1
         for (int n = warp; n < 2 * mine; n += threads / 32) {
-            const int m = n >> 1, d = (n & 1) * 256 + lane * 4;      // its place in the slot, and 128 on
+            const int m = n >> 1, unit = (n & 1) * 8 + (lane >> 3) * 16 + (lane >> 1 & 3);     // and + 4
             float o[2][4] = {};
 #pragma unroll 2
             for (int p = 0; p < splits; ++p) {
-                const uint32_t at = part(rank, m, p) + d * 4;
+                const uint32_t at = part(rank, m, p) + unit * 32 + (lane & 1) * 16;
                 const float f = ml[m * splits + p].x;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const uint4 x = ld_smem_v4(at + u * 512);
+                    const uint4 x = ld_smem_v4(at + u * 128);
                     o[u][0] = fmaf(f, __uint_as_float(x.x), o[u][0]);
                     o[u][1] = fmaf(f, __uint_as_float(x.y), o[u][1]);
                     o[u][2] = fmaf(f, __uint_as_float(x.z), o[u][2]);
                     o[u][3] = fmaf(f, __uint_as_float(x.w), o[u][3]);
                 }
             }
-            uint8_t *out = a.out + (int64_t)r * a.out_rs + (int64_t)(h0 + rank + m * splits) * a.out_hs + d * 2;
+            uint8_t *out = a.out + (int64_t)r * a.out_rs + (int64_t)(h0 + rank + m * splits) * a.out_hs +
+                           unit_values(unit) * 2 + (lane & 1) * 8;
             const bool odd = lane & 1;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
