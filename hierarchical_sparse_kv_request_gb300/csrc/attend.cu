@@ -236,6 +236,52 @@ __device__ __forceinline__ void place_queries(const AttendLaunch &a, int h0, uin
     tmem_wait_st();
 }
 
+// ---- out -------------------------------------------------------------------------
+
+// O of a quarter's heads times their factors (ml[head].x), from tensor memory to
+// out: four units a time whose values are 32 neighbours, one unit a thread of
+// the four that have a head's fragment.
+template <int DT>
+__device__ __forceinline__ void store_out(const AttendLaunch &a, int r, int h0, int heads, uint32_t o_at, const float2 *ml,
+                                          int quarter, int share, int lane)
+{
+    const int q = lane & 3, i0 = quarter * 16 + (lane >> 2);
+    const float f[2] = {ml[i0].x, ml[i0 + 8].x};
+    uint8_t *out = a.out + (int64_t)r * a.out_rs + (int64_t)(h0 + i0) * a.out_hs + q * 16;
+#pragma unroll 1
+    for (int n = share; n < 16; n += QUARTER_WARPS) {      // units n and the three that follow by 16
+        uint32_t v[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tmem_ld_16x8(o_at + (n + 16 * j) * 8, v[j]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            // Of unit j this thread has values 0 2, 4 6, 1 3 or 5 7, by q.
+            uint32_t x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x[j] = floats_to_pair<DT>(__uint_as_float(v[j][2 * half]) * f[half], __uint_as_float(v[j][2 * half + 1]) * f[half]);
+            // threads q and q ^ 2 swap: q keeps units 0 and 1 or 2 and 3, with
+            // values 0-3 (q even) or 4-7
+            const bool hi = q & 2;
+            uint32_t y[2][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? x[j] : x[j + 2], 2), own = hi ? x[j + 2] : x[j];
+                const uint32_t even = hi ? got : own, odd = hi ? own : got;
+                y[j][0] = __byte_perm(even, odd, 0x5410);
+                y[j][1] = __byte_perm(even, odd, 0x7632);
+            }
+            // threads q and q ^ 1 swap: q keeps unit q
+            const bool second = q & 1;
+            const uint32_t g0 = __shfl_xor_sync(0xffffffffu, second ? y[0][0] : y[1][0], 1);
+            const uint32_t g1 = __shfl_xor_sync(0xffffffffu, second ? y[0][1] : y[1][1], 1);
+            const uint4 z = second ? make_uint4(g0, g1, y[1][0], y[1][1]) : make_uint4(y[0][0], y[0][1], g0, g1);
+            if (i0 + 8 * half < heads) *reinterpret_cast<uint4 *>(out + half * 8 * a.out_hs + unit_values(n) * 2) = z;
+        }
+    }
+}
+
 template <int DT>
 __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant__ AttendLaunch a,
                                                           const __grid_constant__ AttendParts w)
@@ -515,64 +561,77 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
         l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
     }
 
-    // ---- join (see attend.cuh): O from tensor memory to where the tiles were -------
     const int last = tiles - 1;
-    Join join{stages, sm.ml, heads, w.splits, split, false};
-    join.staged = w.splits > 1 && staged_slots(heads, w.splits) <= SLOTS;
-    const bool staged = join.staged;
     const bool done = all(mbar_wait(smem_u32(&sm.empty[last % STAGES]), (last / STAGES) & 1, gave_up));
     tc_fence_after();
-    if (w.splits > 1) cluster_arrive();       // this CTA's tiles are free
-    if (w.splits > 1 && !staged) cluster_wait();
-    if (done && serves) {
-        const uint32_t upper = tmem + ((uint32_t)(quarter * 32) << 16) + TMEM_UPPER;
-        uint32_t at[2];
-        bool on[2];
+    const uint32_t o_at = tmem + ((uint32_t)(quarter * 32) << 16) + TMEM_UPPER;
+    const bool keeps = warp < SOFTMAX_WARPS && (lane & 3) == 0;      // a thread with references and sums
+    if (w.splits == 1) {
+        // ---- out from tensor memory ------------------------------------------------
+        if (keeps) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int i = quarter * 16 + (lane >> 2) + 8 * half, owner = i % w.splits;
-            on[half] = i < heads;
-            at[half] = (staged ? stages + i * O_STRIDE : join.part(owner, i / w.splits, split)) + (lane & 3) * 8;
-            if (!staged) at[half] = in_cta(at[half], owner);
+            for (int half = 0; half < 2; ++half) {
+                const int i = warp * 16 + (lane >> 2) + 8 * half;
+                sm.ml[i].x = out_factor(half ? l1 : l0);
+                if (i < heads) store_lse(a, w, (int64_t)r * a.H + h0 + i, half ? m1 : m0, half ? l1 : l0);
+            }
         }
-#pragma unroll 1
-        for (int c = share; c < kLatent / 32; c += QUARTER_WARPS) {
-            uint32_t v[16];
-            tmem_ld_16x32(upper + c * 32, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-                if (on[half]) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (staged)
-                            st_smem_v2(at[half] + c * 128 + j * 32, v[4 * j + 2 * half], v[4 * j + 2 * half + 1]);
-                        else
-                            st_cluster_v2(at[half] + c * 128 + j * 32, v[4 * j + 2 * half], v[4 * j + 2 * half + 1]);
-                    }
-                }
-        }
-        tc_fence_before();
-    }
-    if (staged) {
         __syncthreads();
-        cluster_wait();
-        join.send(warp, AT_NT / 32, lane);
-    }
-    if (warp < SOFTMAX_WARPS && (lane & 3) == 0) {
+        if (done && serves) store_out<DT>(a, r, h0, heads, o_at, sm.ml, quarter, share, lane);
+        tc_fence_before();
+        __syncthreads();
+    } else {
+        // ---- join (see attend.cuh): O from tensor memory to where the tiles were ---
+        Join join{stages, sm.ml, heads, w.splits, split, w.split_inv, false};
+        const bool staged = join.staged = staged_slots(heads, w.splits) <= SLOTS;
+        cluster_arrive();       // this CTA's tiles are free
+        if (!staged) cluster_wait();
+        if (done && serves) {
+            uint32_t at[2];
+            bool on[2];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int i = warp * 16 + (lane >> 2) + 8 * half;
-            if (i < heads) join.send_ml(i, half ? m1 : m0, half ? l1 : l0);
+            for (int half = 0; half < 2; ++half) {
+                const int i = quarter * 16 + (lane >> 2) + 8 * half, m = join.over_splits(i), owner = i - m * w.splits;
+                on[half] = i < heads;
+                at[half] = (staged ? stages + i * O_STRIDE : join.part(owner, m, split)) + (lane & 3) * 8;
+                if (!staged) at[half] = in_cta(at[half], owner);
+            }
+#pragma unroll 1
+            for (int c = share; c < kLatent / 32; c += QUARTER_WARPS) {
+                uint32_t v[16];
+                tmem_ld_16x32(o_at + c * 32, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    if (on[half]) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t to = at[half] + c * 128 + j * 32;
+                            if (staged)
+                                st_smem_v2(to, v[4 * j + 2 * half], v[4 * j + 2 * half + 1]);
+                            else
+                                st_cluster_v2(to, v[4 * j + 2 * half], v[4 * j + 2 * half + 1]);
+                        }
+                    }
+            }
+            tc_fence_before();
         }
-    }
-    if (w.splits > 1) {
+        if (staged) {
+            __syncthreads();
+            cluster_wait();
+            join.send(warp, AT_NT / 32, lane);
+        }
+        if (keeps) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int i = warp * 16 + (lane >> 2) + 8 * half;
+                if (i < heads) join.send_ml(i, half ? m1 : m0, half ? l1 : l0);
+            }
+        }
         cluster_arrive();
         cluster_wait();
-    } else {
-        __syncthreads();
+        join.finish<DT>(a, w, r, h0, tid, AT_NT);
     }
-    join.finish<DT>(a, w, r, h0, tid, AT_NT);
     if (tid == 0 && sm.gave_up && a.status) record_status(a.status, r, kStatusAttendTimeout);
     if (warp == MMA_WARP) tmem_free_all(tmem);
 }
@@ -717,6 +776,7 @@ AttendParts lay_out(int32_t R, int32_t H, int32_t k, bool weights, const Capacit
     AttendParts p = {};
     p.tiles = (k + TILE - 1) / TILE;
     p.splits = choose_splits((int64_t)R * ((H + HEADS - 1) / HEADS), p.tiles, cap);
+    p.split_inv = 65536u / (unsigned)p.splits + 1u;
     p.rows_per_split = (p.tiles + p.splits - 1) / p.splits * TILE;
     p.head_blocks = (H + 15) / 16;
     float *f = reinterpret_cast<float *>(ws);

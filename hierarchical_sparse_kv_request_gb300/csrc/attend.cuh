@@ -206,6 +206,7 @@ __device__ __forceinline__ float query_factor(const AttendLaunch &a, int e)
 struct AttendParts {
     int splits;             // CTAs a request's (or head tile's) rows are split over: a cluster
     int rows_per_split;
+    uint32_t split_inv;     // n / splits = n * split_inv >> 16 for n up to 64
     float *lse2;            // [R][H] log2 of the sums, for the weights
     // Base-2 scores, for the weights: [R][head_blocks][tiles] blocks of 16 heads
     // by 64 rows, each as a warp holds it: [8][32 lanes][4], where lane's four
@@ -237,6 +238,19 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t at, uint4 v)
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// A head's lse from its reference and sum.
+__device__ __forceinline__ void store_lse(const AttendLaunch &a, const AttendParts &w, int64_t rh, float m, float l)
+{
+    const float l2 = l == 0.0f ? -INFINITY : m + log2f(l);
+    if (a.lse) a.lse[rh] = l2 * kLn2;
+    if (a.weights) w.lse2[rh] = l2;
+}
+
+// What a head's O is multiplied by at the end: 1 / l, and decode8's 2^7; l is
+// normal or 0 (its largest term is at least 2^-8), and the quotient's error of
+// two steps of 2^-23 small beside out's type.
+__device__ __forceinline__ float out_factor(float l) { return l == 0.0f ? 0.0f : __fdividef(128.0f, l); }
+
 // ---- join ------------------------------------------------------------------------
 //
 // Every CTA of a cluster has, for each of its heads, a part of O and its
@@ -257,9 +271,11 @@ struct Join {
     uint32_t slots;      // shared-memory address of slot 0
     float2 *ml;          // [mine][splits] reference and sum of each part
     int heads, splits, rank;
+    uint32_t split_inv;
     bool staged;
 
-    __device__ __forceinline__ int mine() const { return (heads - rank + splits - 1) / splits; }
+    __device__ __forceinline__ int over_splits(int n) const { return (int)(n * split_inv >> 16); }
+    __device__ __forceinline__ int mine() const { return over_splits(heads - rank + splits - 1); }
     __device__ __forceinline__ uint32_t part(int owner, int m, int p) const
     {
         const int slot = !staged      ? p + m * splits
@@ -272,12 +288,12 @@ struct Join {
     // 7.9).  Every CTA's slots must be free to take them.
     __device__ __forceinline__ void send(int warp, int warps, int lane) const
     {
-#pragma unroll 1
+#pragma unroll 2
         for (int n = warp; n < heads * 2; n += warps) {       // half a head's values a warp
-            const int i = n >> 1, owner = i % splits;
+            const int i = n >> 1, m = over_splits(i), owner = i - m * splits;
             if (owner == rank) continue;
             const uint32_t off = (n & 1) * 1024 + lane * 16;
-            const uint32_t src = slots + i * O_STRIDE + off, dst = in_cta(part(owner, i / splits, rank) + off, owner);
+            const uint32_t src = slots + i * O_STRIDE + off, dst = in_cta(part(owner, m, rank) + off, owner);
             const uint4 x = ld_smem_v4(src), y = ld_smem_v4(src + 512);
             st_cluster_v4(dst, x);
             st_cluster_v4(dst + 512, y);
@@ -286,7 +302,7 @@ struct Join {
     // A head's reference and sum to its owner.
     __device__ __forceinline__ void send_ml(int i, float m, float l) const
     {
-        const int owner = i % splits;
+        const int owner = i - over_splits(i) * splits;
         st_cluster_v2(in_cta(smem_u32(&ml[i - owner + rank]), owner), __float_as_uint(m), __float_as_uint(l));
     }
     // Once all parts are here: out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p
@@ -296,27 +312,21 @@ struct Join {
     {
         const int lane = tid & 31, warp = tid >> 5;
         const int mine = this->mine();
-        // the parts' factors, a thread a part
-        int group = 1;       // threads a head
-        while (group < splits) group *= 2;
-        for (int n = tid; n < (mine * group + 31) / 32 * 32; n += threads) {
-            const int m = n / group, p = n % group;
-            const bool on = m < mine && p < splits;
-            const float2 x = on ? ml[m * splits + p] : make_float2(-INFINITY, 0.0f);
+        // the parts' factors, 16 threads a head
+        static_assert(MAX_SPLITS == 16, "");
+        if (tid < mine * 16) {
+            const uint32_t both = mine * 16 - (tid & ~31) >= 32 ? 0xffffffffu : 0xffffu;
+            const int m = tid >> 4, p = tid & 15;
+            const float2 x = p < splits ? ml[m * splits + p] : make_float2(-INFINITY, 0.0f);
             float top = x.x;
-#pragma unroll 1
-            for (int o = 1; o < group; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+            for (int o = 1; o < 16; o *= 2) top = fmaxf(top, __shfl_xor_sync(both, top, o));
             const float f = ex2(x.x - (top == -INFINITY ? 0.0f : top));
             float l = f * x.y;
-#pragma unroll 1
-            for (int o = 1; o < group; o *= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
-            if (on) ml[m * splits + p].x = l == 0.0f ? 0.0f : f * (128.0f / l);        // decode8's 2^7
-            if (on && p == 0) {
-                const int64_t rh = (int64_t)r * a.H + h0 + rank + m * splits;
-                const float l2 = l == 0.0f ? -INFINITY : top + log2f(l);
-                if (a.lse) a.lse[rh] = l2 * kLn2;
-                if (a.weights) w.lse2[rh] = l2;
-            }
+#pragma unroll
+            for (int o = 1; o < 16; o *= 2) l += __shfl_xor_sync(both, l, o);
+            if (p < splits) ml[m * splits + p].x = f * out_factor(l);
+            if (p == 0) store_lse(a, w, (int64_t)r * a.H + h0 + rank + m * splits, top, l);
         }
         __syncthreads();
         // The sums, half a head's values a warp: 32 units, two threads a unit and
@@ -327,7 +337,7 @@ struct Join {
         for (int n = warp; n < 2 * mine; n += threads / 32) {
             const int m = n >> 1, unit = (n & 1) * 8 + (lane >> 3) * 16 + (lane >> 1 & 3);     // and + 4
             float o[2][4] = {};
-#pragma unroll 2
+#pragma unroll 4
             for (int p = 0; p < splits; ++p) {
                 const uint32_t at = part(rank, m, p) + unit * 32 + (lane & 1) * 16;
                 const float f = ml[m * splits + p].x;

@@ -134,6 +134,11 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t at, uint32_t (&v)[16])
                  : "r"(at));
 }
 
+__device__ __forceinline__ void tmem_ld_16x8(uint32_t at, uint32_t (&v)[4])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];" : HS_R4(v, 0) : "r"(at));
+}
+
 __device__ __forceinline__ void tmem_st_16x8(uint32_t at, const uint32_t (&v)[4])
 {
     asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%4], {%0,%1,%2,%3};" ::HS_I4(v, 0), "r"(at) : "memory");
