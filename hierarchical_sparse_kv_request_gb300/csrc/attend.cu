@@ -60,7 +60,7 @@ constexpr int SLOTS = (STAGES * OPERAND + HEADS * 64) / O_STRIDE;
 static_assert(SLOTS >= HEADS + MAX_SPLITS - 1, "the parts that a CTA joins");
 
 struct AttendSmem {
-    uint64_t full[STAGES], empty[STAGES], scored[2], weighed[2], fetched[SOFTMAX_WARPS], queries, drained;
+    uint64_t full[STAGES], empty[STAGES], scored[2], weighed[2], fetched[SOFTMAX_WARPS], queries, drained, joined;
     uint32_t tmem;
     int gave_up;
     __align__(16) uint8_t valid[STAGES][16];   // bit b of byte n: row 4 n + b of the stage's tile is named
@@ -147,8 +147,7 @@ __device__ __forceinline__ void fetch_queries(const AttendLaunch &a, int r, int 
     if (lane == 0) {
         mbar_init(bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        fence_async_smem();
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(heads * kRowValues * 2) : "memory");
+        mbar_expect(bar, heads * kRowValues * 2);
     }
     __syncwarp();
     if (lane < heads) {
@@ -200,38 +199,43 @@ __device__ __forceinline__ void place_queries(const AttendLaunch &a, int h0, uin
     // with the sign of the scale, so that the factor of the scores is positive
     const bool neg = a.scale < 0.0f;
     const bool on[2] = {h0 + i0 < a.H, h0 + i0 + 8 < a.H};
-    // 8 columns a time.  Latent columns 8 j + 2 q and + 1 hold the even (q
-    // even) or the odd values of the eight in unit 2 j + q / 2, the order of
-    // decode8, with its 2^7; rope columns their values in order.
-    const PowerOfTwo<DT> up7[2] = {{7 - e[0], neg}, {7 - e[1], neg}};
-    const uint32_t pick = q & 1 ? 0x7632 : 0x5410;
-#pragma unroll 1
-    for (int j = share; j < kLatent / 16; j += QUARTER_WARPS) {
-        uint32_t v[4];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const uint4 x = ld_smem_v4(at + half * 8 * Q_STRIDE + unit_values(2 * j + (q >> 1)) * 2);
-            uint32_t lo = up7[half].times(__byte_perm(x.x, x.y, pick)), hi = up7[half].times(__byte_perm(x.z, x.w, pick));
-            if (DT == kBf16) {
-                const float2 y = pair_to_float<DT>(lo), z = pair_to_float<DT>(hi);
-                lo = floats_to_pair<kF16>(y.x, y.y);
-                hi = floats_to_pair<kF16>(z.x, z.y);
-            }
-            v[2 * half] = on[half] ? lo : 0u;
-            v[2 * half + 1] = on[half] ? hi : 0u;
-        }
-        tmem_st_16x8(tmem + j * 8, v);
-    }
+    // Four of the quarter's warps take 64 columns each, the fifth the rope part.
+    // Latent columns 8 j + 2 q and + 1 hold the even (q even) or the odd values
+    // of the eight in unit 2 j + q / 2, the order of decode8, with its 2^7; rope
+    // columns their values in order.
+    static_assert(QUARTER_WARPS == 5, "");
     if (share < 4) {
-        const PowerOfTwo<DT> up[2] = {{-e[0], neg}, {-e[1], neg}};
-        uint32_t v[4];
+        const PowerOfTwo<DT> up7[2] = {{7 - e[0], neg}, {7 - e[1], neg}};
+        const uint32_t pick = q & 1 ? 0x7632 : 0x5410;
+        uint32_t v[32];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const uint2 x = ld_smem_v2(at + half * 8 * Q_STRIDE + kLatent * 2 + share * 32 + q * 8);
-            v[2 * half] = on[half] ? up[half].times(x.x) : 0u;
-            v[2 * half + 1] = on[half] ? up[half].times(x.y) : 0u;
-        }
-        tmem_st_16x8(tmem + kLatent / 2 + share * 8, v);
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                // units of one block of 8 are 64 bytes apart
+                const uint4 x = ld_smem_v4(at + half * 8 * Q_STRIDE + unit_values(share * 16 + (j >> 2) * 8 + (q >> 1)) * 2 + (j & 3) * 128);
+                uint32_t lo = up7[half].times(__byte_perm(x.x, x.y, pick)), hi = up7[half].times(__byte_perm(x.z, x.w, pick));
+                if (DT == kBf16) {
+                    const float2 f = pair_to_float<DT>(lo), g = pair_to_float<DT>(hi);
+                    lo = floats_to_pair<kF16>(f.x, f.y);
+                    hi = floats_to_pair<kF16>(g.x, g.y);
+                }
+                v[4 * j + 2 * half] = on[half] ? lo : 0u;
+                v[4 * j + 2 * half + 1] = on[half] ? hi : 0u;
+            }
+        tmem_st_16x64(tmem + share * 64, v);
+    } else {
+        const PowerOfTwo<DT> up[2] = {{-e[0], neg}, {-e[1], neg}};
+        uint32_t v[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const uint2 x = ld_smem_v2(at + half * 8 * Q_STRIDE + kLatent * 2 + j * 32 + q * 8);
+                v[4 * j + 2 * half] = on[half] ? up[half].times(x.x) : 0u;
+                v[4 * j + 2 * half + 1] = on[half] ? up[half].times(x.y) : 0u;
+            }
+        tmem_st_16x32(tmem + kLatent / 2, v);
     }
     tmem_wait_st();
 }
@@ -316,6 +320,7 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
     int32_t id = -1;            // of the next eight tiles
     int bad = 0;
     const int heads = min(HEADS, a.H - h0);
+    const Join join{stages, smem_u32(&sm.joined), sm.ml, heads, w.splits, split, w.split_inv, staged_slots(heads, w.splits) <= SLOTS};
     if (decodes) {
         id = ids_at(0);
     } else if (warp < SOFTMAX_WARPS) {
@@ -332,8 +337,10 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
             }
             mbar_init(smem_u32(&sm.queries), MMA_WARP);
             mbar_init(smem_u32(&sm.drained), 1);
+            mbar_init(smem_u32(&sm.joined), 1);
             sm.gave_up = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            mbar_expect(smem_u32(&sm.joined), join.bytes());
         }
         sm.top[lane] = sm.top[lane + 32] = 0;
         __syncwarp();
@@ -582,19 +589,20 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
         __syncthreads();
     } else {
         // ---- join (see attend.cuh): O from tensor memory to where the tiles were ---
-        Join join{stages, sm.ml, heads, w.splits, split, w.split_inv, false};
-        const bool staged = join.staged = staged_slots(heads, w.splits) <= SLOTS;
-        cluster_arrive();       // this CTA's tiles are free
-        if (!staged) cluster_wait();
-        if (done && serves) {
-            uint32_t at[2];
-            bool on[2];
+        __syncwarp();
+        cluster_arrive();       // this CTA's tiles are free: the last product is done with them
+        if (!join.staged) cluster_wait();
+        if (serves) {       // (also if a wait gave up: the others wait for as many bytes)
+            uint32_t at[2], bar[2];
+            bool on[2], local[2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int i = quarter * 16 + (lane >> 2) + 8 * half, m = join.over_splits(i), owner = i - m * w.splits;
                 on[half] = i < heads;
-                at[half] = (staged ? stages + i * O_STRIDE : join.part(owner, m, split)) + (lane & 3) * 8;
-                if (!staged) at[half] = in_cta(at[half], owner);
+                local[half] = join.staged || owner == split;
+                at[half] = (join.staged ? stages + i * O_STRIDE : join.place(owner, m)) + (lane & 3) * 8;
+                if (!local[half]) at[half] = in_cta(at[half], owner);
+                bar[half] = in_cta(join.here, owner);
             }
 #pragma unroll 1
             for (int c = share; c < kLatent / 32; c += QUARTER_WARPS) {
@@ -607,17 +615,17 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const uint32_t to = at[half] + c * 128 + j * 32;
-                            if (staged)
+                            if (local[half])
                                 st_smem_v2(to, v[4 * j + 2 * half], v[4 * j + 2 * half + 1]);
                             else
-                                st_cluster_v2(to, v[4 * j + 2 * half], v[4 * j + 2 * half + 1]);
+                                send_v2(to, v[4 * j + 2 * half], v[4 * j + 2 * half + 1], bar[half]);
                         }
                     }
             }
-            tc_fence_before();
         }
-        if (staged) {
-            __syncthreads();
+        tc_fence_before();
+        __syncthreads();
+        if (join.staged) {
             cluster_wait();
             join.send(warp, AT_NT / 32, lane);
         }
@@ -628,9 +636,14 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
                 if (i < heads) join.send_ml(i, half ? m1 : m0, half ? l1 : l0);
             }
         }
+        // No CTA leaves before the others have sent it their parts, whatever
+        // has gone wrong: a part that is late is waited for once more.
         cluster_arrive();
-        cluster_wait();
+        const bool here = mbar_wait(join.here, 0, gave_up);
+        __syncthreads();
         join.finish<DT>(a, w, r, h0, tid, AT_NT);
+        cluster_wait();
+        for (int i = 0; !here && i < (1 << 20) && !mbar_try(join.here, 0); ++i) {}
     }
     if (tid == 0 && sm.gave_up && a.status) record_status(a.status, r, kStatusAttendTimeout);
     if (warp == MMA_WARP) tmem_free_all(tmem);

@@ -225,17 +225,25 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t at, int rank)
     return y;
 }
 
-__device__ __forceinline__ void st_cluster_v2(uint32_t at, uint32_t x, uint32_t y)
+// Stores to a CTA of the cluster; its mbarrier `bar` counts the bytes as they
+// arrive.
+__device__ __forceinline__ void send_v2(uint32_t at, uint32_t x, uint32_t y, uint32_t bar)
 {
-    asm volatile("st.shared::cluster.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(x), "r"(y) : "memory");
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1,%2}, [%3];" ::"r"(at), "r"(x), "r"(y),
+                 "r"(bar)
+                 : "memory");
 }
 
-__device__ __forceinline__ void st_cluster_v4(uint32_t at, uint4 v)
+__device__ __forceinline__ void send_v4(uint32_t at, uint4 v, uint32_t bar)
 {
-    asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1,%2,%3,%4}, [%5];" ::"r"(at), "r"(v.x),
+                 "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
+                 : "memory");
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// The cluster's barrier, for what has been waited for already (a release of all
+// that a CTA has written takes some 1,400 cycles).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // A head's lse from its reference and sum.
@@ -256,10 +264,12 @@ __device__ __forceinline__ float out_factor(float l) { return l == 0.0f ? 0.0f :
 // Every CTA of a cluster has, for each of its heads, a part of O and its
 // reference and sum; head i is joined by CTA i % splits, whose m-th head is its
 // rank + m splits.  Parts are slots of 512 floats in shared memory, values in
-// the columns' order (unit_values, decode8).  `staged`: a CTA's own parts are in slots 0 to heads - 1, and
-// what the others send goes behind them; else part p of head m comes to slot p
-// + m splits of its owner.
-constexpr uint32_t O_STRIDE = (kLatent + 4) * 4;     // (keeps a fragment's bank conflicts to two ways)
+// the columns' order (unit_values, decode8).  `staged`: a CTA's own parts are in
+// slots 0 to heads - 1 first, and are sent on from there (512 bytes a store, 64 KB
+// to a neighbour: 3.8 thousand cycles); else they go to their owner at once, 32
+// bytes of a row at a time, straight from fragments (7.9 thousand).  What a CTA gets from the others comes behind its own: for each
+// of its heads, one slot for each of the others, in their order.
+constexpr uint32_t O_STRIDE = (kLatent + 8) * 4;     // (no bank conflicts between a fragment's rows)
 
 // Slots that a staged join of so many heads and CTAs takes at most.
 __host__ __device__ constexpr int staged_slots(int heads, int splits)
@@ -269,41 +279,50 @@ __host__ __device__ constexpr int staged_slots(int heads, int splits)
 
 struct Join {
     uint32_t slots;      // shared-memory address of slot 0
-    float2 *ml;          // [mine][splits] reference and sum of each part
+    uint32_t here;       // its address of the mbarrier that counts what the others send
+    float2 *ml;          // [mine][splits] reference and sum of each part, the own first
     int heads, splits, rank;
     uint32_t split_inv;
     bool staged;
 
     __device__ __forceinline__ int over_splits(int n) const { return (int)(n * split_inv >> 16); }
-    __device__ __forceinline__ int mine() const { return over_splits(heads - rank + splits - 1); }
-    __device__ __forceinline__ uint32_t part(int owner, int m, int p) const
+    __device__ __forceinline__ int count(int owner) const { return over_splits(heads - owner + splits - 1); }
+    // The own part of the CTA's m-th head, and the first that another sends it.
+    __device__ __forceinline__ uint32_t own(int m) const { return slots + (staged ? rank + m * splits : m) * O_STRIDE; }
+    __device__ __forceinline__ uint32_t others(int owner, int m) const
     {
-        const int slot = !staged      ? p + m * splits
-                         : p == owner ? owner + m * splits
-                                      : heads + m * (splits - 1) + (p < owner ? p : p - 1);
-        return slots + slot * O_STRIDE;
+        return slots + ((staged ? heads : count(owner)) + m * (splits - 1)) * O_STRIDE;
     }
-    // Staged parts to their owners, 512 bytes a store (64 KB to a neighbour: 3.8
-    // thousand cycles; 32 bytes of a row at a time, straight from fragments,
-    // 7.9).  Every CTA's slots must be free to take them.
+    // Where this CTA's part of owner's m-th head goes: in owner, if that is another.
+    __device__ __forceinline__ uint32_t place(int owner, int m) const
+    {
+        return owner == rank ? own(m) : others(owner, m) + (rank - (rank > owner)) * O_STRIDE;
+    }
+    // What the others send a CTA.
+    __device__ __forceinline__ uint32_t bytes() const { return count(rank) * (splits - 1) * (kLatent * 4 + 8); }
+    // Staged parts to their owners.  Every CTA's slots must be free to take them.
     __device__ __forceinline__ void send(int warp, int warps, int lane) const
     {
 #pragma unroll 2
         for (int n = warp; n < heads * 2; n += warps) {       // half a head's values a warp
             const int i = n >> 1, m = over_splits(i), owner = i - m * splits;
             if (owner == rank) continue;
-            const uint32_t off = (n & 1) * 1024 + lane * 16;
-            const uint32_t src = slots + i * O_STRIDE + off, dst = in_cta(part(owner, m, rank) + off, owner);
+            const uint32_t off = (n & 1) * 1024 + lane * 16, bar = in_cta(here, owner);
+            const uint32_t src = slots + i * O_STRIDE + off, dst = in_cta(place(owner, m) + off, owner);
             const uint4 x = ld_smem_v4(src), y = ld_smem_v4(src + 512);
-            st_cluster_v4(dst, x);
-            st_cluster_v4(dst + 512, y);
+            send_v4(dst, x, bar);
+            send_v4(dst + 512, y, bar);
         }
     }
     // A head's reference and sum to its owner.
     __device__ __forceinline__ void send_ml(int i, float m, float l) const
     {
         const int owner = i - over_splits(i) * splits;
-        st_cluster_v2(in_cta(smem_u32(&ml[i - owner + rank]), owner), __float_as_uint(m), __float_as_uint(l));
+        if (owner == rank)
+            ml[i - owner] = make_float2(m, l);
+        else
+            send_v2(in_cta(smem_u32(&ml[i - owner + rank + (rank < owner)]), owner), __float_as_uint(m), __float_as_uint(l),
+                    in_cta(here, owner));
     }
     // Once all parts are here: out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p
     // and lse, of heads h0 + ... of request r.  The whole CTA.
@@ -311,7 +330,7 @@ struct Join {
     __device__ __forceinline__ void finish(const AttendLaunch &a, const AttendParts &w, int r, int h0, int tid, int threads) const
     {
         const int lane = tid & 31, warp = tid >> 5;
-        const int mine = this->mine();
+        const int mine = count(rank);
         // the parts' factors, 16 threads a head
         static_assert(MAX_SPLITS == 16, "");
         if (tid < mine * 16) {
@@ -336,11 +355,10 @@ struct Join {
 #pragma unroll 1
         for (int n = warp; n < 2 * mine; n += threads / 32) {
             const int m = n >> 1, unit = (n & 1) * 8 + (lane >> 3) * 16 + (lane >> 1 & 3);     // and + 4
+            const float2 *f = ml + m * splits;
+            const uint32_t off = unit * 32 + (lane & 1) * 16;
             float o[2][4] = {};
-#pragma unroll 4
-            for (int p = 0; p < splits; ++p) {
-                const uint32_t at = part(rank, m, p) + unit * 32 + (lane & 1) * 16;
-                const float f = ml[m * splits + p].x;
+            auto add = [&](uint32_t at, float f) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const uint4 x = ld_smem_v4(at + u * 128);
@@ -349,7 +367,11 @@ struct Join {
                     o[u][2] = fmaf(f, __uint_as_float(x.z), o[u][2]);
                     o[u][3] = fmaf(f, __uint_as_float(x.w), o[u][3]);
                 }
-            }
+            };
+            add(own(m) + off, f[0].x);
+            uint32_t at = others(rank, m) + off;
+#pragma unroll 3
+            for (int p = 1; p < splits; ++p, at += O_STRIDE) add(at, f[p].x);
             uint8_t *out = a.out + (int64_t)r * a.out_rs + (int64_t)(h0 + rank + m * splits) * a.out_hs +
                            unit_values(unit) * 2 + (lane & 1) * 8;
             const bool odd = lane & 1;

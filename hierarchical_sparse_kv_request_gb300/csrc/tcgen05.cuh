@@ -39,6 +39,12 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// Arrives, and `bytes` more have to come before the phase ends.
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
@@ -139,9 +145,11 @@ __device__ __forceinline__ void tmem_ld_16x8(uint32_t at, uint32_t (&v)[4])
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];" : HS_R4(v, 0) : "r"(at));
 }
 
-__device__ __forceinline__ void tmem_st_16x8(uint32_t at, const uint32_t (&v)[4])
+__device__ __forceinline__ void tmem_st_16x32(uint32_t at, const uint32_t (&v)[16])
 {
-    asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%4], {%0,%1,%2,%3};" ::HS_I4(v, 0), "r"(at) : "memory");
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::HS_I4(v, 0),
+                 HS_I4(v, 4), HS_I4(v, 8), HS_I4(v, 12), "r"(at)
+                 : "memory");
 }
 
 // ---- MMA ----------------------------------------------------------------------
