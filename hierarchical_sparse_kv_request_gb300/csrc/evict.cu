@@ -6,11 +6,19 @@
 // integer of the same order (no candidate: the largest key), held in
 // registers, slot s by thread s % NT.  The want-th smallest key T is found by
 // a radix select (digits of 11, 11 and 10 bits, a shared-memory histogram
-// each); the chosen slots are those with a key below T and the lowest slots
-// among those equal to T, which is ascending (weight, slot) without a sort.
-// Chosen and tied slots become two bitmaps in slot order (one ballot per 32
-// slots), and one block scan over their words gives every chosen slot its
-// place.
+// each, until a bin holds just the keys that are left to choose); the chosen
+// slots are those with a key below T and the lowest slots among those equal to
+// T, which is ascending (weight, slot) without a sort.  Chosen and tied slots
+// become two bitmaps in slot order (one ballot per 32 slots), and one scan over
+// their words gives every chosen slot its place.
+//
+// Bound by the gather of the weights by token, a 128-byte line of L1 a cycle
+// and SM, and, below some 10,000 slots, by the latency of the steps.  Reading all
+// of a request's weights into shared memory and gathering there was slower but
+// for the largest buffers over the shortest contexts (256 requests, 81,920
+// tokens: 16,384 slots 35 against 29.5 us, 32,768 slots 51 against 52.5).
+// Measured on GB300: 32 requests of 6,144 slots, 40,000 tokens 8.8 us, 256 of
+// 32,768 slots 53 us.
 //
 // Freeing keeps what the resolver relies on: the LRU list stays sorted by
 // (last_used, slot).  A freed slot's stamp is 0, so the new list is all
@@ -34,134 +42,172 @@ __device__ __forceinline__ uint32_t weight_key(float w)
 
 struct EvictSmem {
     uint32_t hist[2048];
-    uint32_t less[EV_NT], tied[EV_NT];   // bitmaps over slots (D <= 32 * EV_NT)
+    uint32_t less[33 * 32], tied[33 * 32];   // bitmaps over slots (D <= 32 * EV_NT)
     uint32_t pos[EV_NT];                 // output place of each word's first chosen slot
     uint32_t zero[EV_NT];                // bitmap: stamp 0 after the call
     uint32_t warp_tot[EV_NT / 32];
-    uint32_t bin, before;
+    uint32_t bin, before, in_bin;
 };
+
+__device__ __forceinline__ uint32_t warp_inclusive_scan(uint32_t x, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
+// Finds the bin of the histogram in which the need-th key lies: sm.bin, with
+// sm.before keys in the bins before it and sm.in_bin in it.  Returns the number
+// of keys; need is brought down to it.  Clears the histogram.  Begins and ends
+// with a barrier.
+__device__ __forceinline__ uint32_t find_bin(EvictSmem &sm, uint32_t &need, int tid)
+{
+    const int lane = tid & 31, warp = tid >> 5;
+    __syncthreads();
+    uint2 &mine = reinterpret_cast<uint2 *>(sm.hist)[tid];
+    const uint2 h = mine;
+    const uint32_t sum = __reduce_add_sync(0xffffffffu, h.x + h.y);
+    if (lane == 0) sm.warp_tot[warp] = sum;
+    mine = make_uint2(0, 0);
+    __syncthreads();
+    const uint32_t upto = warp_inclusive_scan(sm.warp_tot[lane], lane);
+    const uint32_t total = __shfl_sync(0xffffffffu, upto, 31);
+    need = min(need, total);
+    const uint32_t reached = __ballot_sync(0xffffffffu, upto >= need);
+    if (need > 0 && __ffs(reached) - 1 == warp) {
+        const uint32_t in = warp_inclusive_scan(h.x + h.y, lane) + __shfl_sync(0xffffffffu, upto, warp) - sum;
+        if (__ffs(__ballot_sync(0xffffffffu, in >= need)) - 1 == lane) {
+            const bool second = need > in - h.y;
+            sm.bin = 2 * tid + second;
+            sm.before = second ? in - h.y : in - h.y - h.x;
+            sm.in_bin = second ? h.y : h.x;
+        }
+    }
+    __syncthreads();
+    return total;
+}
 
 // KT: slots per thread, D <= KT * EV_NT.  FREE: with a hot state.
 template <int KT, bool FREE>
 __global__ void __launch_bounds__(EV_NT) evict_kernel(EvictLaunch a)
 {
     __shared__ EvictSmem sm;
-    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = a.D, n = a.n;
-    const int32_t S = a.seq_lens[r];
-    int32_t *out = a.out_slots ? a.out_slots + (int64_t)r * n : nullptr;
-    int want = n;
-    if (a.want) want = max(0, min(n, a.want[r]));
-
-    // keys
     const int32_t *s2t = a.slot2tok + (int64_t)r * D;
+    const int32_t S = a.seq_lens[r];
+    uint32_t key[KT];        // first its slot's token, then the token's weight
+#pragma unroll
+    for (int i = 0; i < KT; ++i) {
+        const int s = tid + i * EV_NT;
+        key[i] = s < D ? (uint32_t)s2t[s] : kNoCandidate;
+    }
+    int32_t *out = a.out_slots ? a.out_slots + (int64_t)r * n : nullptr;
+    uint32_t need = (uint32_t)max(0, a.want ? min(n, a.want[r]) : n);
+    reinterpret_cast<uint2 *>(sm.hist)[tid] = make_uint2(0, 0);
+
     const float *wt = a.weights + (int64_t)r * a.weights_stride;
-    const int64_t horizon = S > D ? min((int64_t)S - a.keep_recent, a.weights_tokens) : 0;
+    const int32_t horizon = S > D ? (int32_t)max(min((int64_t)S - a.keep_recent, a.weights_tokens), (int64_t)0) : 0;
     uint32_t thr = 0xFFFFFFFFu;
     if (FREE && a.protect_calls) {
         const uint32_t tick = a.st.tick[r];
         thr = tick >= a.protect_calls ? tick - a.protect_calls + 1u : 1u;
     }
     const uint32_t *lu = FREE ? a.st.last_used + (int64_t)r * D : nullptr;
-    uint32_t key[KT];
-    int32_t tok[KT];
-    int mine = 0;
+    uint32_t candidates = 0;     // bit i: slot i is one
 #pragma unroll
     for (int i = 0; i < KT; ++i) {
-        const int s = tid + i * EV_NT;
-        tok[i] = s < D && horizon > 0 ? s2t[s] : -1;
+        bool ok = key[i] < (uint32_t)horizon;
+        if (FREE && ok && a.protect_calls) ok = lu[tid + i * EV_NT] < thr;
+        if (ok) candidates |= 1u << i;
     }
 #pragma unroll
+    for (int i = 0; i < KT; ++i)
+        if (candidates >> i & 1u) key[i] = __float_as_uint(wt[key[i]]);
+    __syncthreads();
+#pragma unroll
     for (int i = 0; i < KT; ++i) {
-        const int s = tid + i * EV_NT;
-        key[i] = kNoCandidate;
-        bool ok = tok[i] >= 0 && tok[i] < horizon;
-        if (FREE && ok && a.protect_calls) ok = lu[s] < thr;
-        if (ok) key[i] = weight_key(wt[tok[i]]);
-        mine += ok;
+        key[i] = candidates >> i & 1u ? weight_key(__uint_as_float(key[i])) : kNoCandidate;
+        if (key[i] != kNoCandidate) atomicAdd(&sm.hist[key[i] >> 21], 1u);
     }
-    uint32_t candidates;
-    block_exclusive_scan<EV_NT>((uint32_t)mine, sm.warp_tot, candidates);
-    const int m = min(want, (int)candidates);
-    if (m <= 0) {     // the same for the whole CTA
+    find_bin(sm, need, tid);
+    const int m = (int)need;
+    if (m == 0) {     // the same for the whole CTA
         for (int i = tid; out && i < n; i += EV_NT) out[i] = -1;
         if (tid == 0 && a.out_counts) a.out_counts[r] = 0;
         return;
     }
 
-    // T = the m-th smallest key; `need` of the keys equal to T are chosen
-    uint32_t prefix = 0, mask = 0, need = (uint32_t)m;
-#pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const uint32_t digits = pass == 2 ? 1024u : 2048u;
-        for (int b = tid; b < 2048; b += EV_NT) sm.hist[b] = 0;
-        __syncthreads();
+    // Of the keys whose digits so far are T's, `need` are still to be chosen;
+    // if that is all of them, the keys up to T (its other digits all ones) are.
+    uint32_t T = sm.bin << 21;
+    need -= sm.before;
+    int digits_left = 21;
+#pragma unroll 1
+    while (sm.in_bin != need && digits_left > 0) {
+        const int shift = digits_left == 21 ? 10 : 0;
+        const uint32_t digits = (1u << (digits_left - shift)) - 1u;
 #pragma unroll
         for (int i = 0; i < KT; ++i)
-            if (key[i] != kNoCandidate && (key[i] & mask) == prefix)
-                atomicAdd(&sm.hist[(key[i] >> shift) & (digits - 1u)], 1u);
-        __syncthreads();
-        const uint32_t h0 = sm.hist[2 * tid], h1 = sm.hist[2 * tid + 1];
-        uint32_t tot;
-        const uint32_t pre = block_exclusive_scan<EV_NT>(h0 + h1, sm.warp_tot, tot);
-        if (pre < need && need <= pre + h0 + h1) {   // one thread
-            const bool second = need > pre + h0;
-            sm.bin = 2 * tid + second;
-            sm.before = pre + (second ? h0 : 0u);
-        }
-        __syncthreads();
+            if (key[i] != kNoCandidate && (key[i] ^ T) >> digits_left == 0)
+                atomicAdd(&sm.hist[key[i] >> shift & digits], 1u);
+        find_bin(sm, need, tid);
+        T |= sm.bin << shift;
         need -= sm.before;
-        prefix |= sm.bin << shift;
-        mask |= (digits - 1u) << shift;
-        __syncthreads();
+        digits_left = shift;
     }
-    const uint32_t T = prefix;
+    const bool ties = sm.in_bin != need;
+    if (!ties) T = min(T | ((1u << digits_left) - 1u), kNoCandidate - 1u);
 
     // bitmaps in slot order, and where each word's chosen slots go
-    if (tid < EV_NT) sm.less[tid] = sm.tied[tid] = 0;
-    __syncthreads();
+    // (word i * 32 + warp is at warp * 33 + i: no bank conflicts either way)
+    uint32_t less = 0, tied = 0;
 #pragma unroll
     for (int i = 0; i < KT; ++i) {
-        const uint32_t l = __ballot_sync(0xffffffffu, key[i] < T);
-        const uint32_t t = __ballot_sync(0xffffffffu, key[i] == T);
-        if (lane == 0) {
-            sm.less[i * 32 + (tid >> 5)] = l;
-            sm.tied[i * 32 + (tid >> 5)] = t;
+        const uint32_t b = __ballot_sync(0xffffffffu, ties ? key[i] < T : key[i] <= T);
+        if (lane == i) less = b;
+    }
+    if (ties) {
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+            const uint32_t b = __ballot_sync(0xffffffffu, key[i] == T);
+            if (lane == i) tied = b;
         }
     }
+    sm.less[warp * 33 + lane] = less;
+    sm.tied[warp * 33 + lane] = tied;
     __syncthreads();
     {
-        const uint32_t l = __popc(sm.less[tid]), t = __popc(sm.tied[tid]);
+        less = sm.less[lane * 33 + warp];
+        tied = sm.tied[lane * 33 + warp];
+        const uint32_t l = __popc(less), t = __popc(tied);
         uint32_t tot;
         const uint32_t pre = block_exclusive_scan<EV_NT>((t << 16) | l, sm.warp_tot, tot);
         // of the ties, the lowest `need` slots are chosen
         const uint32_t tb = min(pre >> 16, need);
-        sm.pos[tid] = (pre & 0xFFFFu) + tb;
-        uint32_t bits = sm.tied[tid], left = need - tb, keep = 0;
+        uint32_t left = need - tb, keep = 0;
         if (left >= t) {
-            keep = bits;
+            keep = tied;
         } else {
             for (; left; --left) {
-                keep |= bits & (0u - bits);
-                bits &= bits - 1u;
+                keep |= tied & (0u - tied);
+                tied &= tied - 1u;
             }
         }
-        sm.tied[tid] = sm.less[tid] | keep;       // now: the chosen slots
-    }
-    __syncthreads();
-    const uint32_t below = (1u << lane) - 1u;
-    if (out) {
-#pragma unroll
-        for (int i = 0; i < KT; ++i) {
-            const int w = i * 32 + (tid >> 5);
-            const uint32_t c = sm.tied[w];
-            if ((c >> lane) & 1u) out[sm.pos[w] + __popc(c & below)] = tid + i * EV_NT;
+        uint32_t chosen = less | keep, at = (pre & 0xFFFFu) + tb;
+        if (FREE) sm.tied[tid] = chosen;
+        if (out) {
+            for (; chosen; chosen &= chosen - 1u) out[at++] = tid * 32 + __ffs(chosen) - 1;
+            for (int i = m + tid; i < n; i += EV_NT) out[i] = -1;
         }
-        for (int i = m + tid; i < n; i += EV_NT) out[i] = -1;
     }
     if (tid == 0 && a.out_counts) a.out_counts[r] = m;
     if (!FREE) return;
+    __syncthreads();
+    const uint32_t below = (1u << lane) - 1u;
 
     // free the chosen slots; zero: the slots whose stamp is 0 afterwards
     int32_t *t2s = a.st.tok2slot + a.host_off[r];
