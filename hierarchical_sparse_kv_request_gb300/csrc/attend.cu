@@ -16,27 +16,35 @@
 // enter the second product as f16 (relative step 2^-11).
 //
 // One CTA takes up to 64 heads of one request over a range of its rows, 64
-// rows a tile, three tiles in flight:
+// rows a tile, three tiles in shared memory:
 //   warps 4-19   fetch a tile's packed rows into registers one tile ahead,
 //                decode them to f16 in shared memory (128-byte swizzle);
 //   warp 20      issues the MMAs (M = 64 heads): S = Q K^T, then O += P V of
 //                the tile before, its rows now the k dimension;
 //   warps 0-3    softmax: read S, move the reference, write P as f16 over the
 //                tile's rope part (S no longer needs it), keep l.
-// M = 64 uses 16 of the 32 lanes of each warp's part of tensor memory: O fills
+// O of 64 heads takes half of tensor memory, and with 128 heads nothing would be
+// left for S.  M = 64 uses 16 of the 32 lanes of each warp's part of it: O fills
 // the upper 16 (512 columns), S (two tiles) and the queries the lower.  With
 // the queries there, an MMA of the first product reads 2 KB of shared memory
 // in its 32 cycles instead of 4 KB, which would take all of its bandwidth and
-// leave the decoding warps none (measured: 45.9 -> XX us for 32 requests, 128
-// heads, 2,048 rows).
+// leave the decoding warps none.
 //
 // The rows of a request are split over the CTAs of a cluster when there are
 // few (request, head tile) pairs.  At the end the CTAs of a cluster share out
-// the heads: every CTA writes its part of a head's O from tensor memory into
-// the shared memory of the CTA that joins it (writes, as nothing waits for
-// them; reading took several times as long).  With weights, the scores
-// (base 2) go to the workspace and a second launch adds up each row's
-// probabilities over the heads.
+// the heads, and every CTA sends its part of a head's O to the shared memory of
+// the CTA that joins it.  With weights, the scores (base 2, 32 bits) go to the
+// workspace and a second launch adds up each row's probabilities over the heads,
+// which need the heads' final sums.
+//
+// What bounds it.  The two products of a tile take 2,176 cycles of the tensor
+// pipe; measured, a tile takes some 2,650, as shared memory serves their
+// operands (1,200 cycles), the decoded tile's stores (580) and the fetches.  A
+// CTA's start (ids, then rows; queries) takes some 11 thousand cycles to the
+// first scores, its end 9 to 11 thousand with a join, 5 without.  Measured on
+// GB300, 2,048 rows, GPU time: 32 requests of 128 heads 34 us (537 TFLOP/s), with
+// weights 43; 32 of 16 heads 21; one request of 16 heads 11; 256 requests of 64
+// heads with weights 160.
 #include <atomic>
 #include <mutex>
 
@@ -765,7 +773,9 @@ cudaError_t capacity(const Capacity **out)
 
 // How many parts the rows of `units` head tiles, `tiles` tiles each, are split
 // into, one for each CTA of a cluster: the count for which the waves of clusters
-// take the fewest tiles, counting a CTA's own start and end as kFixedTiles.
+// take the fewest tiles, counting a CTA's own start and end as kFixedTiles (some
+// 22 thousand cycles, a tile 2,650).  Measured with 8 against 3, 2,048 rows of 64
+// heads: 100 requests 53.5 against 75.6 us, 160 requests 98 against 123.
 constexpr int kFixedTiles = 8;
 
 int choose_splits(int64_t units, int tiles, const Capacity &cap)
