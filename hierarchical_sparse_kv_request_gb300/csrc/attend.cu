@@ -34,8 +34,10 @@
 // few (request, head tile) pairs.  At the end the CTAs of a cluster share out
 // the heads, and every CTA sends its part of a head's O to the shared memory of
 // the CTA that joins it.  With weights, the scores (base 2, 32 bits) go to the
-// workspace and a second launch adds up each row's probabilities over the heads,
-// which need the heads' final sums.
+// workspace, and each row's probabilities over the heads, which need the heads'
+// final sums, are added up from there: by the CTA itself where it has all heads
+// and rows of a request (256 requests of 64 heads 150 us, 158 with a launch for
+// it), else by a second launch.
 //
 // What bounds it.  The two products of a tile take 2,176 cycles of the tensor
 // pipe; measured, a tile takes some 2,650, as shared memory serves their
@@ -44,7 +46,7 @@
 // first scores, its end 9 to 11 thousand with a join, 5 without.  Measured on
 // GB300, 2,048 rows, GPU time: 32 requests of 128 heads 34 us (537 TFLOP/s), with
 // weights 43; 32 of 16 heads 21; one request of 16 heads 11; 256 requests of 64
-// heads with weights 160.
+// heads with weights 150.
 #include <atomic>
 #include <mutex>
 
@@ -248,6 +250,114 @@ __device__ __forceinline__ void place_queries(const AttendLaunch &a, int h0, uin
     tmem_wait_st();
 }
 
+// ---- weights -----------------------------------------------------------------------
+
+// weights[position] += sum over the heads of 2^(score - lse2), for eight rows a
+// warp, the j-th of tile t: it reads the j-th 512 bytes of every block of 16 heads,
+// a thread two rows by two heads at a time; then the 8 threads of a row meet,
+// always in the same order, and two of them (lane / 4 < 2) have a row each.
+struct WeightRow {
+    int32_t id, pos;      // of this thread's row in the end
+    __device__ __forceinline__ void load(const AttendLaunch &a, int r, int t, int j, int lane)
+    {
+        const int i = t * TILE + 8 * j + 2 * (lane & 3) + (lane >> 2 & 1);
+        const bool on = lane < 8 && i < a.k;
+        id = on ? a.ids[(int64_t)r * a.ids_stride + i] : -1;
+        pos = on ? a.positions[(int64_t)r * a.positions_stride + i] : -1;
+    }
+    // sum0, sum1: of rows 2 (lane % 4) and + 1 over this thread's heads
+    __device__ __forceinline__ void add(const AttendLaunch &a, int r, float sum0, float sum1, int lane) const
+    {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            sum0 += __shfl_xor_sync(0xffffffffu, sum0, o);
+            sum1 += __shfl_xor_sync(0xffffffffu, sum1, o);
+        }
+        int bad = 0;
+        if (checked_id(a, id, &bad) < 0) return;
+        if (pos >= 0 && pos < a.weights_tokens)
+            atomicAdd(a.weights + (int64_t)r * a.weights_stride + pos, lane & 4 ? sum1 : sum0);
+        else if (a.status)
+            record_status(a.status, r, kStatusBadPosition);
+    }
+};
+
+__device__ __forceinline__ void add_weight(float &sum0, float &sum1, float score0, float score1, float lse2)
+{
+    sum0 += ex2(score0 - lse2);
+    sum1 += ex2(score1 - lse2);
+}
+
+__device__ __forceinline__ const float4 *scores_at(const AttendParts &w, int r, int t, int j, int lane)
+{
+    return w.scores + ((int64_t)r * w.head_blocks * w.tiles + t) * 256 + j * 32 + lane;
+}
+
+// A CTA takes the 64 rows of a tile.  Bound by reading the scores once.
+constexpr int WT_NT = 256;
+
+__global__ void __launch_bounds__(WT_NT, 6) weights_kernel(const __grid_constant__ AttendLaunch a,
+                                                           const __grid_constant__ AttendParts w)
+{
+    const int t = blockIdx.x, r = blockIdx.y, j = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
+    WeightRow row;
+    row.load(a, r, t, j, lane);      // (inputs: they do not wait for the launch before)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float4 *s = scores_at(w, r, t, j, lane);
+    const float *lse2 = w.lse2 + (int64_t)r * a.H;
+    float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll 4
+    for (int b = 0; b < (int)w.head_blocks; ++b) {
+        const float4 x = s[(int64_t)b * w.tiles * 256];
+        const int h = b * 16 + g;
+        if (h < a.H) add_weight(sum0, sum1, x.x, x.y, lse2[h]);
+        if (h + 8 < a.H) add_weight(sum0, sum1, x.z, x.w, lse2[h + 8]);
+    }
+    row.add(a, r, sum0, sum1, lane);
+}
+
+// The same by a CTA that has all heads and rows of request r and has written
+// their scores; ml[head].y: its lse2.  The next eight rows' loads are under way
+// while a warp adds up.
+__device__ __forceinline__ void add_own_weights(const AttendLaunch &a, const AttendParts &w, int r, const float2 *ml, int warp,
+                                                int lane)
+{
+    constexpr int BLOCKS = HEADS / 16, WARPS = AT_NT / 32;
+    const int pieces = w.tiles * 8;
+    float ref[BLOCKS][2];
+#pragma unroll
+    for (int b = 0; b < BLOCKS; ++b) {
+        ref[b][0] = ml[b * 16 + (lane >> 2)].y;
+        ref[b][1] = ml[b * 16 + (lane >> 2) + 8].y;
+    }
+    float4 next[BLOCKS];
+    WeightRow next_row;
+    auto load = [&](int n) {
+        const float4 *s = scores_at(w, r, n >> 3, n & 7, lane);
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b)
+            next[b] = b < w.head_blocks ? s[(int64_t)b * w.tiles * 256] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        next_row.load(a, r, n >> 3, n & 7, lane);
+    };
+    if (warp < pieces) load(warp);
+#pragma unroll 1
+    for (int n = warp; n < pieces; n += WARPS) {
+        float4 x[BLOCKS];
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) x[b] = next[b];
+        const WeightRow row = next_row;
+        if (n + WARPS < pieces) load(n + WARPS);
+        float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) {
+            const int h = b * 16 + (lane >> 2);
+            if (h < a.H) add_weight(sum0, sum1, x[b].x, x[b].y, ref[b][0]);
+            if (h + 8 < a.H) add_weight(sum0, sum1, x[b].z, x[b].w, ref[b][1]);
+        }
+        row.add(a, r, sum0, sum1, lane);
+    }
+}
+
 // ---- out -------------------------------------------------------------------------
 
 // O of a quarter's heads times their factors (ml[head].x), from tensor memory to
@@ -300,7 +410,7 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     // this call's own next launch may be placed now; it waits for this grid
-    if (a.weights) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (a.weights && !w.whole) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     AttendSmem &sm = *reinterpret_cast<AttendSmem *>(smem + MISC_AT);
     const uint32_t stages = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -587,12 +697,14 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int i = warp * 16 + (lane >> 2) + 8 * half;
-                sm.ml[i].x = out_factor(half ? l1 : l0);
-                if (i < heads) store_lse(a, w, (int64_t)r * a.H + h0 + i, half ? m1 : m0, half ? l1 : l0);
+                const float m = half ? m1 : m0, l = half ? l1 : l0;
+                sm.ml[i] = make_float2(out_factor(l), log2_sum(m, l));
+                if (i < heads) store_lse(a, w, (int64_t)r * a.H + h0 + i, sm.ml[i].y);
             }
         }
         __syncthreads();
         if (done && serves) store_out<DT>(a, r, h0, heads, o_at, sm.ml, quarter, share, lane);
+        if (a.weights && w.whole) add_own_weights(a, w, r, sm.ml, warp, lane);
         tc_fence_before();
         __syncthreads();
     } else {
@@ -655,52 +767,6 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
     }
     if (tid == 0 && sm.gave_up && a.status) record_status(a.status, r, kStatusAttendTimeout);
     if (warp == MMA_WARP) tmem_free_all(tmem);
-}
-
-// ---- weights -----------------------------------------------------------------------
-
-// weights[position] += sum over the heads of 2^(score - lse2).  A CTA takes the
-// 64 rows of a tile, warp j eight of them: it reads the j-th 512 bytes of every
-// block of 16 heads, a thread two rows by two heads at a time; then the 8
-// threads of a row meet, always in the same order.  Bound by reading the
-// scores once.
-constexpr int WT_NT = 256;
-
-__global__ void __launch_bounds__(WT_NT) weights_kernel(const __grid_constant__ AttendLaunch a,
-                                                        const __grid_constant__ AttendParts w)
-{
-    const int t = blockIdx.x, r = blockIdx.y, j = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-    const int i = t * TILE + 8 * j + 2 * (lane & 3) + (g & 1);      // this thread's row in the end (g < 2)
-    int32_t pos = -1;
-    bool on = g < 2 && i < a.k;
-    if (on) {     // (inputs: they do not wait for the launch before)
-        int bad = 0;
-        on = checked_id(a, a.ids[(int64_t)r * a.ids_stride + i], &bad) >= 0;
-        if (on) pos = a.positions[(int64_t)r * a.positions_stride + i];
-    }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const float4 *s = w.scores + ((int64_t)r * w.head_blocks * w.tiles + t) * 256 + j * 32 + lane;
-    const float *lse2 = w.lse2 + (int64_t)r * a.H;
-    float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll 8
-    for (int b = 0; b < (int)w.head_blocks; ++b) {
-        const float4 x = s[(int64_t)b * w.tiles * 256];
-        const int h = b * 16 + g;
-        const float ref0 = h < a.H ? lse2[h] : INFINITY, ref1 = h + 8 < a.H ? lse2[h + 8] : INFINITY;
-        sum0 += ex2(x.x - ref0) + ex2(x.z - ref1);
-        sum1 += ex2(x.y - ref0) + ex2(x.w - ref1);
-    }
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-        sum0 += __shfl_xor_sync(0xffffffffu, sum0, o);
-        sum1 += __shfl_xor_sync(0xffffffffu, sum1, o);
-    }
-    if (!on) return;
-    if (pos < 0 || pos >= a.weights_tokens) {
-        if (a.status) record_status(a.status, r, kStatusBadPosition);
-        return;
-    }
-    atomicAdd(a.weights + (int64_t)r * a.weights_stride + pos, g & 1 ? sum1 : sum0);
 }
 
 // ---- host ----------------------------------------------------------------------------
@@ -802,6 +868,7 @@ AttendParts lay_out(int32_t R, int32_t H, int32_t k, bool weights, const Capacit
     p.split_inv = 65536u / (unsigned)p.splits + 1u;
     p.rows_per_split = (p.tiles + p.splits - 1) / p.splits * TILE;
     p.head_blocks = (H + 15) / 16;
+    p.whole = p.splits == 1 && H <= HEADS;
     float *f = reinterpret_cast<float *>(ws);
     int64_t n = 4;          // never empty
     p.lse2 = f + n;
@@ -836,7 +903,7 @@ cudaError_t launch_attend(const AttendLaunch &a, int64_t workspace_bytes, bool *
     const unsigned ctas = (unsigned)(a.R * ((a.H + HEADS - 1) / HEADS) * w.splits);
     cluster_launch(cfg, attr, ctas, w.splits, s);
     e = cudaLaunchKernelEx(&cfg, a.dtype == kBf16 ? attend_kernel<kBf16> : attend_kernel<kF16>, a, w);
-    if (e != cudaSuccess || !a.weights) return e;
+    if (e != cudaSuccess || !a.weights || w.whole) return e;
     cfg = {};
     cfg.gridDim = dim3((unsigned)w.tiles, (unsigned)a.R);
     cfg.blockDim = dim3(WT_NT);

@@ -215,6 +215,7 @@ struct AttendParts {
     float4 *scores;
     int64_t head_blocks;
     int tiles;
+    bool whole;             // a CTA has all of a request: it adds up the weights itself
 };
 
 // This CTA's shared-memory address `at` in CTA `rank` of the cluster.
@@ -246,10 +247,11 @@ __device__ __forceinline__ void send_v4(uint32_t at, uint4 v, uint32_t bar)
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// A head's lse from its reference and sum.
-__device__ __forceinline__ void store_lse(const AttendLaunch &a, const AttendParts &w, int64_t rh, float m, float l)
+// Log2 of a head's whole sum, from its reference and sum, and where it goes.
+__device__ __forceinline__ float log2_sum(float m, float l) { return l == 0.0f ? -INFINITY : m + log2f(l); }
+
+__device__ __forceinline__ void store_lse(const AttendLaunch &a, const AttendParts &w, int64_t rh, float l2)
 {
-    const float l2 = l == 0.0f ? -INFINITY : m + log2f(l);
     if (a.lse) a.lse[rh] = l2 * kLn2;
     if (a.weights) w.lse2[rh] = l2;
 }
@@ -345,7 +347,7 @@ struct Join {
 #pragma unroll
             for (int o = 1; o < 16; o *= 2) l += __shfl_xor_sync(both, l, o);
             if (p < splits) ml[m * splits + p].x = f * out_factor(l);
-            if (p == 0) store_lse(a, w, (int64_t)r * a.H + h0 + rank + m * splits, top, l);
+            if (p == 0) store_lse(a, w, (int64_t)r * a.H + h0 + rank + m * splits, log2_sum(top, l));
         }
         __syncthreads();
         // The sums, half a head's values a warp: 32 units, two threads a unit and
