@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -61,6 +62,7 @@ class Plan(ctypes.Structure):
 
 
 class AttendArgs(ctypes.Structure):
+    """hisparse_attend_args (attend() fills it in with struct: 0.9 -> 0.3 us)."""
     _fields_ = [("num_requests", ctypes.c_int32), ("num_heads", ctypes.c_int32),
                 ("top_k", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("q", ctypes.c_void_p), ("q_request_stride", ctypes.c_int64),
@@ -81,6 +83,9 @@ class AttendArgs(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
+_pack_attend_args = struct.Struct("@" + "".join(
+    {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_void_p: "P"}[t]
+    for _, t in AttendArgs._fields_)).pack
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -165,24 +170,31 @@ def _addr(x) -> Optional[int]:
     return x.data_ptr()
 
 
-_torch = _raw_stream = None
+_torch = _raw_stream = _device = None
 
 
 def _load_torch():
-    global _torch, _raw_stream
+    global _torch
     if _torch is None:
         import torch
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _torch = torch
     return _torch
 
 
+def _current_stream() -> int:
+    """Initialises CUDA, and leaves behind the same call without Stream and
+    Device objects where torch has it (2.9 -> 0.3 us)."""
+    global _raw_stream, _device
+    t = _torch or _load_torch()
+    stream = t.cuda.current_stream().cuda_stream
+    _device = getattr(t._C, "_cuda_getDevice", None)
+    _raw_stream = _device and getattr(t._C, "_cuda_getCurrentRawStream", None)
+    return stream
+
+
 def _stream(s) -> Optional[int]:
     if s is None:
-        t = _torch or _load_torch()
-        if _raw_stream is not None:     # the same without a Stream object (2.9 -> 0.4 us)
-            return _raw_stream(t.cuda.current_device())
-        return t.cuda.current_stream().cuda_stream
+        return _raw_stream(_device()) if _raw_stream is not None else _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -469,13 +481,13 @@ class HiSparse:
               out_slots=None, out_counts=None, stream=None) -> None:
         """hisparse_evict: free, per request, up to n (or want[r]) hot slots
         of the least accumulated weight (weights: float32 [R][tokens])."""
-        _rows_of(weights, "weights", "float32", self.R)
+        tokens, stride = _rows_of(weights, "weights", "float32", self.R)
         _ints(seq_lens, "seq_lens", (self.R,))
         _ints(want, "want", (self.R,))
         _ints(out_slots, "out_slots", (self.R, n))
         _ints(out_counts, "out_counts", (self.R,))
-        _check(self.lib.hisparse_evict(self.h, layer, _addr(weights), _row_stride(weights),
-                                       weights.shape[1], _addr(seq_lens), keep_recent, n,
+        _check(self.lib.hisparse_evict(self.h, layer, _addr(weights), stride,
+                                       tokens, _addr(seq_lens), keep_recent, n,
                                        _addr(want), _addr(out_slots), _addr(out_counts),
                                        _stream(stream)), "hisparse_evict")
 
@@ -506,16 +518,15 @@ def _dtype16(x, what: str) -> int:
     raise ValueError(f"{what} must be bfloat16 or float16, not {x.dtype}")
 
 
-def _rows_of(x, what: str, dtype: str, n: int) -> None:
-    """x is [n][...] of dtype with contiguous rows."""
-    if (x.dtype is not getattr(_torch or _load_torch(), dtype) or x.dim() != 2 or x.shape[0] != n
-            or (x.stride(1) != 1 and x.shape[1] > 1)):
-        raise ValueError(f"{what} must be {dtype} [{n}][...] with contiguous rows")
-
-
-def _row_stride(x) -> int:
-    """Elements from row to row (a single row has no stride to go by)."""
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+def _rows_of(x, what: str, dtype: str, n: int):
+    """Columns and row stride of x, which is [n][...] of dtype with contiguous
+    rows (a single row has no stride to go by)."""
+    shape = x.shape
+    if x.dtype is getattr(_torch or _load_torch(), dtype) and len(shape) == 2 and shape[0] == n:
+        stride, one = x.stride()
+        if one == 1 or shape[1] <= 1:
+            return shape[1], stride if n > 1 else shape[1]
+    raise ValueError(f"{what} must be {dtype} [{n}][...] with contiguous rows")
 
 
 def _ints(x, what: str, shape) -> None:
@@ -526,20 +537,24 @@ def _ints(x, what: str, shape) -> None:
 
 
 def _packed(rows, what: str, dims: int):
-    if (rows.dtype is not (_torch or _load_torch()).uint8 or rows.dim() != dims
-            or rows.shape[-1] != ROW4_BYTES or rows.stride(-1) != 1):
+    """Shape and strides of packed rows."""
+    shape, strides = rows.shape, rows.stride()
+    if (rows.dtype is not (_torch or _load_torch()).uint8 or len(shape) != dims
+            or shape[-1] != ROW4_BYTES or strides[-1] != 1):
         raise ValueError(f"{what} must be uint8 [...][{ROW4_BYTES}] with contiguous rows")
+    return shape, strides
 
 
 def _pack_args(values, rows):
     dt = _dtype16(values, "values")
-    if values.dim() != 2 or values.shape[1] != ROW4_VALUES or values.stride(1) != 1:
+    shape, strides = values.shape, values.stride()
+    if len(shape) != 2 or shape[1] != ROW4_VALUES or strides[1] != 1:
         raise ValueError(f"values must be [n][{ROW4_VALUES}] with contiguous rows")
-    _packed(rows, "rows", 2)
-    n = values.shape[0]
-    if rows.shape[0] != n:
+    row_shape, row_strides = _packed(rows, "rows", 2)
+    n = shape[0]
+    if row_shape[0] != n:
         raise ValueError("values and rows differ in length")
-    return dt, n, _row_stride(values), _row_stride(rows)
+    return (dt, n, strides[0], row_strides[0]) if n > 1 else (dt, n, ROW4_VALUES, ROW4_BYTES)
 
 
 def pack_rows(values, rows, stream=None) -> None:
@@ -579,54 +594,48 @@ def attend(q, rows, slot_ids, out, scale: float, lse=None, positions=None, weigh
     or None; resident_rows uint8 [n][416] for flagged ids; status int32 [R]
     or None; workspace a uint8 tensor of attend_workspace_bytes (None:
     allocated for this call)."""
-    _packed(rows, "rows", 3)
-    R, D = rows.shape[0], rows.shape[1]
-    _attend(q, rows.data_ptr(), rows.stride(1) if D > 1 else ROW4_BYTES,
-            rows.stride(0) if R > 1 else 0, R, D, slot_ids, out, scale, lse, positions, weights,
-            resident_rows, status, workspace, stream)
+    (R, D, _), (request_stride, row_stride, _) = _packed(rows, "rows", 3)
+    _attend(q, rows.data_ptr(), row_stride if D > 1 else ROW4_BYTES, request_stride if R > 1 else 0,
+            R, D, slot_ids, out, scale, lse, positions, weights, resident_rows, status, workspace,
+            stream)
 
 
 def _attend(q, rows, row_stride, request_stride, R, D, slot_ids, out, scale, lse, positions,
             weights, resident_rows, status, workspace, stream) -> None:
     dt = _dtype16(q, "q")
-    if q.dim() != 3 or q.shape[0] != R or q.shape[2] != ROW4_VALUES or q.stride(2) != 1:
+    shape, strides = q.shape, q.stride()
+    if len(shape) != 3 or shape[0] != R or shape[2] != ROW4_VALUES or strides[2] != 1:
         raise ValueError(f"q must be [{R}][H][{ROW4_VALUES}] with contiguous heads")
-    H = q.shape[1]
-    if out.dtype is not q.dtype or out.shape != (R, H, ROW4_LATENT) or out.stride(2) != 1:
+    H = shape[1]
+    out_strides = out.stride()
+    if out.dtype is not q.dtype or out.shape != (R, H, ROW4_LATENT) or out_strides[2] != 1:
         raise ValueError(f"out must be [{R}][{H}][{ROW4_LATENT}] of q's type with contiguous heads")
-    _rows_of(slot_ids, "slot_ids", "int32", R)
-    k = slot_ids.shape[1]
+    k, ids_stride = _rows_of(slot_ids, "slot_ids", "int32", R)
     if lse is not None and (lse.dtype is not _torch.float32 or lse.shape != (R, H)
                             or not lse.is_contiguous()):
         raise ValueError(f"lse must be a contiguous float32 tensor of shape ({R}, {H})")
-    a = AttendArgs()
+    resident = (0, 0, 0)
+    if resident_rows is not None:
+        (count, _), (stride, _) = _packed(resident_rows, "resident_rows", 2)
+        resident = (resident_rows.data_ptr(), stride if count > 1 else ROW4_BYTES, count)
+    acc, where = (0, 0, 0), (0, 0)
     if weights is not None:
-        _rows_of(weights, "weights", "float32", R)
+        tokens, stride = _rows_of(weights, "weights", "float32", R)
         if positions is None:
             raise ValueError("weights need positions")
-        _rows_of(positions, "positions", "int32", R)
-        if positions.shape[1] != k:
+        columns, positions_stride = _rows_of(positions, "positions", "int32", R)
+        if columns != k:
             raise ValueError("positions and slot_ids differ in length")
-        a.weights, a.positions = weights.data_ptr(), positions.data_ptr()
-        a.weights_stride, a.weights_tokens = _row_stride(weights), weights.shape[1]
-        a.positions_stride = _row_stride(positions)
-    if resident_rows is not None:
-        _packed(resident_rows, "resident_rows", 2)
-        a.resident_rows = resident_rows.data_ptr()
-        a.resident_count = resident_rows.shape[0]
-        a.resident_stride = resident_rows.stride(0) if a.resident_count > 1 else ROW4_BYTES
+        acc, where = (weights.data_ptr(), stride, tokens), (positions.data_ptr(), positions_stride)
     if workspace is None:
         workspace = _torch.empty(attend_workspace_bytes(R, H, k, weights is not None),
-                                dtype=_torch.uint8, device=q.device)
-    a.num_requests, a.num_heads, a.top_k, a.dtype = R, H, k, dt
-    a.q, a.q_request_stride, a.q_head_stride = q.data_ptr(), q.stride(0), q.stride(1)
-    a.rows, a.row_stride, a.request_stride, a.rows_per_request = rows, row_stride, request_stride, D
-    a.scale = scale
-    a.slot_ids, a.ids_stride = slot_ids.data_ptr(), _row_stride(slot_ids)
-    a.out, a.out_request_stride, a.out_head_stride = out.data_ptr(), out.stride(0), out.stride(1)
-    a.lse, a.status = _addr(lse), _addr(status)
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check((_lib or load_library()).hisparse_attend(ctypes.byref(a), _stream(stream)), "hisparse_attend")
+                                 dtype=_torch.uint8, device=q.device)
+    args = _pack_attend_args(
+        R, H, k, dt, q.data_ptr(), strides[0], strides[1], rows, row_stride, request_stride, D, scale,
+        slot_ids.data_ptr(), ids_stride, *resident, out.data_ptr(), out_strides[0], out_strides[1],
+        _addr(lse) or 0, *acc, *where, _addr(status) or 0, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size())
+    _check((_lib or load_library()).hisparse_attend(args, _stream(stream)), "hisparse_attend")
 
 
 def evict_select(weights, slot2tok, seq_lens, out_slots, out_counts, keep_recent: int = 0,
@@ -635,7 +644,7 @@ def evict_select(weights, slot2tok, seq_lens, out_slots, out_counts, keep_recent
     (out_slots int32 [R][n], ascending, -1 behind them; out_counts int32 [R])
     of slot2tok int32 [R][D]; weights float32 [R][tokens]."""
     R, D = slot2tok.shape
-    _rows_of(weights, "weights", "float32", R)
+    tokens, stride = _rows_of(weights, "weights", "float32", R)
     _ints(slot2tok, "slot2tok", (R, D))
     _ints(seq_lens, "seq_lens", (R,))
     n = out_slots.shape[1]
@@ -643,7 +652,7 @@ def evict_select(weights, slot2tok, seq_lens, out_slots, out_counts, keep_recent
     _ints(out_counts, "out_counts", (R,))
     _ints(want, "want", (R,))
     _check((_lib or load_library()).hisparse_evict_select(
-        R, D, weights.data_ptr(), _row_stride(weights), weights.shape[1], slot2tok.data_ptr(),
+        R, D, weights.data_ptr(), stride, tokens, slot2tok.data_ptr(),
         seq_lens.data_ptr(), keep_recent, n, _addr(want), out_slots.data_ptr(),
         out_counts.data_ptr(), _stream(stream)), "hisparse_evict_select")
 
