@@ -414,11 +414,8 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
     AttendSmem &sm = *reinterpret_cast<AttendSmem *>(smem + MISC_AT);
     const uint32_t stages = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int head_tiles = (a.H + HEADS - 1) / HEADS;
-    const int split = blockIdx.x % w.splits;          // the CTA's rank in its cluster
-    const int ht = (blockIdx.x / w.splits) % head_tiles;
-    const int r = blockIdx.x / w.splits / head_tiles;
-    const int h0 = ht * HEADS;
+    const int split = blockIdx.x;        // the CTA's rank in its cluster
+    const int h0 = blockIdx.y * HEADS, r = blockIdx.z;
     const int k0 = split * w.rows_per_split;
     const int rows = min(a.k - k0, w.rows_per_split);
     const int tiles = (rows + TILE - 1) / TILE;
@@ -725,16 +722,16 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
                 bar[half] = in_cta(join.here, owner);
             }
 #pragma unroll 1
-            for (int c = share; c < kLatent / 32; c += QUARTER_WARPS) {
-                uint32_t v[16];
-                tmem_ld_16x32(o_at + c * 32, v);
+            for (int c = share; c < kLatent / 64; c += QUARTER_WARPS) {
+                uint32_t v[32];
+                tmem_ld_16x64(o_at + c * 64, v);
                 tmem_wait_ld();
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
                     if (on[half]) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t to = at[half] + c * 128 + j * 32;
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t to = at[half] + c * 256 + j * 32;
                             if (local[half])
                                 st_smem_v2(to, v[4 * j + 2 * half], v[4 * j + 2 * half + 1]);
                             else
@@ -776,15 +773,16 @@ struct Capacity {
     int clusters[MAX_SPLITS + 1];
 };
 
-void cluster_launch(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &attr, unsigned ctas, int splits, cudaStream_t s)
+// grid.x: the CTAs of a cluster
+void cluster_launch(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &attr, dim3 grid, cudaStream_t s)
 {
     cfg = {};
-    cfg.gridDim = dim3(ctas);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(AT_NT);
     cfg.dynamicSmemBytes = AT_SMEM;
     cfg.stream = s;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)splits;
+    attr.val.clusterDim.x = grid.x;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
@@ -800,7 +798,7 @@ cudaError_t prepare(Kernel kernel, Capacity *cap)
     for (int c = 1; e == cudaSuccess && c <= MAX_SPLITS; ++c) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr;
-        cluster_launch(cfg, attr, c, c, nullptr);
+        cluster_launch(cfg, attr, dim3(c), nullptr);
         int n = 0;
         if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
             cudaGetLastError();
@@ -900,8 +898,7 @@ cudaError_t launch_attend(const AttendLaunch &a, int64_t workspace_bytes, bool *
     if (*too_small) return cudaSuccess;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr;
-    const unsigned ctas = (unsigned)(a.R * ((a.H + HEADS - 1) / HEADS) * w.splits);
-    cluster_launch(cfg, attr, ctas, w.splits, s);
+    cluster_launch(cfg, attr, dim3(w.splits, (a.H + HEADS - 1) / HEADS, a.R), s);
     e = cudaLaunchKernelEx(&cfg, a.dtype == kBf16 ? attend_kernel<kBf16> : attend_kernel<kF16>, a, w);
     if (e != cudaSuccess || !a.weights || w.whole) return e;
     cfg = {};
