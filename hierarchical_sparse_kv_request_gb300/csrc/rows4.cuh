@@ -41,9 +41,9 @@ __device__ __forceinline__ __half2 scale_half2(uint32_t e4m3)
 }
 
 cudaError_t launch_pack_rows(const void *values, int64_t value_stride, int32_t dtype, int64_t n,
-                             void *rows, int64_t row_stride, int num_sms, cudaStream_t s);
+                             void *rows, int64_t row_stride, cudaStream_t s);
 cudaError_t launch_unpack_rows(const void *rows, int64_t row_stride, int64_t n, void *values,
-                               int64_t value_stride, int32_t dtype, int num_sms, cudaStream_t s);
+                               int64_t value_stride, int32_t dtype, cudaStream_t s);
 
 // Arguments of the attention kernels (see hisparse_attend_args).
 struct AttendLaunch {

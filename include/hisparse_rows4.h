@@ -47,6 +47,9 @@ extern "C" {
  * ran out (not expected; the request's outputs are not valid). */
 #define HISPARSE_STATUS_ATTEND_TIMEOUT 9
 
+/* Most rows of one hisparse_pack_rows or hisparse_unpack_rows. */
+#define HISPARSE_MAX_PACKED_ROWS (4 * (int64_t)0x7FFFFFFF)
+
 /* Limits of hisparse_attend; top_k is at most HISPARSE_MAX_TOP_K. */
 #define HISPARSE_MAX_HEADS 1024
 
@@ -62,8 +65,9 @@ extern "C" {
  * ties to the even code, at most 6 in magnitude; 0 where the scale is 0.
  * Infinities clip to 6 * 448; a NaN makes its group's scale NaN, and with it
  * the group's values.  The sign bit of a code is the value's, also at 0.
- * Errors: INVALID_ARG (null, n < 0, a short or odd stride, dtype),
- * ALIGNMENT (pointers not 16-byte aligned), CUDA.  n = 0 does nothing.
+ * Errors: INVALID_ARG (null, n < 0, a short or odd stride, dtype), UNSUPPORTED
+ * (n > HISPARSE_MAX_PACKED_ROWS), ALIGNMENT (pointers not 16-byte aligned),
+ * CUDA.  n = 0 does nothing.
  */
 int hisparse_pack_rows(const void *values, int64_t value_stride, int32_t dtype, int64_t n,
                        void *rows, int64_t row_stride, void *stream);

@@ -40,6 +40,12 @@ def test_pack_and_unpack_refuse(lib, args, code):
     assert lib.hisparse_unpack_rows(r, rs, n, v, vs, dt, None) == code
 
 
+def test_more_rows_than_a_launch_takes(lib):
+    n = 4 * 0x7FFFFFFF + 1
+    assert lib.hisparse_pack_rows(A, 576, 0, n, A, 416, None) == H.ERR_UNSUPPORTED
+    assert lib.hisparse_unpack_rows(A, 416, n, A, 576, 0, None) == H.ERR_UNSUPPORTED
+
+
 def test_nothing_to_pack_is_ok(lib):
     assert lib.hisparse_pack_rows(None, 576, 0, 0, None, 416, None) == H.OK
     assert lib.hisparse_unpack_rows(None, 416, 0, None, 576, 1, None) == H.OK
