@@ -70,7 +70,7 @@ constexpr int SLOTS = (STAGES * OPERAND + HEADS * 64) / O_STRIDE;
 static_assert(SLOTS >= HEADS + MAX_SPLITS - 1, "the parts that a CTA joins");
 
 struct AttendSmem {
-    uint64_t full[STAGES], empty[STAGES], scored[2], weighed[2], fetched[SOFTMAX_WARPS], queries, drained, joined;
+    uint64_t full[STAGES], empty[STAGES], scored[2], weighed[2], fetched[SOFTMAX_WARPS], queries, drained, known, joined;
     uint32_t tmem;
     int gave_up;
     __align__(16) uint8_t valid[STAGES][16];   // bit b of byte n: row 4 n + b of the stage's tile is named
@@ -194,21 +194,21 @@ __device__ __forceinline__ void measure_queries(uint32_t src, uint32_t *top, int
 }
 
 template <int DT>
-__device__ __forceinline__ void place_queries(const AttendLaunch &a, int h0, uint32_t src, uint32_t tmem, const uint32_t *top,
+__device__ __forceinline__ void place_queries(const AttendLaunch &a, int heads, uint32_t src, uint32_t tmem, const uint32_t *top,
                                               float *factor, int quarter, int share, int lane)
 {
     const int q = lane & 3, i0 = quarter * 16 + (lane >> 2);
-    const uint32_t at = src + i0 * Q_STRIDE;
+    uint32_t at[2];
     int e[2];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        const int i = i0 + 8 * half;
+        const int i = min(i0 + 8 * half, heads - 1);      // (no head: the last one once more)
+        at[half] = src + i * Q_STRIDE;
         e[half] = query_exponent<DT>(top[i]);
-        if (q == 0 && share == 0) factor[i] = query_factor(a, e[half]);
+        if (q == 0 && share == 0) factor[i0 + 8 * half] = query_factor(a, e[half]);
     }
     // with the sign of the scale, so that the factor of the scores is positive
     const bool neg = a.scale < 0.0f;
-    const bool on[2] = {h0 + i0 < a.H, h0 + i0 + 8 < a.H};
     // Four of the quarter's warps take 64 columns each, the fifth the rope part.
     // Latent columns 8 j + 2 q and + 1 hold the even (q even) or the odd values
     // of the eight in unit 2 j + q / 2, the order of decode8, with its 2^7; rope
@@ -223,15 +223,15 @@ __device__ __forceinline__ void place_queries(const AttendLaunch &a, int h0, uin
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 // units of one block of 8 are 64 bytes apart
-                const uint4 x = ld_smem_v4(at + half * 8 * Q_STRIDE + unit_values(share * 16 + (j >> 2) * 8 + (q >> 1)) * 2 + (j & 3) * 128);
+                const uint4 x = ld_smem_v4(at[half] + unit_values(share * 16 + (j >> 2) * 8 + (q >> 1)) * 2 + (j & 3) * 128);
                 uint32_t lo = up7[half].times(__byte_perm(x.x, x.y, pick)), hi = up7[half].times(__byte_perm(x.z, x.w, pick));
                 if (DT == kBf16) {
                     const float2 f = pair_to_float<DT>(lo), g = pair_to_float<DT>(hi);
                     lo = floats_to_pair<kF16>(f.x, f.y);
                     hi = floats_to_pair<kF16>(g.x, g.y);
                 }
-                v[4 * j + 2 * half] = on[half] ? lo : 0u;
-                v[4 * j + 2 * half + 1] = on[half] ? hi : 0u;
+                v[4 * j + 2 * half] = lo;
+                v[4 * j + 2 * half + 1] = hi;
             }
         tmem_st_16x64(tmem + share * 64, v);
     } else {
@@ -241,9 +241,9 @@ __device__ __forceinline__ void place_queries(const AttendLaunch &a, int h0, uin
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const uint2 x = ld_smem_v2(at + half * 8 * Q_STRIDE + kLatent * 2 + j * 32 + q * 8);
-                v[4 * j + 2 * half] = on[half] ? up[half].times(x.x) : 0u;
-                v[4 * j + 2 * half + 1] = on[half] ? up[half].times(x.y) : 0u;
+                const uint2 x = ld_smem_v2(at[half] + kLatent * 2 + j * 32 + q * 8);
+                v[4 * j + 2 * half] = up[half].times(x.x);
+                v[4 * j + 2 * half + 1] = up[half].times(x.y);
             }
         tmem_st_16x32(tmem + kLatent / 2, v);
     }
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
     int32_t id = -1;            // of the next eight tiles
     int bad = 0;
     const int heads = min(HEADS, a.H - h0);
-    const Join join{stages, smem_u32(&sm.joined), sm.ml, heads, w.splits, split, w.split_inv, staged_slots(heads, w.splits) <= SLOTS};
+    const Join join{stages, smem_u32(&sm.known), smem_u32(&sm.joined), sm.ml, heads, w.splits, split, w.split_inv, staged_slots(heads, w.splits) <= SLOTS};
     if (decodes) {
         id = ids_at(0);
     } else if (warp < SOFTMAX_WARPS) {
@@ -452,10 +452,12 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
             }
             mbar_init(smem_u32(&sm.queries), MMA_WARP);
             mbar_init(smem_u32(&sm.drained), 1);
+            mbar_init(smem_u32(&sm.known), 1);
             mbar_init(smem_u32(&sm.joined), 1);
             sm.gave_up = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-            mbar_expect(smem_u32(&sm.joined), join.bytes());
+            mbar_expect(smem_u32(&sm.known), join.parts() * 8);
+            mbar_expect(smem_u32(&sm.joined), join.parts() * kLatent * 4);
         }
         sm.top[lane] = sm.top[lane + 32] = 0;
         __syncwarp();
@@ -464,6 +466,7 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (w.splits > 1) cluster_arrive();       // its mbarriers are there
     const uint32_t tmem = sm.tmem;
     volatile int *gave_up = &sm.gave_up;
     auto all = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
@@ -492,7 +495,7 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
         // (the rows of a quarter without heads stay as they are: what they give
         // stays in that quarter)
         if (serves)
-            place_queries<DT>(a, h0, stages + Q_AT, tmem + ((uint32_t)(quarter * 32) << 16) + TMEM_Q, sm.top, sm.factor,
+            place_queries<DT>(a, heads, stages + Q_AT, tmem + ((uint32_t)(quarter * 32) << 16) + TMEM_Q, sm.top, sm.factor,
                               quarter, share, lane);
         tc_fence_before();
         __syncwarp();
@@ -683,11 +686,22 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
         l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
     }
 
+    const bool keeps = warp < SOFTMAX_WARPS && (lane & 3) == 0;      // a thread with references and sums
+    if (w.splits > 1) {
+        cluster_wait();
+        if (keeps) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int i = warp * 16 + (lane >> 2) + 8 * half;
+                if (i < heads) join.send_ml(i, half ? m1 : m0, half ? l1 : l0);
+            }
+        }
+        __syncwarp();
+    }
     const int last = tiles - 1;
     const bool done = all(mbar_wait(smem_u32(&sm.empty[last % STAGES]), (last / STAGES) & 1, gave_up));
     tc_fence_after();
     const uint32_t o_at = tmem + ((uint32_t)(quarter * 32) << 16) + TMEM_UPPER;
-    const bool keeps = warp < SOFTMAX_WARPS && (lane & 3) == 0;      // a thread with references and sums
     if (w.splits == 1) {
         // ---- out from tensor memory ------------------------------------------------
         if (keeps) {
@@ -706,7 +720,6 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
         __syncthreads();
     } else {
         // ---- join (see attend.cuh): O from tensor memory to where the tiles were ---
-        __syncwarp();
         cluster_arrive();       // this CTA's tiles are free: the last product is done with them
         if (!join.staged) cluster_wait();
         if (serves) {       // (also if a wait gave up: the others wait for as many bytes)
@@ -719,7 +732,7 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
                 local[half] = join.staged || owner == split;
                 at[half] = (join.staged ? stages + i * O_STRIDE : join.place(owner, m)) + (lane & 3) * 8;
                 if (!local[half]) at[half] = in_cta(at[half], owner);
-                bar[half] = in_cta(join.here, owner);
+                bar[half] = in_cta(join.joined, owner);
             }
 #pragma unroll 1
             for (int c = share; c < kLatent / 64; c += QUARTER_WARPS) {
@@ -746,21 +759,22 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
             cluster_wait();
             join.send(warp, AT_NT / 32, lane);
         }
-        if (keeps) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int i = warp * 16 + (lane >> 2) + 8 * half;
-                if (i < heads) join.send_ml(i, half ? m1 : m0, half ? l1 : l0);
-            }
-        }
         // No CTA leaves before the others have sent it their parts, whatever
         // has gone wrong: a part that is late is waited for once more.
         cluster_arrive();
-        const bool here = mbar_wait(join.here, 0, gave_up);
+        bool here = true;
+        if (warp * 32 < join.count(split) * 16) {
+            here = mbar_wait(join.known, 0, gave_up);
+            join.factors(a, w, (int64_t)r * a.H + h0, tid);
+        }
+        here = mbar_wait(join.joined, 0, gave_up) && here;
         __syncthreads();
-        join.finish<DT>(a, w, r, h0, tid, AT_NT);
+        if (join.count(split) * 4 <= AT_NT / 32)
+            join.finish<DT, 1>(a, r, h0, warp, AT_NT / 32, lane);
+        else
+            join.finish<DT, 4>(a, r, h0, warp, AT_NT / 32, lane);
         cluster_wait();
-        for (int i = 0; !here && i < (1 << 20) && !mbar_try(join.here, 0); ++i) {}
+        for (int i = 0; !here && i < (1 << 20) && !(mbar_try(join.known, 0) && mbar_try(join.joined, 0)); ++i) {}
     }
     if (tid == 0 && sm.gave_up && a.status) record_status(a.status, r, kStatusAttendTimeout);
     if (warp == MMA_WARP) tmem_free_all(tmem);

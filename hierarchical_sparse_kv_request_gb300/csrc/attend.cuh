@@ -281,7 +281,8 @@ __host__ __device__ constexpr int staged_slots(int heads, int splits)
 
 struct Join {
     uint32_t slots;      // shared-memory address of slot 0
-    uint32_t here;       // its address of the mbarrier that counts what the others send
+    uint32_t known, joined;     // and of the mbarriers that count what the others send: references
+                                // and sums, parts of O
     float2 *ml;          // [mine][splits] reference and sum of each part, the own first
     int heads, splits, rank;
     uint32_t split_inv;
@@ -301,7 +302,7 @@ struct Join {
         return owner == rank ? own(m) : others(owner, m) + (rank - (rank > owner)) * O_STRIDE;
     }
     // What the others send a CTA.
-    __device__ __forceinline__ uint32_t bytes() const { return count(rank) * (splits - 1) * (kLatent * 4 + 8); }
+    __device__ __forceinline__ uint32_t parts() const { return count(rank) * (splits - 1); }
     // Staged parts to their owners.  Every CTA's slots must be free to take them.
     __device__ __forceinline__ void send(int warp, int warps, int lane) const
     {
@@ -309,7 +310,7 @@ struct Join {
         for (int n = warp; n < heads * 2; n += warps) {       // half a head's values a warp
             const int i = n >> 1, m = over_splits(i), owner = i - m * splits;
             if (owner == rank) continue;
-            const uint32_t off = (n & 1) * 1024 + lane * 16, bar = in_cta(here, owner);
+            const uint32_t off = (n & 1) * 1024 + lane * 16, bar = in_cta(joined, owner);
             const uint32_t src = slots + i * O_STRIDE + off, dst = in_cta(place(owner, m) + off, owner);
             const uint4 x = ld_smem_v4(src), y = ld_smem_v4(src + 512);
             send_v4(dst, x, bar);
@@ -324,46 +325,46 @@ struct Join {
             ml[i - owner] = make_float2(m, l);
         else
             send_v2(in_cta(smem_u32(&ml[i - owner + rank + (rank < owner)]), owner), __float_as_uint(m), __float_as_uint(l),
-                    in_cta(here, owner));
+                    in_cta(known, owner));
     }
-    // Once all parts are here: out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p
-    // and lse, of heads h0 + ... of request r.  The whole CTA.
-    template <int DT>
-    __device__ __forceinline__ void finish(const AttendLaunch &a, const AttendParts &w, int r, int h0, int tid, int threads) const
+    // Once all references and sums are here: each part's factor 2^(m_p - m) / sum_p
+    // 2^(m_p - m) l_p, and lse, of heads rh + ...; 16 threads a head.
+    __device__ __forceinline__ void factors(const AttendLaunch &a, const AttendParts &w, int64_t rh, int tid) const
     {
-        const int lane = tid & 31, warp = tid >> 5;
-        const int mine = count(rank);
-        // the parts' factors, 16 threads a head
         static_assert(MAX_SPLITS == 16, "");
-        if (tid < mine * 16) {
-            const uint32_t both = mine * 16 - (tid & ~31) >= 32 ? 0xffffffffu : 0xffffu;
-            const int m = tid >> 4, p = tid & 15;
-            const float2 x = p < splits ? ml[m * splits + p] : make_float2(-INFINITY, 0.0f);
-            float top = x.x;
+        const int m = tid >> 4, p = tid & 15;
+        const bool on = m < count(rank);
+        const float2 x = on && p < splits ? ml[m * splits + p] : make_float2(-INFINITY, 0.0f);
+        float top = x.x;
 #pragma unroll
-            for (int o = 1; o < 16; o *= 2) top = fmaxf(top, __shfl_xor_sync(both, top, o));
-            const float f = ex2(x.x - (top == -INFINITY ? 0.0f : top));
-            float l = f * x.y;
+        for (int o = 1; o < 16; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float f = ex2(x.x - (top == -INFINITY ? 0.0f : top));
+        float l = f * x.y;
 #pragma unroll
-            for (int o = 1; o < 16; o *= 2) l += __shfl_xor_sync(both, l, o);
-            if (p < splits) ml[m * splits + p].x = f * out_factor(l);
-            if (p == 0) store_lse(a, w, (int64_t)r * a.H + h0 + rank + m * splits, log2_sum(top, l));
-        }
-        __syncthreads();
-        // The sums, half a head's values a warp: 32 units, two threads a unit and
-        // 16 units at a time, whose values are 256 neighbours of out.  Of eight
-        // values the even are in one 16-byte piece and the odd in the next, here
-        // in neighbouring lanes.
+        for (int o = 1; o < 16; o *= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (on && p < splits) ml[m * splits + p].x = f * out_factor(l);
+        if (on && p == 0) store_lse(a, w, rh + rank + m * splits, log2_sum(top, l));
+    }
+    // Once all parts are here too, their sums.  A warp takes U quarters of a head's
+    // values at a time (1 of few heads, 4 of many: 33.7 against 34.4 us for 32
+    // heads a CTA), two threads a unit, whose values are 128 neighbours of out a
+    // quarter.  Of eight values the even are in one 16-byte piece and the odd in
+    // the next, here in neighbouring lanes.
+    template <int DT, int U>
+    __device__ __forceinline__ void finish(const AttendLaunch &a, int r, int h0, int warp, int warps, int lane) const
+    {
+        const int mine = count(rank);
 #pragma unroll 1
-        for (int n = warp; n < 2 * mine; n += threads / 32) {
-            const int m = n >> 1, unit = (n & 1) * 8 + (lane >> 3) * 16 + (lane >> 1 & 3);     // and + 4
+        for (int n = warp * U; n < 4 * mine; n += warps * U) {
+            const int m = n >> 2, unit0 = (lane >> 3) * 16 + (lane >> 1 & 3);
+            auto unit = [&](int u) { return unit0 + ((n + u) & 1) * 8 + ((n + u) >> 1 & 1) * 4; };
             const float2 *f = ml + m * splits;
-            const uint32_t off = unit * 32 + (lane & 1) * 16;
-            float o[2][4] = {};
+            const uint32_t off = (lane & 1) * 16;
+            float o[U][4] = {};
             auto add = [&](uint32_t at, float f) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint4 x = ld_smem_v4(at + u * 128);
+                for (int u = 0; u < U; ++u) {
+                    const uint4 x = ld_smem_v4(at + unit(u) * 32);
                     o[u][0] = fmaf(f, __uint_as_float(x.x), o[u][0]);
                     o[u][1] = fmaf(f, __uint_as_float(x.y), o[u][1]);
                     o[u][2] = fmaf(f, __uint_as_float(x.z), o[u][2]);
@@ -372,17 +373,16 @@ struct Join {
             };
             add(own(m) + off, f[0].x);
             uint32_t at = others(rank, m) + off;
-#pragma unroll 3
+#pragma unroll (U == 1 ? 3 : 1)
             for (int p = 1; p < splits; ++p, at += O_STRIDE) add(at, f[p].x);
-            uint8_t *out = a.out + (int64_t)r * a.out_rs + (int64_t)(h0 + rank + m * splits) * a.out_hs +
-                           unit_values(unit) * 2 + (lane & 1) * 8;
+            uint8_t *out = a.out + (int64_t)r * a.out_rs + (int64_t)(h0 + rank + m * splits) * a.out_hs;
             const bool odd = lane & 1;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < U; ++u) {
                 // even lane: values 0-3 of its eight; odd lane: 4-7
                 const float g0 = __shfl_xor_sync(0xffffffffu, odd ? o[u][0] : o[u][2], 1);
                 const float g1 = __shfl_xor_sync(0xffffffffu, odd ? o[u][1] : o[u][3], 1);
-                *reinterpret_cast<uint2 *>(out + u * 256) =
+                *reinterpret_cast<uint2 *>(out + unit_values(unit(u)) * 2 + odd * 8) =
                     odd ? make_uint2(floats_to_pair<DT>(g0, o[u][2]), floats_to_pair<DT>(g1, o[u][3]))
                         : make_uint2(floats_to_pair<DT>(o[u][0], g0), floats_to_pair<DT>(o[u][1], g1));
             }
