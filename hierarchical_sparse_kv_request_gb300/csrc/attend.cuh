@@ -346,8 +346,8 @@ struct Join {
         if (on && p == 0) store_lse(a, w, rh + rank + m * splits, log2_sum(top, l));
     }
     // Once all parts are here too, their sums.  A warp takes U quarters of a head's
-    // values at a time (1 of few heads, 4 of many: 33.7 against 34.4 us for 32
-    // heads a CTA), two threads a unit, whose values are 128 neighbours of out a
+    // values at a time (1 of few heads, 4 of many: 33.0 against 34.4 us for 32
+    // requests of 128 heads, where a CTA has 32), two threads a unit, whose values are 128 neighbours of out a
     // quarter.  Of eight values the even are in one 16-byte piece and the odd in
     // the next, here in neighbouring lanes.
     template <int DT, int U>

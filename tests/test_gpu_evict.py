@@ -81,6 +81,24 @@ def test_select_large(D):
     check(w, tok, seq, D // 2, 100)
 
 
+@pytest.mark.parametrize("kind", ["random", "ties", "equal", "zero", "odd", "last digit"])
+@pytest.mark.parametrize("D", [8193, 16384, 16385, 24000])
+def test_select_where_two_ctas_share_a_request(D, kind):
+    w, tok, seq = state(2, D, 2 * D + 50, D, kind)
+    seq[1] = D if kind == "odd" else seq[1]      # nothing to choose there
+    for n in (1, D // 5, D):
+        check(w, tok, seq, n, D // 10)
+
+
+def test_select_large_in_more_requests_than_pairs():
+    w, tok, seq = state(100, 9000, 20000, 3, "ties")
+    check(w, tok, seq, 2000, 50)
+
+
+def test_evict_frees_in_a_large_buffer():
+    test_evict_frees_and_the_resolver_goes_on(9000, 700, [20000, 9500], 0)
+
+
 def test_short_requests_recent_tokens_and_want():
     D, tokens = 300, 900
     w, tok, seq = state(8, D, tokens, 1)
