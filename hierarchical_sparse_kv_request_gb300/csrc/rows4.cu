@@ -224,7 +224,8 @@ int hisparse_attend_workspace(int32_t num_requests, int32_t num_heads, int32_t t
     *bytes = 0;
     const int rc = check_attend_sizes(num_requests, num_heads, top_k);
     if (rc != HISPARSE_OK) return rc;
-    return cuda_status(hs::attend_workspace_bytes(num_requests, num_heads, top_k, with_weights != 0, bytes));
+    hs::attend_workspace_bytes(num_requests, num_heads, top_k, with_weights != 0, bytes);
+    return HISPARSE_OK;
 }
 
 int hisparse_attend(const hisparse_attend_args *p, void *stream)

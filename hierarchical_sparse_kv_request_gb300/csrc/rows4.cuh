@@ -67,10 +67,11 @@ struct AttendLaunch {
     int32_t *status;
     uint8_t *workspace;
 };
-// Workspace of a call on the current device.  The first call on a device also
-// loads the attention kernels and finds how many of their clusters it holds.
-cudaError_t attend_workspace_bytes(int32_t R, int32_t H, int32_t k, bool weights, int64_t *bytes);
-// Launches nothing and sets *too_small if the workspace is too small.
+// Workspace of a call.
+void attend_workspace_bytes(int32_t R, int32_t H, int32_t k, bool weights, int64_t *bytes);
+// Launches nothing and sets *too_small if the workspace is too small.  The first
+// call on a device also loads the attention kernels and finds how many of their
+// clusters it holds.
 cudaError_t launch_attend(const AttendLaunch &a, int64_t workspace_bytes, bool *too_small, cudaStream_t s);
 
 // Arguments of the eviction kernel.  With st.tok2slot the chosen slots are

@@ -147,9 +147,9 @@ int hisparse_attend(const hisparse_attend_args *args, void *stream);
 
 /*
  * hisparse_attend_workspace: *bytes <- the workspace of hisparse_attend for
- * these sizes on the current device (with_weights: weights are asked for).
- * Its contents need not survive between calls; calls that may overlap on the
- * GPU need a workspace each.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ * these sizes (with_weights: weights are asked for).  Its contents need not
+ * survive between calls; calls that may overlap on the GPU need a workspace
+ * each.  Errors: INVALID_ARG, UNSUPPORTED.
  */
 int hisparse_attend_workspace(int32_t num_requests, int32_t num_heads, int32_t top_k,
                               int32_t with_weights, int64_t *bytes);

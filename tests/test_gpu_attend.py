@@ -301,6 +301,36 @@ def test_bad_ids_are_skipped_and_recorded():
                                bit(H.STATUS_BAD_INDEX), bit(H.STATUS_BAD_POSITION)]
 
 
+@pytest.mark.parametrize("R,heads,k", [(160, 5, 130), (155, 40, 129), (80, 70, 200), (310, 3, 130)])
+def test_more_requests_than_a_wave(R, heads, k):
+    """The requests behind the last whole wave go in a launch of their own, with
+    their own places in every array."""
+    call(R, heads, k, k + 9, "f16" if R % 2 else "bf16", seed=R, pad=0.2, weights=True, resident=20)
+
+
+def test_status_and_weights_of_requests_behind_a_wave():
+    R, heads, k, D, tokens = 160, 5, 130, 140, 300
+    rows = make_rows(R * D, "bf16", 3).view(R, D, 416)
+    q = make_q(R, heads, "bf16", 4)
+    ids = torch.stack([torch.randperm(D)[:k] for _ in range(R)]).int().cuda()
+    pos = torch.stack([torch.randperm(tokens)[:k] for _ in range(R)]).int().cuda()
+    ids[3, 5], ids[157, 7] = D, -9
+    pos[4, 0], pos[159, 1] = tokens, -2
+    out = torch.empty((R, heads, 512), dtype=torch.bfloat16, device="cuda")
+    acc = torch.zeros((R, tokens), device="cuda")
+    status = torch.zeros(R, dtype=torch.int32, device="cuda")
+    H.attend(q, rows, ids, out, 0.05, weights=acc, positions=pos, status=status)
+    bit, want = H.STATUS_BIT, [0] * R
+    want[3] = want[157] = bit(H.STATUS_BAD_INDEX)
+    want[4] = want[159] = bit(H.STATUS_BAD_POSITION)
+    assert status.tolist() == want
+    for r in (0, 3, 151, 152, 157, 158):      # the same request by itself
+        alone, mine = torch.empty((1, heads, 512), dtype=torch.bfloat16, device="cuda"), torch.zeros((1, tokens), device="cuda")
+        H.attend(q[r:r + 1], rows[r:r + 1], ids[r:r + 1], alone, 0.05, weights=mine, positions=pos[r:r + 1])
+        torch.testing.assert_close(alone[0], out[r], rtol=2.0 ** -7, atol=1e-3)
+        torch.testing.assert_close(mine[0], acc[r], rtol=1e-4, atol=1e-6)
+
+
 def test_repeated_rows_count_twice_and_results_repeat():
     R, heads, k, D = 2, 16, 500, 600
     rows = make_rows(R * D, "bf16", 1).view(R, D, 416)
