@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(WT_NT, 6) weights_kernel(const __grid_constant
     const int t = blockIdx.x, r = blockIdx.y, j = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
     WeightRow row;
     row.load(a, r, t, j, lane);      // (inputs: they do not wait for the launch before)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_launch_before();
     const float4 *s = scores_at(w, r, t, j, lane);
     const float *lse2 = w.lse2 + (int64_t)r * a.H;
     float sum0 = 0.0f, sum1 = 0.0f;
@@ -420,8 +420,6 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
                                                           const __grid_constant__ AttendParts w)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    // this call's own next launch may be placed now; it waits for this grid
-    if (a.weights && !w.whole) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     AttendSmem &sm = *reinterpret_cast<AttendSmem *>(smem + MISC_AT);
     const uint32_t stages = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -448,8 +446,10 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
     const int heads = min(HEADS, a.H - h0);
     const Join join{stages, smem_u32(&sm.known), smem_u32(&sm.joined), sm.ml, heads, w.splits, split, w.split_inv, staged_slots(heads, w.splits) <= SLOTS};
     if (decodes) {
+        after_launch_before();
         id = ids_at(0);
     } else if (warp < SOFTMAX_WARPS) {
+        after_launch_before();
         fetch_queries(a, r, h0, stages + Q_AT, smem_u32(&sm.fetched[warp]), warp, lane);
     } else {
         if (lane == 0) {
@@ -473,6 +473,10 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
         sm.top[lane] = sm.top[lane + 32] = 0;
         __syncwarp();
         tmem_alloc_all(smem_u32(&sm.tmem));
+        after_launch_before();
+        // this call's own next launch may be placed now (the inputs that it reads
+        // are there); it waits for this grid
+        if (a.weights && !w.whole) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
@@ -798,21 +802,6 @@ struct Capacity {
     int clusters[MAX_SPLITS + 1];
 };
 
-// grid.x: the CTAs of a cluster
-void cluster_launch(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &attr, dim3 grid, cudaStream_t s)
-{
-    cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(AT_NT);
-    cfg.dynamicSmemBytes = AT_SMEM;
-    cfg.stream = s;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = grid.x;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-}
-
 // Sets the kernel's attributes on the current device (which also loads it) and
 // fills in cap.
 template <class Kernel>
@@ -821,9 +810,16 @@ cudaError_t prepare(Kernel kernel, Capacity *cap)
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AT_SMEM);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     for (int c = 1; e == cudaSuccess && c <= MAX_SPLITS; ++c) {
-        cudaLaunchConfig_t cfg;
+        cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr;
-        cluster_launch(cfg, attr, dim3(c), nullptr);
+        cfg.gridDim = dim3(c);
+        cfg.blockDim = dim3(AT_NT);
+        cfg.dynamicSmemBytes = AT_SMEM;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = c;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
         int n = 0;
         if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
             cudaGetLastError();
@@ -935,20 +931,10 @@ cudaError_t launch_requests(AttendLaunch a, AttendParts w, int32_t first, int32_
     w.split_inv = 65536u / (unsigned)w.splits + 1u;
     w.rows_per_split = (w.tiles + w.splits - 1) / w.splits * TILE;
     w.whole = w.splits == 1 && a.H <= HEADS;
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr;
-    cluster_launch(cfg, attr, dim3(w.splits, head_tiles, count), s);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, a.dtype == kBf16 ? attend_kernel<kBf16> : attend_kernel<kF16>, a, w);
+    const cudaError_t e = launch_behind(a.dtype == kBf16 ? attend_kernel<kBf16> : attend_kernel<kF16>,
+                                        dim3(w.splits, head_tiles, count), AT_NT, AT_SMEM, w.splits, s, a, w);
     if (e != cudaSuccess || !a.weights || w.whole) return e;
-    cfg = {};
-    cfg.gridDim = dim3((unsigned)w.tiles, (unsigned)count);
-    cfg.blockDim = dim3(WT_NT);
-    cfg.stream = s;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, weights_kernel, a, w);
+    return launch_behind(weights_kernel, dim3(w.tiles, count), WT_NT, 0, 1, s, a, w);
 }
 
 }  // namespace

@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(EV_NT / C) evict_kernel(EvictLaunch a)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = a.D, n = a.n, s0 = rank * KT * NT + tid;      // the thread's first slot
     const int32_t *s2t = a.slot2tok + (int64_t)r * D;
+    after_launch_before();
     const int32_t S = a.seq_lens[r];
     uint32_t key[KT];        // first its slot's token, then the token's weight
 #pragma unroll
@@ -335,30 +336,14 @@ cudaError_t as_pairs(int R, bool *yes)
 template <int KT>
 cudaError_t launch_kt(const EvictLaunch &a, cudaStream_t s)
 {
-    if (a.st.tok2slot) {
-        evict_kernel<KT, true, 1><<<a.R, EV_NT, 0, s>>>(a);
-        return cudaGetLastError();
-    }
+    if (a.st.tok2slot) return launch_behind(evict_kernel<KT, true, 1>, dim3(a.R), EV_NT, 0, 1, s, a);
     if (KT >= 16) {
         bool pairs;
         const cudaError_t e = as_pairs(a.R, &pairs);
         if (e != cudaSuccess) return e;
-        if (pairs) {
-            cudaLaunchConfig_t cfg = {};
-            cudaLaunchAttribute attr;
-            cfg.gridDim = dim3((unsigned)a.R * 2);
-            cfg.blockDim = dim3(EV_NT / 2);
-            cfg.stream = s;
-            attr.id = cudaLaunchAttributeClusterDimension;
-            attr.val.clusterDim.x = 2;
-            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-            cfg.attrs = &attr;
-            cfg.numAttrs = 1;
-            return cudaLaunchKernelEx(&cfg, evict_kernel<KT < 16 ? 16 : KT, false, 2>, a);
-        }
+        if (pairs) return launch_behind(evict_kernel<KT < 16 ? 16 : KT, false, 2>, dim3(a.R * 2), EV_NT / 2, 0, 2, s, a);
     }
-    evict_kernel<KT, false, 1><<<a.R, EV_NT, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_behind(evict_kernel<KT, false, 1>, dim3(a.R), EV_NT, 0, 1, s, a);
 }
 
 }  // namespace

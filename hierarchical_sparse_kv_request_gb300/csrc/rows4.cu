@@ -67,6 +67,7 @@ template <int DT>
 __global__ void __launch_bounds__(ROWS_NT, ROWS_CTAS) pack_kernel(const uint8_t *values, int64_t vstride, int64_t n,
                                                                   uint8_t *rows, int64_t rstride)
 {
+    after_launch_before();
     const int lane = threadIdx.x & 31;
     const int64_t i = (int64_t)blockIdx.x * ROWS_A_CTA + (threadIdx.x >> 5);
     if (i >= n) return;     // the same for the whole warp
@@ -120,6 +121,7 @@ template <int DT>
 __global__ void __launch_bounds__(ROWS_NT, ROWS_CTAS) unpack_kernel(const uint8_t *rows, int64_t rstride, int64_t n,
                                                                     uint8_t *values, int64_t vstride)
 {
+    after_launch_before();
     const int lane = threadIdx.x & 31;
     const int64_t i = (int64_t)blockIdx.x * ROWS_A_CTA + (threadIdx.x >> 5);
     if (i >= n) return;
@@ -149,10 +151,8 @@ cudaError_t launch_pack_rows(const void *values, int64_t value_stride, int32_t d
     auto *v = static_cast<const uint8_t *>(values);
     auto *d = static_cast<uint8_t *>(rows);
     if (dtype == kBf16)
-        pack_kernel<kBf16><<<rows_grid(n), ROWS_NT, 0, s>>>(v, value_stride * 2, n, d, row_stride);
-    else
-        pack_kernel<kF16><<<rows_grid(n), ROWS_NT, 0, s>>>(v, value_stride * 2, n, d, row_stride);
-    return cudaGetLastError();
+        return launch_behind(pack_kernel<kBf16>, dim3(rows_grid(n)), ROWS_NT, 0, 1, s, v, value_stride * 2, n, d, row_stride);
+    return launch_behind(pack_kernel<kF16>, dim3(rows_grid(n)), ROWS_NT, 0, 1, s, v, value_stride * 2, n, d, row_stride);
 }
 
 cudaError_t launch_unpack_rows(const void *rows, int64_t row_stride, int64_t n, void *values,
@@ -161,10 +161,8 @@ cudaError_t launch_unpack_rows(const void *rows, int64_t row_stride, int64_t n, 
     auto *d = static_cast<const uint8_t *>(rows);
     auto *v = static_cast<uint8_t *>(values);
     if (dtype == kBf16)
-        unpack_kernel<kBf16><<<rows_grid(n), ROWS_NT, 0, s>>>(d, row_stride, n, v, value_stride * 2);
-    else
-        unpack_kernel<kF16><<<rows_grid(n), ROWS_NT, 0, s>>>(d, row_stride, n, v, value_stride * 2);
-    return cudaGetLastError();
+        return launch_behind(unpack_kernel<kBf16>, dim3(rows_grid(n)), ROWS_NT, 0, 1, s, d, row_stride, n, v, value_stride * 2);
+    return launch_behind(unpack_kernel<kF16>, dim3(rows_grid(n)), ROWS_NT, 0, 1, s, d, row_stride, n, v, value_stride * 2);
 }
 
 }  // namespace hs
