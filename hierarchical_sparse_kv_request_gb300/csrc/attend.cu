@@ -42,10 +42,10 @@
 // What bounds it.  The two products of a tile take 2,176 cycles of the tensor
 // pipe; measured, a tile takes some 2,650, as shared memory serves their
 // operands (1,200 cycles), the decoded tile's stores (580) and the fetches.  A
-// CTA's start (ids, then rows; queries) takes some 11 thousand cycles to the
-// first scores, its end 9 to 11 thousand with a join, 5 without.  Measured on
-// GB300, 2,048 rows, GPU time: 32 requests of 128 heads 34 us (537 TFLOP/s), with
-// weights 43; 32 of 16 heads 21; one request of 16 heads 11; 256 requests of 64
+// CTA's start (ids, then rows; queries) takes some 10 thousand cycles to the
+// first scores, its end 7 to 10 thousand with a join, 4 without.  Measured on
+// GB300, 2,048 rows, GPU time: 32 requests of 128 heads 33 us (553 TFLOP/s), with
+// weights 41; 32 of 16 heads 20; one request of 16 heads 10; 256 requests of 64
 // heads with weights 142.
 #include <atomic>
 #include <mutex>
