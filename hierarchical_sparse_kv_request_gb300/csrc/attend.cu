@@ -711,7 +711,6 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
                 if (i < heads) join.send_ml(i, half ? m1 : m0, half ? l1 : l0);
             }
         }
-        __syncwarp();
     }
     const int last = tiles - 1;
     const bool done = all(mbar_wait(smem_u32(&sm.empty[last % STAGES]), (last / STAGES) & 1, gave_up));

@@ -244,8 +244,16 @@ __device__ __forceinline__ void send_v4(uint32_t at, uint4 v, uint32_t bar)
 
 // The cluster's barrier, for what has been waited for already (a release of all
 // that a CTA has written takes some 1,400 cycles).
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive()
+{
+    __syncwarp();      // (.aligned: the warp together)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // Log2 of a head's whole sum, from its reference and sum, and where it goes.
 __device__ __forceinline__ float log2_sum(float m, float l) { return l == 0.0f ? -INFINITY : m + log2f(l); }

@@ -56,10 +56,12 @@ struct EvictSmem {
 template <int C>
 __device__ __forceinline__ void sync_ctas()
 {
-    if (C == 1)
+    if (C == 1) {
         __syncthreads();
-    else
+    } else {
+        __syncwarp();      // (.aligned: the warp together)
         asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
 }
 
 // The address in the cluster's other CTA (of two).
