@@ -574,6 +574,20 @@ def unpack_rows(rows, values, stream=None) -> None:
            "hisparse_unpack_rows")
 
 
+def _allocate(size: int, device, stream, handle: int):
+    """uint8 tensor for work on `stream` (None, a Stream or an address;
+    handle: its address) that may be dropped once that work is launched: its
+    memory is the allocator's for that stream, so what gets it next runs
+    behind the work."""
+    t = _torch
+    if stream is None:
+        return t.empty(size, dtype=t.uint8, device=device)
+    if not isinstance(stream, t.cuda.Stream):
+        stream = t.cuda.ExternalStream(handle, device=device)
+    with t.cuda.stream(stream):
+        return t.empty(size, dtype=t.uint8, device=device)
+
+
 def attend_workspace_bytes(num_requests: int, num_heads: int, top_k: int,
                            weights: bool = False) -> int:
     """Bytes of workspace that attend() needs for these sizes."""
@@ -593,7 +607,7 @@ def attend(q, rows, slot_ids, out, scale: float, lse=None, positions=None, weigh
     weights float32 [R][tokens] (accumulated into at positions, int32 [R][k])
     or None; resident_rows uint8 [n][416] for flagged ids; status int32 [R]
     or None; workspace a uint8 tensor of attend_workspace_bytes (None:
-    allocated for this call)."""
+    allocated for this call, on its stream)."""
     (R, D, _), (request_stride, row_stride, _) = _packed(rows, "rows", 3)
     _attend(q, rows.data_ptr(), row_stride if D > 1 else ROW4_BYTES, request_stride if R > 1 else 0,
             R, D, slot_ids, out, scale, lse, positions, weights, resident_rows, status, workspace,
@@ -627,15 +641,16 @@ def _attend(q, rows, row_stride, request_stride, R, D, slot_ids, out, scale, lse
         if columns != k:
             raise ValueError("positions and slot_ids differ in length")
         acc, where = (weights.data_ptr(), stride, tokens), (positions.data_ptr(), positions_stride)
+    launch_stream = _stream(stream)
     if workspace is None:
-        workspace = _torch.empty(attend_workspace_bytes(R, H, k, weights is not None),
-                                 dtype=_torch.uint8, device=q.device)
+        workspace = _allocate(attend_workspace_bytes(R, H, k, weights is not None), q.device,
+                              stream, launch_stream)
     args = _pack_attend_args(
         R, H, k, dt, q.data_ptr(), strides[0], strides[1], rows, row_stride, request_stride, D, scale,
         slot_ids.data_ptr(), ids_stride, *resident, out.data_ptr(), out_strides[0], out_strides[1],
         _addr(lse) or 0, *acc, *where, _addr(status) or 0, workspace.data_ptr(),
         workspace.numel() * workspace.element_size())
-    _check((_lib or load_library()).hisparse_attend(args, _stream(stream)), "hisparse_attend")
+    _check((_lib or load_library()).hisparse_attend(args, launch_stream), "hisparse_attend")
 
 
 def evict_select(weights, slot2tok, seq_lens, out_slots, out_counts, keep_recent: int = 0,

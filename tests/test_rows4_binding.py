@@ -1,0 +1,92 @@
+"""What the binding of the 4-bit row calls does before a launch, with the GPU's
+part played by fakes (CPU only): the library's calls are recorded instead of
+made, and torch's allocator and streams by what they were asked for."""
+
+import types
+
+import pytest
+import torch
+
+from hierarchical_sparse_kv_request_gb300 import build as B
+from hierarchical_sparse_kv_request_gb300 import hisparse as H
+
+R, HEADS, K, D, TOKENS = 2, 3, 5, 8, 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build_library()
+    return H.load_library()
+
+
+class Stream:
+    """Stands for torch.cuda.Stream."""
+
+    def __init__(self, address):
+        self.cuda_stream = address
+
+
+class Gpu:
+    """torch as the binding sees it: `empty` notes the stream that is current
+    while it allocates; and the library: hisparse_attend notes its stream."""
+
+    def __init__(self, lib):
+        self.now, self.allocations, self.launches = Stream(0x111), [], []
+        gpu = self
+
+        class scope:
+            def __init__(self, s):
+                self.s = s
+
+            def __enter__(self):
+                self.s, gpu.now = gpu.now, self.s
+
+            def __exit__(self, *e):
+                gpu.now = self.s
+
+        def empty(size, dtype, device):
+            gpu.allocations.append((gpu.now.cuda_stream, size))
+            return torch.empty(size, dtype=dtype, device=device)
+
+        self.torch = types.SimpleNamespace(
+            bfloat16=torch.bfloat16, float16=torch.float16, float32=torch.float32, int32=torch.int32,
+            uint8=torch.uint8, empty=empty,
+            cuda=types.SimpleNamespace(Stream=Stream, stream=scope, current_stream=lambda: gpu.now,
+                                       ExternalStream=lambda a, device: Stream(a)))
+        self.lib = types.SimpleNamespace(hisparse_attend=self.launch,
+                                         hisparse_attend_workspace=lib.hisparse_attend_workspace)
+
+    def launch(self, args, stream):
+        self.launches.append(stream)
+        return H.OK
+
+
+@pytest.fixture
+def gpu(lib, monkeypatch):
+    g = Gpu(lib)
+    monkeypatch.setattr(H, "_torch", g.torch)
+    monkeypatch.setattr(H, "_lib", g.lib)
+    monkeypatch.setattr(H, "_raw_stream", lambda device: g.now.cuda_stream)
+    monkeypatch.setattr(H, "_device", lambda: 0)
+    return g
+
+
+def tensors():
+    t = dict(q=torch.zeros((R, HEADS, 576), dtype=torch.bfloat16),
+             rows=torch.zeros((R, D, 416), dtype=torch.uint8),
+             slot_ids=torch.zeros((R, K), dtype=torch.int32),
+             out=torch.zeros((R, HEADS, 512), dtype=torch.bfloat16))
+    more = dict(weights=torch.zeros((R, TOKENS)), positions=torch.zeros((R, K), dtype=torch.int32))
+    return t, more
+
+
+@pytest.mark.parametrize("stream,address", [(None, 0x111), (Stream(0x222), 0x222), (0x333, 0x333), (0, 0)])
+@pytest.mark.parametrize("weights", [False, True])
+def test_a_workspace_of_the_call_belongs_to_the_launch_stream(gpu, stream, address, weights):
+    """Freed when the call returns, its memory may go only to work that the
+    launch stream runs behind the call's own."""
+    t, more = tensors()
+    H.attend(**t, scale=1.0, **(more if weights else {}), stream=stream)
+    assert gpu.launches == [address]
+    assert gpu.allocations == [(address, H.attend_workspace_bytes(R, HEADS, K, weights))]
+    assert gpu.now.cuda_stream == 0x111      # the current stream is as it was
