@@ -173,6 +173,10 @@ def _addr(x) -> Optional[int]:
 _torch = _raw_stream = _device = None
 
 
+def _current_device() -> int:
+    return _device() if _device is not None else (_torch or _load_torch()).cuda.current_device()
+
+
 def _load_torch():
     global _torch
     if _torch is None:
@@ -234,6 +238,7 @@ class HiSparse:
         else:
             _check(self.lib.hisparse_create(ctypes.byref(lay), ctypes.byref(h)), "hisparse_create")
         self.h = h
+        self.device = _current_device()
 
     @classmethod
     def for_workload(cls, w, host_block_tokens: int = 0) -> "HiSparse":
@@ -470,9 +475,12 @@ class HiSparse:
     def attend(self, layer: int, q, slot_ids, out, scale: float, lse=None, positions=None,
                weights=None, resident_rows=None, workspace=None, stream=None) -> None:
         """attend() over the layer's hot buffer (row_bytes must be
-        ROW4_BYTES); data errors go to this handle's status words."""
+        ROW4_BYTES); data errors go to this handle's status words.
+        INVALID_ARG unless the handle's device is current."""
         if self.B != ROW4_BYTES:
             raise ValueError(f"row_bytes is {self.B}: attention reads {ROW4_BYTES}-byte rows")
+        if _current_device() != self.device:
+            raise HiSparseError(ERR_INVALID_ARG, f"attend of a handle of device {self.device}")
         _attend(q, self.device_buffer_ptr(layer), self.B, self.D * self.B, self.R, self.D, slot_ids,
                 out, scale, lse, positions, weights, resident_rows, self.status_ptr(), workspace,
                 stream)

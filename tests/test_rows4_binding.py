@@ -53,7 +53,8 @@ class Gpu:
             uint8=torch.uint8, empty=empty,
             cuda=types.SimpleNamespace(Stream=Stream, stream=scope, current_stream=lambda: gpu.now,
                                        ExternalStream=lambda a, device: Stream(a)))
-        self.lib = types.SimpleNamespace(hisparse_attend=self.launch,
+        self.lib = types.SimpleNamespace(hisparse_attend=self.launch, hisparse_destroy=lambda h: H.OK,
+                                         hisparse_error_string=lib.hisparse_error_string,
                                          hisparse_attend_workspace=lib.hisparse_attend_workspace)
 
     def launch(self, args, stream):
@@ -90,3 +91,25 @@ def test_a_workspace_of_the_call_belongs_to_the_launch_stream(gpu, stream, addre
     assert gpu.launches == [address]
     assert gpu.allocations == [(address, H.attend_workspace_bytes(R, HEADS, K, weights))]
     assert gpu.now.cuda_stream == 0x111      # the current stream is as it was
+
+
+def handle(gpu, device):
+    """A handle of this device, without the library's side of one."""
+    h = object.__new__(H.HiSparse)
+    h.lib, h.h, h.device = gpu.lib, None, device
+    h.R, h.D, h.B = R, D, H.ROW4_BYTES
+    h.device_buffer_ptr, h.status_ptr = lambda layer: 1 << 20, lambda: 1 << 21
+    return h
+
+
+def test_a_handle_refuses_to_attend_on_another_device(gpu, monkeypatch):
+    """As its other launching calls do."""
+    t, _ = tensors()
+    del t["rows"]
+    handle(gpu, 0).attend(0, **t, scale=1.0)
+    assert len(gpu.launches) == 1
+    monkeypatch.setattr(H, "_device", lambda: 1)
+    with pytest.raises(H.HiSparseError) as e:
+        handle(gpu, 0).attend(0, **t, scale=1.0)
+    assert e.value.code == H.ERR_INVALID_ARG
+    assert len(gpu.launches) == 1 and len(gpu.allocations) == 1
