@@ -544,6 +544,14 @@ def _ints(x, what: str, shape) -> None:
         raise ValueError(f"{what} must be a contiguous int32 tensor of shape {shape}")
 
 
+def _words(status, R: int) -> int:
+    """Address of status: None, an address, or a contiguous int32 tensor [R]."""
+    if status is None or isinstance(status, int):
+        return status or 0
+    _ints(status, "status", (R,))
+    return status.data_ptr()
+
+
 def _packed(rows, what: str, dims: int):
     """Shape and strides of packed rows."""
     shape, strides = rows.shape, rows.stride()
@@ -656,7 +664,7 @@ def _attend(q, rows, row_stride, request_stride, R, D, slot_ids, out, scale, lse
     args = _pack_attend_args(
         R, H, k, dt, q.data_ptr(), strides[0], strides[1], rows, row_stride, request_stride, D, scale,
         slot_ids.data_ptr(), ids_stride, *resident, out.data_ptr(), out_strides[0], out_strides[1],
-        _addr(lse) or 0, *acc, *where, _addr(status) or 0, workspace.data_ptr(),
+        _addr(lse) or 0, *acc, *where, _words(status, R), workspace.data_ptr(),
         workspace.numel() * workspace.element_size())
     _check((_lib or load_library()).hisparse_attend(args, launch_stream), "hisparse_attend")
 

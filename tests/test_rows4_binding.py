@@ -113,3 +113,17 @@ def test_a_handle_refuses_to_attend_on_another_device(gpu, monkeypatch):
         handle(gpu, 0).attend(0, **t, scale=1.0)
     assert e.value.code == H.ERR_INVALID_ARG
     assert len(gpu.launches) == 1 and len(gpu.allocations) == 1
+
+
+@pytest.mark.parametrize("status", [
+    torch.zeros(R - 1, dtype=torch.int32), torch.zeros(R + 1, dtype=torch.int32), torch.zeros((R, 1), dtype=torch.int32),
+    torch.zeros(R, dtype=torch.int64), torch.zeros(R), torch.zeros(2 * R, dtype=torch.int32)[::2]])
+def test_attend_refuses_status_words_of_another_shape_or_type(gpu, status):
+    """A word past the end would be written at the first bad id there."""
+    t, _ = tensors()
+    with pytest.raises(ValueError):
+        H.attend(**t, scale=1.0, status=status)
+    assert gpu.launches == []
+    for good in (torch.zeros(R, dtype=torch.int32), 1 << 20, None):
+        H.attend(**t, scale=1.0, status=good)
+    assert len(gpu.launches) == 3
