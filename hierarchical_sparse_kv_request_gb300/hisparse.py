@@ -661,6 +661,8 @@ def _attend(q, rows, row_stride, request_stride, R, D, slot_ids, out, scale, lse
     if workspace is None:
         workspace = _allocate(attend_workspace_bytes(R, H, k, weights is not None), q.device,
                               stream, launch_stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     args = _pack_attend_args(
         R, H, k, dt, q.data_ptr(), strides[0], strides[1], rows, row_stride, request_stride, D, scale,
         slot_ids.data_ptr(), ids_stride, *resident, out.data_ptr(), out_strides[0], out_strides[1],

@@ -127,3 +127,16 @@ def test_attend_refuses_status_words_of_another_shape_or_type(gpu, status):
     for good in (torch.zeros(R, dtype=torch.int32), 1 << 20, None):
         H.attend(**t, scale=1.0, status=good)
     assert len(gpu.launches) == 3
+
+
+def test_attend_refuses_a_workspace_that_is_not_contiguous(gpu):
+    """Its size says nothing about the memory that it has."""
+    t, _ = tensors()
+    size = H.attend_workspace_bytes(R, HEADS, K)
+    one = torch.zeros(16, dtype=torch.uint8)
+    for bad in (one[:1].expand(size), torch.zeros(2 * size, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            H.attend(**t, scale=1.0, workspace=bad)
+    assert gpu.launches == []
+    H.attend(**t, scale=1.0, workspace=torch.zeros(size // 4, dtype=torch.int32))
+    assert len(gpu.launches) == 1
