@@ -481,9 +481,9 @@ class HiSparse:
             raise ValueError(f"row_bytes is {self.B}: attention reads {ROW4_BYTES}-byte rows")
         if _current_device() != self.device:
             raise HiSparseError(ERR_INVALID_ARG, f"attend of a handle of device {self.device}")
-        _attend(q, self.device_buffer_ptr(layer), self.B, self.D * self.B, self.R, self.D, slot_ids,
-                out, scale, lse, positions, weights, resident_rows, self.status_ptr(), workspace,
-                stream)
+        _attend(q, None, self.device_buffer_ptr(layer), self.B, self.D * self.B, self.R, self.D,
+                slot_ids, out, scale, lse, positions, weights, resident_rows, self.status_ptr(),
+                workspace, stream)
 
     def evict(self, layer: int, weights, seq_lens, n: int, keep_recent: int = 0, want=None,
               out_slots=None, out_counts=None, stream=None) -> None:
@@ -616,21 +616,23 @@ def attend_workspace_bytes(num_requests: int, num_heads: int, top_k: int,
 
 def attend(q, rows, slot_ids, out, scale: float, lse=None, positions=None, weights=None,
            resident_rows=None, status=None, workspace=None, stream=None) -> None:
-    """hisparse_attend: one step's sparse attention over 4-bit rows.
+    """hisparse_attend: one step's sparse attention over 4-bit rows, on the
+    current device.
 
     q [R][H][576] and out [R][H][512] in bf16 or f16; rows uint8 [R][D][416];
     slot_ids int32 [R][k] as swap_in writes them; lse float32 [R][H] or None;
     weights float32 [R][tokens] (accumulated into at positions, int32 [R][k])
     or None; resident_rows uint8 [n][416] for flagged ids; status int32 [R]
     or None; workspace a uint8 tensor of attend_workspace_bytes (None:
-    allocated for this call, on its stream)."""
+    allocated for this call, on its stream).  All of them on that device;
+    slot_ids and positions also in pinned host memory."""
     (R, D, _), (request_stride, row_stride, _) = _packed(rows, "rows", 3)
-    _attend(q, rows.data_ptr(), row_stride if D > 1 else ROW4_BYTES, request_stride if R > 1 else 0,
-            R, D, slot_ids, out, scale, lse, positions, weights, resident_rows, status, workspace,
-            stream)
+    _attend(q, rows, rows.data_ptr(), row_stride if D > 1 else ROW4_BYTES,
+            request_stride if R > 1 else 0, R, D, slot_ids, out, scale, lse, positions, weights,
+            resident_rows, status, workspace, stream)
 
 
-def _attend(q, rows, row_stride, request_stride, R, D, slot_ids, out, scale, lse, positions,
+def _attend(q, rows, rows_at, row_stride, request_stride, R, D, slot_ids, out, scale, lse, positions,
             weights, resident_rows, status, workspace, stream) -> None:
     dt = _dtype16(q, "q")
     shape, strides = q.shape, q.stride()
@@ -657,6 +659,14 @@ def _attend(q, rows, row_stride, request_stride, R, D, slot_ids, out, scale, lse
         if columns != k:
             raise ValueError("positions and slot_ids differ in length")
         acc, where = (weights.data_ptr(), stride, tokens), (positions.data_ptr(), positions_stride)
+    words = _words(status, R)
+    device = _current_device()
+    for x in (q, rows, out, lse, weights, resident_rows, workspace, status):
+        if x is not None and not isinstance(x, int) and x.get_device() != device:
+            raise ValueError(f"only slot_ids and positions may be outside the current device, {device}")
+    for x in (slot_ids, positions):
+        if x is not None and x.get_device() not in (device, -1):
+            raise ValueError(f"slot_ids and positions must be on device {device} or pinned")
     launch_stream = _stream(stream)
     if workspace is None:
         workspace = _allocate(attend_workspace_bytes(R, H, k, weights is not None), q.device,
@@ -664,9 +674,9 @@ def _attend(q, rows, row_stride, request_stride, R, D, slot_ids, out, scale, lse
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     args = _pack_attend_args(
-        R, H, k, dt, q.data_ptr(), strides[0], strides[1], rows, row_stride, request_stride, D, scale,
+        R, H, k, dt, q.data_ptr(), strides[0], strides[1], rows_at, row_stride, request_stride, D, scale,
         slot_ids.data_ptr(), ids_stride, *resident, out.data_ptr(), out_strides[0], out_strides[1],
-        _addr(lse) or 0, *acc, *where, _words(status, R), workspace.data_ptr(),
+        _addr(lse) or 0, *acc, *where, words, workspace.data_ptr(),
         workspace.numel() * workspace.element_size())
     _check((_lib or load_library()).hisparse_attend(args, launch_stream), "hisparse_attend")
 

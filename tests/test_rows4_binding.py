@@ -68,7 +68,7 @@ def gpu(lib, monkeypatch):
     monkeypatch.setattr(H, "_torch", g.torch)
     monkeypatch.setattr(H, "_lib", g.lib)
     monkeypatch.setattr(H, "_raw_stream", lambda device: g.now.cuda_stream)
-    monkeypatch.setattr(H, "_device", lambda: 0)
+    monkeypatch.setattr(H, "_device", lambda: -1)     # the tensors' (the CPU's) number
     return g
 
 
@@ -102,15 +102,14 @@ def handle(gpu, device):
     return h
 
 
-def test_a_handle_refuses_to_attend_on_another_device(gpu, monkeypatch):
+def test_a_handle_refuses_to_attend_on_another_device(gpu):
     """As its other launching calls do."""
     t, _ = tensors()
     del t["rows"]
-    handle(gpu, 0).attend(0, **t, scale=1.0)
+    handle(gpu, -1).attend(0, **t, scale=1.0)
     assert len(gpu.launches) == 1
-    monkeypatch.setattr(H, "_device", lambda: 1)
     with pytest.raises(H.HiSparseError) as e:
-        handle(gpu, 0).attend(0, **t, scale=1.0)
+        handle(gpu, 1).attend(0, **t, scale=1.0)
     assert e.value.code == H.ERR_INVALID_ARG
     assert len(gpu.launches) == 1 and len(gpu.allocations) == 1
 
@@ -139,4 +138,43 @@ def test_attend_refuses_a_workspace_that_is_not_contiguous(gpu):
             H.attend(**t, scale=1.0, workspace=bad)
     assert gpu.launches == []
     H.attend(**t, scale=1.0, workspace=torch.zeros(size // 4, dtype=torch.int32))
+    assert len(gpu.launches) == 1
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor of another GPU."""
+
+    def get_device(self):
+        return 1
+
+
+@pytest.mark.parametrize("name", ["q", "rows", "slot_ids", "out", "lse", "positions", "weights", "resident_rows",
+                                  "status", "workspace"])
+def test_attend_refuses_tensors_of_another_device(gpu, name):
+    t, more = tensors()
+    t.update(more, lse=torch.zeros((R, HEADS)), resident_rows=torch.zeros((4, 416), dtype=torch.uint8),
+             status=torch.zeros(R, dtype=torch.int32),
+             workspace=torch.zeros(H.attend_workspace_bytes(R, HEADS, K, True), dtype=torch.uint8))
+    H.attend(**t, scale=1.0)
+    assert len(gpu.launches) == 1
+    t[name] = t[name].as_subclass(Elsewhere)
+    with pytest.raises(ValueError):
+        H.attend(**t, scale=1.0)
+    if name != "rows":
+        del t["rows"], t["status"]
+        if name != "status":
+            with pytest.raises(ValueError):
+                handle(gpu, -1).attend(0, **t, scale=1.0)
+    assert len(gpu.launches) == 1
+
+
+def test_only_ids_and_positions_may_be_host_tensors(gpu, monkeypatch):
+    t, more = tensors()
+    t.update(more)
+    monkeypatch.setattr(H, "_device", lambda: 1)       # now the CPU's tensors are the host's
+    with pytest.raises(ValueError):
+        H.attend(**t, scale=1.0)
+    for name in ("q", "rows", "out", "weights"):
+        t[name] = t[name].as_subclass(Elsewhere)
+    H.attend(**t, scale=1.0, workspace=torch.zeros(1 << 16, dtype=torch.uint8).as_subclass(Elsewhere))
     assert len(gpu.launches) == 1
