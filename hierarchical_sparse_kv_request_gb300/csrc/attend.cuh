@@ -187,12 +187,13 @@ struct PowerOfTwo {
 // A query is multiplied by 2^-e (latent: 2^(7 - e), decode8's 2^7) and the sign
 // of the scale; top: the 16 bits of its largest magnitude.  e is that one's
 // exponent, or 0 where there is none and for infinities, which pass through as
-// they are (as NaN does); 2^(7 - e) has to be representable, in one step or two.
+// they are (as NaN does); 2^-e and 2^(7 - e) have to be normal, f16's in two
+// steps (so bf16's largest exponent, 127, counts as 126).
 template <int DT>
 __device__ __forceinline__ int query_exponent(uint32_t top)
 {
     const int e = (int)(__float_as_uint(pair_to_float<DT>(top).x) >> 23) - 127;
-    return max(top == 0 || e == 128 ? 0 : e, DT == kBf16 ? -119 : -23);
+    return min(max(top == 0 || e == 128 ? 0 : e, DT == kBf16 ? -119 : -23), 126);
 }
 
 // What the products of such a query have to be multiplied by to be base-2
