@@ -197,10 +197,11 @@ __device__ __forceinline__ int query_exponent(uint32_t top)
 }
 
 // What the products of such a query have to be multiplied by to be base-2
-// scores; positive.
+// scores; positive.  (The power of two first: the largest scales times log2(e)
+// are infinite, and the smallest lose bits.)
 __device__ __forceinline__ float query_factor(const AttendLaunch &a, int e)
 {
-    return fmaxf(fabsf(a.scale) * kLog2e * exp2i(e), FLT_MIN);
+    return fmaxf(fabsf(a.scale) * exp2i(e) * kLog2e, FLT_MIN);
 }
 
 // How a call is cut up, and its workspace.
