@@ -207,15 +207,16 @@ __device__ __forceinline__ void place_queries(const AttendLaunch &a, int heads, 
         e[half] = query_exponent<DT>(top[i]);
         if (q == 0 && share == 0) factor[i0 + 8 * half] = query_factor(a, e[half]);
     }
-    // with the sign of the scale, so that the factor of the scores is positive
-    const bool neg = a.scale < 0.0f;
+    // with the sign of the scale, so that the factor of the scores is positive,
+    // and NaN if it is: the scores of rows, not of holes, become so
+    const float sign = a.scale != a.scale ? a.scale : copysignf(1.0f, a.scale);
     // Four of the quarter's warps take 64 columns each, the fifth the rope part.
     // Latent columns 8 j + 2 q and + 1 hold the even (q even) or the odd values
     // of the eight in unit 2 j + q / 2, the order of decode8, with its 2^7; rope
     // columns their values in order.
     static_assert(QUARTER_WARPS == 5, "");
     if (share < 4) {
-        const PowerOfTwo<DT> up7[2] = {{7 - e[0], neg}, {7 - e[1], neg}};
+        const PowerOfTwo<DT> up7[2] = {{7 - e[0], sign}, {7 - e[1], sign}};
         const uint32_t pick = q & 1 ? 0x7632 : 0x5410;
         uint32_t v[32];
 #pragma unroll
@@ -235,7 +236,7 @@ __device__ __forceinline__ void place_queries(const AttendLaunch &a, int heads, 
             }
         tmem_st_16x64(tmem + share * 64, v);
     } else {
-        const PowerOfTwo<DT> up[2] = {{-e[0], neg}, {-e[1], neg}};
+        const PowerOfTwo<DT> up[2] = {{-e[0], sign}, {-e[1], sign}};
         uint32_t v[16];
 #pragma unroll
         for (int j = 0; j < 4; ++j)

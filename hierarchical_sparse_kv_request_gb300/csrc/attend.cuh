@@ -155,14 +155,13 @@ __device__ __forceinline__ uint32_t magnitude(uint32_t m, uint4 x)
     return max2<DT>(m, max2<DT>(max2<DT>(x.x, x.y), max2<DT>(x.z, x.w)));
 }
 
-// Two values times a power of two, exactly: 2^n for bf16, 2^n in two steps for
-// f16, whose own powers reach 2^15.
+// Two values times a power of two and a sign (or NaN), exactly: 2^n for bf16, 2^n
+// in two steps for f16, whose own powers reach 2^15.
 template <int DT>
 struct PowerOfTwo {
     uint32_t f[2];
-    __device__ __forceinline__ PowerOfTwo(int n, bool negative)
+    __device__ __forceinline__ PowerOfTwo(int n, float s)
     {
-        const float s = negative ? -1.0f : 1.0f;
         if (DT == kBf16) {
             f[0] = floats_to_pair<DT>(s * exp2i(n), s * exp2i(n));
         } else {
