@@ -236,11 +236,11 @@ int hisparse_attend(const hisparse_attend_args *p, void *stream)
     if (!a.q || !a.rows || !a.slot_ids || !a.out || !a.workspace || a.rows_per_request < 1 ||
         a.ids_stride < a.top_k)
         return HISPARSE_ERR_INVALID_ARG;
-    if (a.q_request_stride % 8 != 0 || a.q_head_stride % 8 != 0 || a.out_request_stride % 8 != 0 ||
-        a.out_head_stride % 8 != 0)
+    // (the stride of a dimension of one is not used and means nothing)
+    if (a.num_requests > 1 && (a.q_request_stride % 8 != 0 || a.out_request_stride % 8 != 0 || a.request_stride % 16 != 0))
         return HISPARSE_ERR_INVALID_ARG;
-    if (a.row_stride < HISPARSE_ROW4_BYTES || a.row_stride % 16 != 0 || a.request_stride % 16 != 0)
-        return HISPARSE_ERR_INVALID_ARG;
+    if (a.num_heads > 1 && (a.q_head_stride % 8 != 0 || a.out_head_stride % 8 != 0)) return HISPARSE_ERR_INVALID_ARG;
+    if (a.row_stride < HISPARSE_ROW4_BYTES || a.row_stride % 16 != 0) return HISPARSE_ERR_INVALID_ARG;
     if (a.resident_count < 0 || (a.resident_count > 0 && !a.resident_rows)) return HISPARSE_ERR_INVALID_ARG;
     if (a.resident_count > 0 && (a.resident_stride < HISPARSE_ROW4_BYTES || a.resident_stride % 16 != 0))
         return HISPARSE_ERR_INVALID_ARG;

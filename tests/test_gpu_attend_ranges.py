@@ -40,3 +40,19 @@ def test_queries_up_to_the_largest_bf16_values(top):
     q = (q * 2.0 ** top).to(torch.bfloat16)
     assert torch.isfinite(q).all()
     attend(q, rows, 2.0 ** (-4 - top), k, "bf16")
+
+
+@pytest.mark.parametrize("R,heads,k", [(1, 1, 90), (1, 1, 1000), (1, 20, 300), (3, 1, 300)])
+def test_strides_of_a_single_head_or_request_mean_nothing(R, heads, k):
+    D = k + 9
+    rows = make_rows(R * D, "bf16", 3).view(R, D, 416)
+    q, out = make_q(R, heads, "bf16", 4), torch.empty((R, heads, 512), dtype=torch.bfloat16, device="cuda")
+
+    def odd(x, n):
+        return torch.as_strided(x, x.shape, (n * heads if R > 1 else 3, n if heads > 1 else 1, 1))
+
+    odd_rows = torch.as_strided(rows, rows.shape, (D * 416 if R > 1 else 5, 416, 1))
+    ids = torch.stack([torch.randperm(D)[:k] for _ in range(R)]).int().cuda()
+    acc = torch.zeros((R, D), device="cuda")
+    H.attend(odd(q, 576), odd_rows, ids, odd(out, 512), 0.05, weights=acc, positions=ids)
+    check(q, rows, ids, out, float(np.float32(0.05)), "bf16", None, acc, torch.zeros_like(acc), ids)
