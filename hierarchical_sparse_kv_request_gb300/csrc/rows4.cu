@@ -171,6 +171,8 @@ namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+uint64_t apart(int64_t stride) { return stride < 0 ? 0u - (uint64_t)stride : (uint64_t)stride; }
+
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? HISPARSE_OK : HISPARSE_ERR_CUDA; }
 
 int check_rows(const void *values, int64_t value_stride, int32_t dtype, int64_t n, const void *rows,
@@ -240,6 +242,9 @@ int hisparse_attend(const hisparse_attend_args *p, void *stream)
     if (a.num_requests > 1 && (a.q_request_stride % 8 != 0 || a.out_request_stride % 8 != 0 || a.request_stride % 16 != 0))
         return HISPARSE_ERR_INVALID_ARG;
     if (a.num_heads > 1 && (a.q_head_stride % 8 != 0 || a.out_head_stride % 8 != 0)) return HISPARSE_ERR_INVALID_ARG;
+    if ((a.num_requests > 1 && apart(a.out_request_stride) < HISPARSE_ROW4_LATENT) ||
+        (a.num_heads > 1 && apart(a.out_head_stride) < HISPARSE_ROW4_LATENT))
+        return HISPARSE_ERR_INVALID_ARG;      // heads of out would overlap
     if (a.row_stride < HISPARSE_ROW4_BYTES || a.row_stride % 16 != 0) return HISPARSE_ERR_INVALID_ARG;
     if (a.resident_count < 0 || (a.resident_count > 0 && !a.resident_rows)) return HISPARSE_ERR_INVALID_ARG;
     if (a.resident_count > 0 && (a.resident_stride < HISPARSE_ROW4_BYTES || a.resident_stride % 16 != 0))

@@ -83,7 +83,8 @@ int hisparse_unpack_rows(const void *rows, int64_t row_stride, int64_t n, void *
 /*
  * Arguments of hisparse_attend.  Strides of q and out are in elements (of
  * `dtype`), multiples of 8; row strides are in bytes, multiples of 16.  The
- * request and head strides of a single request or head are not looked at.
+ * request and head strides of a single request or head are not looked at;
+ * otherwise those of out are at least 512 apart.
  */
 typedef struct hisparse_attend_args {
     int32_t num_requests;          /* R >= 1 */

@@ -41,3 +41,16 @@ def test_strides_of_a_single_head_or_request_mean_nothing(lib, change):
     dict(num_heads=1, request_stride=8)])
 def test_strides_of_the_other_dimension_still_count(lib, change):
     assert call(lib, **change) == H.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(out_head_stride=0), H.ERR_INVALID_ARG),            # one head's row for all
+    (dict(out_request_stride=0), H.ERR_INVALID_ARG),
+    (dict(out_head_stride=504), H.ERR_INVALID_ARG),
+    (dict(out_head_stride=-8), H.ERR_INVALID_ARG),
+    (dict(out_request_stride=-(1 << 63) + 16), H.ERR_CAPACITY),
+    (dict(out_request_stride=512, out_head_stride=1024), H.ERR_CAPACITY),     # [H][R][512]
+    (dict(out_request_stride=-1536, out_head_stride=-512), H.ERR_CAPACITY),
+    (dict(q_request_stride=0, q_head_stride=0), H.ERR_CAPACITY)])             # read only: one query for all
+def test_heads_of_out_may_not_overlap(lib, change, code):
+    assert call(lib, **change) == code
