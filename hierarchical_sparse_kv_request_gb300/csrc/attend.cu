@@ -69,6 +69,11 @@ constexpr uint32_t TMEM_Q = 2 * TILE;            // lower lanes: S of two tiles,
 constexpr int SLOTS = (STAGES * OPERAND + HEADS * 64) / O_STRIDE;
 static_assert(SLOTS >= HEADS + MAX_SPLITS - 1, "the parts that a CTA joins");
 
+// See AttendParts::split_inv: n * (65536 / splits + 1 - f) >> 16, f < 1, is exact
+// while n < 65536 / splits.
+constexpr uint32_t inverse_of(int splits) { return 65536u / (unsigned)splits + 1u; }
+static_assert((HEADS + MAX_SPLITS) * MAX_SPLITS <= 65536, "");
+
 struct AttendSmem {
     uint64_t full[STAGES], empty[STAGES], scored[2], weighed[2], fetched[SOFTMAX_WARPS], queries, drained, known, joined;
     uint32_t tmem;
@@ -928,7 +933,7 @@ cudaError_t launch_requests(AttendLaunch a, AttendParts w, int32_t first, int32_
     const int head_tiles = (a.H + HEADS - 1) / HEADS;
     int64_t cost;
     w.splits = choose_splits((int64_t)count * head_tiles, w.tiles, cap, &cost);
-    w.split_inv = 65536u / (unsigned)w.splits + 1u;
+    w.split_inv = inverse_of(w.splits);
     w.rows_per_split = (w.tiles + w.splits - 1) / w.splits * TILE;
     w.whole = w.splits == 1 && a.H <= HEADS;
     const cudaError_t e = launch_behind(a.dtype == kBf16 ? attend_kernel<kBf16> : attend_kernel<kF16>,

@@ -207,7 +207,7 @@ __device__ __forceinline__ float query_factor(const AttendLaunch &a, int e)
 struct AttendParts {
     int splits;             // CTAs a request's (or head tile's) rows are split over: a cluster
     int rows_per_split;
-    uint32_t split_inv;     // n / splits = n * split_inv >> 16 for n up to 64
+    uint32_t split_inv;     // n / splits = n * split_inv >> 16 for n below HEADS + MAX_SPLITS
     float *lse2;            // [R][H] log2 of the sums, for the weights
     // Base-2 scores, for the weights: [R][head_blocks][tiles] blocks of 16 heads
     // by 64 rows, each as a warp holds it: [8][32 lanes][4], where lane's four
@@ -297,21 +297,27 @@ struct Join {
     uint32_t split_inv;
     bool staged;
 
-    __device__ __forceinline__ int over_splits(int n) const { return (int)(n * split_inv >> 16); }
-    __device__ __forceinline__ int count(int owner) const { return over_splits(heads - owner + splits - 1); }
+    __host__ __device__ __forceinline__ int over_splits(int n) const { return (int)(n * split_inv >> 16); }
+    __host__ __device__ __forceinline__ int count(int owner) const { return over_splits(heads - owner + splits - 1); }
     // The own part of the CTA's m-th head, and the first that another sends it.
-    __device__ __forceinline__ uint32_t own(int m) const { return slots + (staged ? rank + m * splits : m) * O_STRIDE; }
-    __device__ __forceinline__ uint32_t others(int owner, int m) const
+    __host__ __device__ __forceinline__ uint32_t own(int m) const { return slots + (staged ? rank + m * splits : m) * O_STRIDE; }
+    __host__ __device__ __forceinline__ uint32_t others(int owner, int m) const
     {
         return slots + ((staged ? heads : count(owner)) + m * (splits - 1)) * O_STRIDE;
     }
     // Where this CTA's part of owner's m-th head goes: in owner, if that is another.
-    __device__ __forceinline__ uint32_t place(int owner, int m) const
+    __host__ __device__ __forceinline__ uint32_t place(int owner, int m) const
     {
         return owner == rank ? own(m) : others(owner, m) + (rank - (rank > owner)) * O_STRIDE;
     }
+    // Where this CTA's reference and sum of head i go in owner's ml: a head's own
+    // first, then the others' in the order of their parts.
+    __host__ __device__ __forceinline__ int ml_at(int i, int owner) const
+    {
+        return owner == rank ? i - owner : i - owner + rank + (rank < owner);
+    }
     // What the others send a CTA.
-    __device__ __forceinline__ uint32_t parts() const { return count(rank) * (splits - 1); }
+    __host__ __device__ __forceinline__ uint32_t parts() const { return count(rank) * (splits - 1); }
     // Staged parts to their owners.  Every CTA's slots must be free to take them.
     __device__ __forceinline__ void send(int warp, int warps, int lane) const
     {
@@ -331,9 +337,9 @@ struct Join {
     {
         const int owner = i - over_splits(i) * splits;
         if (owner == rank)
-            ml[i - owner] = make_float2(m, l);
+            ml[ml_at(i, owner)] = make_float2(m, l);
         else
-            send_v2(in_cta(smem_u32(&ml[i - owner + rank + (rank < owner)]), owner), __float_as_uint(m), __float_as_uint(l),
+            send_v2(in_cta(smem_u32(&ml[ml_at(i, owner)]), owner), __float_as_uint(m), __float_as_uint(l),
                     in_cta(known, owner));
     }
     // Once all references and sums are here: each part's factor 2^(m_p - m) / sum_p
