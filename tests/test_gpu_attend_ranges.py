@@ -56,3 +56,33 @@ def test_strides_of_a_single_head_or_request_mean_nothing(R, heads, k):
     acc = torch.zeros((R, D), device="cuda")
     H.attend(odd(q, 576), odd_rows, ids, odd(out, 512), 0.05, weights=acc, positions=ids)
     check(q, rows, ids, out, float(np.float32(0.05)), "bf16", None, acc, torch.zeros_like(acc), ids)
+
+
+@pytest.mark.parametrize("heads", [257, 960, 1000, 1024])
+def test_as_many_heads_as_a_call_takes(heads):
+    call(2, heads, 150, 170, "f16" if heads % 2 else "bf16", seed=heads, pad=0.1, weights=True)
+
+
+def test_as_many_heads_and_rows_as_a_call_takes():
+    call(1, 1024, 8192, 8192, "bf16", seed=1, weights=True)
+
+
+@pytest.mark.parametrize("R,heads,k", [(8192, 3, 5), (8192, 66, 70), (8191, 17, 1)])
+def test_as_many_requests_as_a_call_takes(R, heads, k):
+    """Compared: the first, the last, those around whole waves, and some between."""
+    D, tokens = k + 4, 2 * k + 20
+    rows = make_rows(R * D, "bf16", 1).view(R, D, 416)
+    q = make_q(R, heads, "bf16", 2)
+    order = torch.rand((R, D), device="cuda").argsort(1)
+    ids = order[:, :k].int().contiguous()
+    ids[::7, 0] = -1
+    pos = torch.rand((R, tokens), device="cuda").argsort(1)[:, :k].int().contiguous()
+    out = torch.empty((R, heads, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((R, heads), device="cuda")
+    acc = torch.rand((R, tokens), device="cuda")
+    before, status = acc.clone(), torch.zeros(R, dtype=torch.int32, device="cuda")
+    H.attend(q, rows, ids, out, 0.05, lse=lse, weights=acc, positions=pos, status=status)
+    some = sorted({0, 1, 151, 152, 153, 4095, 4096, R - 2, R - 1, *range(R // 152 * 152 - 3, min(R // 152 * 152 + 3, R)),
+                   *np.random.default_rng(R).integers(0, R, 100).tolist()})
+    check(q, rows, ids, out, float(np.float32(0.05)), "bf16", lse, acc, before, pos, requests=some)
+    assert (status == 0).all()
