@@ -11,10 +11,9 @@
 namespace hs {
 
 constexpr int kLatent = 512, kRope = 64, kRowValues = kLatent + kRope;
-constexpr int kScaleAt = 256, kRopeAt = 288, kRow4Bytes = 416;
+constexpr int kScaleAt = 256, kRopeAt = 288;
 constexpr int kBf16 = 0, kF16 = 1;
 constexpr int kStatusAttendTimeout = 9;
-constexpr int kMaxHeads = 1024;
 
 // 8 codes (one 32-bit word of a row) as four f16 pairs in value order:
 // pair j holds codes 2j and 2j + 1.

@@ -132,14 +132,7 @@ __device__ __forceinline__ void tmem_st_16x64(uint32_t at, const uint32_t (&v)[3
                  : "memory");
 }
 
-// The same for 32 and for 8 columns.
-__device__ __forceinline__ void tmem_ld_16x32(uint32_t at, uint32_t (&v)[16])
-{
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : HS_R4(v, 0), HS_R4(v, 4), HS_R4(v, 8), HS_R4(v, 12)
-                 : "r"(at));
-}
-
+// The same for 8 and for 32 columns.
 __device__ __forceinline__ void tmem_ld_16x8(uint32_t at, uint32_t (&v)[4])
 {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];" : HS_R4(v, 0) : "r"(at));
