@@ -661,12 +661,17 @@ def _attend(q, rows, rows_at, row_stride, request_stride, R, D, slot_ids, out, s
         acc, where = (weights.data_ptr(), stride, tokens), (positions.data_ptr(), positions_stride)
     words = _words(status, R)
     device = _current_device()
-    for x in (q, rows, out, lse, weights, resident_rows, workspace, status):
-        if x is not None and not isinstance(x, int) and x.get_device() != device:
-            raise ValueError(f"only slot_ids and positions may be outside the current device, {device}")
-    for x in (slot_ids, positions):
-        if x is not None and x.get_device() not in (device, -1):
-            raise ValueError(f"slot_ids and positions must be on device {device} or pinned")
+    if (q.get_device() != device or out.get_device() != device
+            or rows is not None and rows.get_device() != device
+            or lse is not None and lse.get_device() != device
+            or weights is not None and weights.get_device() != device
+            or resident_rows is not None and resident_rows.get_device() != device
+            or workspace is not None and workspace.get_device() != device
+            or words and status is not words and status.get_device() != device):
+        raise ValueError(f"only slot_ids and positions may be outside the current device, {device}")
+    if (slot_ids.get_device() not in (device, -1)
+            or positions is not None and positions.get_device() not in (device, -1)):
+        raise ValueError(f"slot_ids and positions must be on device {device} or pinned")
     launch_stream = _stream(stream)
     if workspace is None:
         workspace = _allocate(attend_workspace_bytes(R, H, k, weights is not None), q.device,
@@ -676,8 +681,8 @@ def _attend(q, rows, rows_at, row_stride, request_stride, R, D, slot_ids, out, s
     args = _pack_attend_args(
         R, H, k, dt, q.data_ptr(), strides[0], strides[1], rows_at, row_stride, request_stride, D, scale,
         slot_ids.data_ptr(), ids_stride, *resident, out.data_ptr(), out_strides[0], out_strides[1],
-        _addr(lse) or 0, *acc, *where, words, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size())
+        0 if lse is None else lse.data_ptr(), *acc, *where, words, workspace.data_ptr(),
+        workspace.nbytes)
     _check((_lib or load_library()).hisparse_attend(args, launch_stream), "hisparse_attend")
 
 
