@@ -11,9 +11,17 @@
 // Exactness.  A latent value (e2m1 times e4m3) has at most six significant
 // bits, so the decoded tile is exact in f16, scaled by 2^-7 (see decode8).
 // A query row is multiplied by a power of two that brings its largest value
-// to [1, 2), and is then exact in f16 down to 2^-22 of that; the rope parts
-// stay in the model's type.  Scores, sums and O are 32-bit; probabilities
-// enter the second product as f16 (relative step 2^-11).
+// to [1, 2) ([2, 4) from 2^127 on).  Its latent part, with another 2^7, is then
+// exact in f16 down to 2^-22 of that value, its rope part in bf16, or in f16 down
+// to 2^-14; below, values round to multiples of 2^-31 and 2^-24 of it, the latter
+// the step of a 32-bit number that size.
+// Scores, sums and O are 32-bit; probabilities enter the second product as f16,
+// relative to the reference (the largest lies between it and 2^8 times it): half
+// a step is 2^-11 of a probability, and below 2^-14 of the reference 2^-25 of
+// the latter (less is dropped; l keeps all in 32 bits).  The product's other
+// operand is f16 and the two have one type, that with the most bits at its rate.
+// The error of out against 64 bits is that of the plain 32-bit form in bf16, and
+// a quarter more in f16 (2.6 against 2.1 x 10^-4, 37 requests of 40 heads).
 //
 // One CTA takes up to 64 heads of one request over a range of its rows, 64
 // rows a tile, three tiles in shared memory:
@@ -318,7 +326,7 @@ __global__ void __launch_bounds__(WT_NT, 6) weights_kernel(const __grid_constant
 {
     const int t = blockIdx.x, r = blockIdx.y, j = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
     WeightRow row;
-    row.load(a, r, t, j, lane);      // (inputs: they do not wait for the launch before)
+    row.load(a, r, t, j, lane);      // (inputs, ahead of the wait: see launch_behind)
     after_launch_before();
     const float4 *s = scores_at(w, r, t, j, lane);
     const float *lse2 = w.lse2 + (int64_t)r * a.H;
@@ -480,8 +488,8 @@ __global__ void __launch_bounds__(AT_NT, 1) attend_kernel(const __grid_constant_
         __syncwarp();
         tmem_alloc_all(smem_u32(&sm.tmem));
         after_launch_before();
-        // this call's own next launch may be placed now (the inputs that it reads
-        // are there); it waits for this grid
+        // this call's own next launch may be placed now: after this wait, as it
+        // reads inputs ahead of its own (see launch_behind)
         if (a.weights && !w.whole) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
     tc_fence_before();

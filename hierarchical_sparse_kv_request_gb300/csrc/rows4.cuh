@@ -76,7 +76,11 @@ cudaError_t launch_attend(const AttendLaunch &a, int64_t workspace_bytes, bool *
 // A launch that may be set up while the stream's last kernel ends; the kernel
 // reads and writes nothing before after_launch_before(), which waits for that
 // one's completion.  (70,001 rows packed and unpacked, call after call: 33.2
-// against 38.1 us.)  cluster: CTAs along x.
+// against 38.1 us.)  One exception: weights_kernel reads its ids and positions
+// ahead of its wait.  It always follows attend_kernel, which lets it start only
+// once every CTA has waited for the launch before; whatever wrote those two
+// arrays is complete by then, and attend_kernel does not write them.  cluster:
+// CTAs along x.
 template <class... P, class... A>
 cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t s,
                           const A &...args)

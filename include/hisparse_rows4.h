@@ -44,7 +44,8 @@ extern "C" {
 #define HISPARSE_F16 1
 
 /* Status code (see hisparse_status): an attention kernel's own bounded wait
- * ran out (not expected; the request's outputs are not valid). */
+ * ran out (not expected; the request's outputs and the weights added by the
+ * call are not valid). */
 #define HISPARSE_STATUS_ATTEND_TIMEOUT 9
 
 /* Most rows of one hisparse_pack_rows or hisparse_unpack_rows. */
@@ -133,14 +134,21 @@ typedef struct hisparse_attend_args {
  * A request that names nothing gets out = 0, lse = -inf and no weight.  A
  * row may be named twice (it counts twice).  Products accumulate in 32 bits;
  * probabilities enter the second product as f16 relative to a running
- * maximum, everything else of the softmax is 32-bit; out is rounded once.
+ * maximum (half a step: 2^-11 of a probability, and never less than 2^-25 of
+ * that maximum: far smaller ones are dropped from out, not from lse and
+ * weights), everything else of the softmax is 32-bit; out is rounded once.
+ * Queries are exact down to 2^-22 (rope values in f16: 2^-14) of the largest
+ * value of their head, and rounded to 2^-31 (2^-24) of it below.
  * Results do not depend on the batch's other requests' values, and a call
  * repeated on the same inputs gives the same bits if each request's positions
  * are distinct.
  * Ids outside these ranges are skipped and recorded in status: BAD_INDEX for
  * an id below -1 or a slot >= D, BAD_RESIDENT for a flagged id past
  * resident_count, BAD_POSITION for a named row's position outside
- * [0, weights_tokens) (its weight is dropped).
+ * [0, weights_tokens) (its weight is dropped).  With status NULL
+ * neither these nor ATTEND_TIMEOUT leave a trace.
+ * A NaN scale gives NaN wherever a row is named.  One to four launches,
+ * capturable.
  * Errors: INVALID_ARG, UNSUPPORTED (H or k beyond the limits), ALIGNMENT
  * (q, rows, resident_rows, out or workspace not 16-byte aligned), CAPACITY
  * (workspace too small), CUDA.
