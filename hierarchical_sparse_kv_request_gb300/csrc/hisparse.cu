@@ -1047,6 +1047,13 @@ int hisparse_get_copy_ctas(hisparse_t h, int32_t *ctas)
     return HISPARSE_OK;
 }
 
+int hisparse_get_device(hisparse_t h, int32_t *device)
+{
+    if (!h || !device) return HISPARSE_ERR_INVALID_ARG;
+    *device = h->device;
+    return HISPARSE_OK;
+}
+
 int hisparse_set_programmatic_launch(hisparse_t h, int32_t on)
 {
     if (!h || (on != 0 && on != 1)) return HISPARSE_ERR_INVALID_ARG;

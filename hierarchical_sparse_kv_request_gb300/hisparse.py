@@ -129,6 +129,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "hisparse_set_programmatic_launch": [P, I32],
         "hisparse_set_copy_ctas": [P, I32],
         "hisparse_get_copy_ctas": [P, P],
+        "hisparse_get_device": [P, P],
         "hisparse_check_guards": [P, P],
         "hisparse_version": [],
         "hisparse_synthetic_compute": [P, I64, I32, I32, P],
@@ -238,7 +239,9 @@ class HiSparse:
         else:
             _check(self.lib.hisparse_create(ctypes.byref(lay), ctypes.byref(h)), "hisparse_create")
         self.h = h
-        self.device = _current_device()
+        device = ctypes.c_int32(-1)
+        _check(self.lib.hisparse_get_device(self.h, ctypes.byref(device)), "hisparse_get_device")
+        self.device = device.value
 
     @classmethod
     def for_workload(cls, w, host_block_tokens: int = 0) -> "HiSparse":

@@ -528,6 +528,12 @@ int hisparse_set_copy_ctas(hisparse_t h, int32_t ctas);
 int hisparse_get_copy_ctas(hisparse_t h, int32_t *ctas);
 
 /*
+ * hisparse_get_device: *device <- the device that the handle belongs to (the
+ * one current at its creation).  INVALID_ARG for a null pointer.
+ */
+int hisparse_get_device(hisparse_t h, int32_t *device);
+
+/*
  * hisparse_set_programmatic_launch: on = 1 launches the swap-in's resolve grid
  * and the backups with a programmatic dependency on the previous kernel of
  * the stream (programmatic dependent launch): when that kernel signals its

@@ -58,3 +58,9 @@ def test_the_default_stream_by_its_address():
     H.attend(q, rows, ids, out, 0.05, weights=acc, positions=ids, stream=0)
     torch.cuda.synchronize()
     check(q, rows, ids, out, float(np.float32(0.05)), "bf16", None, acc, torch.zeros_like(acc), ids)
+
+
+def test_a_handle_knows_its_device():
+    hs = H.HiSparse(2, 1, H.ROW4_BYTES, 4, 8, host_to_device_ratio=2, host_capacity=[16, 16])
+    assert hs.device == torch.cuda.current_device()
+    hs.close()

@@ -2,6 +2,7 @@
 part played by fakes (CPU only): the library's calls are recorded instead of
 made, and torch's allocator and streams by what they were asked for."""
 
+import ctypes
 import types
 
 import pytest
@@ -178,3 +179,24 @@ def test_only_ids_and_positions_may_be_host_tensors(gpu, monkeypatch):
         t[name] = t[name].as_subclass(Elsewhere)
     H.attend(**t, scale=1.0, workspace=torch.zeros(1 << 16, dtype=torch.uint8).as_subclass(Elsewhere))
     assert len(gpu.launches) == 1
+
+
+def test_a_handle_is_made_without_torch(monkeypatch):
+    """Its device is the library's to say; torch is loaded by calls that need it."""
+    def get_device(h, device):
+        device._obj.value = 3
+        return H.OK
+
+    def load():
+        raise AssertionError("torch is not needed here")
+
+    monkeypatch.setattr(H, "_torch", None)
+    monkeypatch.setattr(H, "_device", None)
+    monkeypatch.setattr(H, "_load_torch", load)
+    monkeypatch.setattr(H, "_lib", types.SimpleNamespace(hisparse_create=lambda layout, h: H.OK,
+                                                         hisparse_get_device=get_device))
+    assert H.HiSparse(2, 1, H.ROW4_BYTES, 4, 8, 1, [16, 16]).device == 3
+
+
+def test_get_device_refuses_null(lib):
+    assert lib.hisparse_get_device(None, ctypes.byref(ctypes.c_int32())) == H.ERR_INVALID_ARG
