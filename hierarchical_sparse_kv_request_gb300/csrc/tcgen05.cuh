@@ -61,7 +61,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 
 // The long part of a wait, kept out of line: the attention kernel's loops have
 // to stay in the instruction cache.
-__device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int *gave_up)
+inline __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int *gave_up)
 {
     uint64_t t0, t;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));

@@ -41,6 +41,10 @@ ROW4_LATENT, ROW4_ROPE, ROW4_VALUES, ROW4_BYTES = 512, 64, 576, 416
 BF16, F16 = 0, 1
 MAX_HEADS = 1024
 
+# resident pages (include/hisparse_pages.h)
+ROW8_BYTES, ROW16_BYTES = 656, 1152
+MAX_PREFIX = 1 << 20
+
 
 class HiSparseError(RuntimeError):
     def __init__(self, code: int, what: str):
@@ -83,9 +87,47 @@ class AttendArgs(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
-_pack_attend_args = struct.Struct("@" + "".join(
-    {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_void_p: "P"}[t]
-    for _, t in AttendArgs._fields_)).pack
+class PageTablesArgs(ctypes.Structure):
+    """hisparse_page_tables_args."""
+    _fields_ = [("num_requests", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("num_shared", ctypes.c_int32),
+                ("lens", ctypes.c_void_p), ("tables", ctypes.c_void_p),
+                ("tables_stride", ctypes.c_int64), ("held", ctypes.c_void_p),
+                ("free_list", ctypes.c_void_p), ("free_capacity", ctypes.c_int32),
+                ("free_count", ctypes.c_void_p), ("shared", ctypes.c_void_p),
+                ("new_tokens", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("num_tokens", ctypes.c_int32), ("status", ctypes.c_void_p)]
+
+
+class AttendPrefixArgs(ctypes.Structure):
+    """hisparse_attend_prefix_args."""
+    _fields_ = [("num_requests", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("row_bytes", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("q_request_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64),
+                ("rows", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("num_rows", ctypes.c_int64), ("table", ctypes.c_void_p),
+                ("block_size", ctypes.c_int32), ("prefix_len", ctypes.c_int32),
+                ("scale", ctypes.c_float),
+                ("part", ctypes.c_void_p), ("part_request_stride", ctypes.c_int64),
+                ("part_head_stride", ctypes.c_int64), ("part_lse", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("out_request_stride", ctypes.c_int64),
+                ("out_head_stride", ctypes.c_int64), ("lse", ctypes.c_void_p),
+                ("status", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+def _packer(args):
+    """struct.pack with the layout of a ctypes structure."""
+    return struct.Struct("@" + "".join(
+        {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_void_p: "P"}[t]
+        for _, t in args._fields_)).pack
+
+
+_pack_attend_args = _packer(AttendArgs)
+_pack_page_tables_args = _packer(PageTablesArgs)
+_pack_attend_prefix_args = _packer(AttendPrefixArgs)
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -141,6 +183,11 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "hisparse_attend_workspace": [I32, I32, I32, I32, P],
         "hisparse_evict_select": [I32, I32, P, I64, I64, P, P, I32, I32, P, P, P, P],
         "hisparse_evict": [P, I32, P, I64, I64, P, I32, I32, P, P, P, P],
+        "hisparse_page_tables": [P, P],
+        "hisparse_norm_rows": [P, I64, I32, I64, P, ctypes.c_float, P, I64, I32, I64, P, P],
+        "hisparse_gather_rows": [P, I64, I32, I64, P, I64, P, I64, I32, P],
+        "hisparse_attend_prefix": [P, P],
+        "hisparse_attend_prefix_workspace": [I32, I32, I32, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -706,6 +753,181 @@ def evict_select(weights, slot2tok, seq_lens, out_slots, out_counts, keep_recent
         R, D, weights.data_ptr(), stride, tokens, slot2tok.data_ptr(),
         seq_lens.data_ptr(), keep_recent, n, _addr(want), out_slots.data_ptr(),
         out_counts.data_ptr(), _stream(stream)), "hisparse_evict_select")
+
+
+# -- resident pages (include/hisparse_pages.h) ------------------------------
+
+def _here(device: int, **tensors) -> None:
+    """Tensors (None: not there) are on the current device."""
+    for name, x in tensors.items():
+        if x is not None and x.get_device() != device:
+            raise ValueError(f"{name} is not on the current device, {device}")
+
+
+def _reachable(device: int, **tensors) -> None:
+    """Tensors (None: not there) are on the current device or in pinned memory."""
+    for name, x in tensors.items():
+        if x is not None and x.get_device() != device and not (x.get_device() == -1 and x.is_pinned()):
+            raise ValueError(f"{name} is neither on the current device, {device}, nor pinned")
+
+
+def _line(x, what: str) -> int:
+    """Length of x, a contiguous int32 tensor of one dimension."""
+    if x.dtype is not (_torch or _load_torch()).int32 or len(x.shape) != 1 or not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of one dimension")
+    return x.shape[0]
+
+
+def page_tables(lens, tables, held, free_list, free_count, block_size: int, shared=None,
+                new_tokens=None, offsets=None, slots=None, positions=None, status=None,
+                stream=None) -> None:
+    """hisparse_page_tables: brings the block tables (int32 [R][blocks], held
+    int32 [R] entries of each in use) to the lengths lens (int32 [R]; negative:
+    left alone), with free pages from and back to free_list (int32 [pages],
+    free_count int32 [1]); shared: int32 page ids of a common prefix.  With
+    new_tokens (int32 [R]) also offsets (int32 [R + 1]), slots and positions
+    (int32 [tokens]; positions may be None) of the last new_tokens[r] tokens of
+    each request.  status int32 [R] or None.  On the current device; lens,
+    new_tokens and shared also in pinned host memory."""
+    R = _line(lens, "lens")
+    blocks, stride = _rows_of(tables, "tables", "int32", R)
+    if _line(held, "held") != R or _line(free_count, "free_count") != 1:
+        raise ValueError(f"held must have {R} entries and free_count one")
+    capacity = _line(free_list, "free_list")
+    prefix = 0 if shared is None else _line(shared, "shared")
+    tokens = 0
+    if new_tokens is not None:
+        if _line(new_tokens, "new_tokens") != R:
+            raise ValueError(f"new_tokens must have {R} entries")
+        if offsets is None or slots is None:
+            raise ValueError("new_tokens need offsets and slots")
+        tokens = _line(slots, "slots")
+        if _line(offsets, "offsets") != R + 1 or positions is not None and _line(positions, "positions") != tokens:
+            raise ValueError(f"offsets must have {R + 1} entries, and positions as many as slots")
+    elif offsets is not None or slots is not None or positions is not None:
+        raise ValueError("offsets, slots and positions need new_tokens")
+    words = _words(status, R)
+    device = _current_device()
+    _here(device, tables=tables, held=held, free_list=free_list, free_count=free_count, offsets=offsets,
+          slots=slots, positions=positions, status=None if isinstance(status, int) else status)
+    _reachable(device, lens=lens, new_tokens=new_tokens, shared=shared)
+    at = _addr
+    args = _pack_page_tables_args(
+        R, blocks, block_size, prefix, lens.data_ptr(), tables.data_ptr(), stride, held.data_ptr(),
+        free_list.data_ptr(), capacity, free_count.data_ptr(), at(shared) or 0, at(new_tokens) or 0,
+        at(offsets) or 0, at(slots) or 0, at(positions) or 0, tokens, words)
+    _check((_lib or load_library()).hisparse_page_tables(args, _stream(stream)), "hisparse_page_tables")
+
+
+def _format_rows(rows, what: str):
+    """Count, stride and format of rows, uint8 [count][416, 656 or 1152]."""
+    shape = rows.shape
+    if rows.dtype is (_torch or _load_torch()).uint8 and len(shape) == 2 and shape[1] in (
+            ROW4_BYTES, ROW8_BYTES, ROW16_BYTES):
+        stride, one = rows.stride()
+        if one == 1:
+            return shape[0], stride if shape[0] > 1 else shape[1], shape[1]
+    raise ValueError(f"{what} must be uint8 [...][{ROW4_BYTES}, {ROW8_BYTES} or {ROW16_BYTES}] with contiguous rows")
+
+
+def _row_values(values, rows, slots):
+    dt = _dtype16(values, "values")
+    shape, strides = values.shape, values.stride()
+    if len(shape) != 2 or shape[1] != ROW4_VALUES or strides[1] != 1:
+        raise ValueError(f"values must be [n][{ROW4_VALUES}] with contiguous rows")
+    n = shape[0]
+    count, stride, row_bytes = _format_rows(rows, "rows")
+    if slots is not None:
+        if _line(slots, "slots") != n:
+            raise ValueError(f"slots must have {n} entries")
+    elif count < n:
+        raise ValueError("more values than rows")
+    _reachable(_current_device(), values=values, rows=rows, slots=slots)
+    return dt, n, strides[0] if n > 1 else ROW4_VALUES, count, stride, row_bytes
+
+
+def norm_rows(values, rows, slots=None, weight=None, eps: float = 1e-6, stream=None) -> None:
+    """hisparse_norm_rows: rows[slots[i]] (uint8 [count][416, 656 or 1152]) <-
+    values[i] (bf16 or f16 [n][576]), the 512 latent values divided by their root
+    mean square and times weight ([512] of that type; None: stored as they are),
+    in the rows' format.  slots int32 [n] (negative: not stored) or None: row i.
+    On the current device or in pinned host memory."""
+    dt, n, vs, count, rs, row_bytes = _row_values(values, rows, slots)
+    if weight is not None:
+        if weight.dtype is not values.dtype or weight.shape != (ROW4_LATENT,) or not weight.is_contiguous():
+            raise ValueError(f"weight must be a contiguous [{ROW4_LATENT}] of the values' type")
+        _reachable(_current_device(), weight=weight)
+    _check((_lib or load_library()).hisparse_norm_rows(
+        values.data_ptr(), vs, dt, n, _addr(weight), eps, rows.data_ptr(), rs, row_bytes, count,
+        _addr(slots), _stream(stream)), "hisparse_norm_rows")
+
+
+def gather_rows(rows, values, slots=None, stream=None) -> None:
+    """hisparse_gather_rows: values[i] (bf16 or f16 [n][576]) <- what
+    rows[slots[i]] stands for; arguments as norm_rows()."""
+    dt, n, vs, count, rs, row_bytes = _row_values(values, rows, slots)
+    _check((_lib or load_library()).hisparse_gather_rows(
+        rows.data_ptr(), rs, row_bytes, count, _addr(slots), n, values.data_ptr(), vs, dt,
+        _stream(stream)), "hisparse_gather_rows")
+
+
+def attend_prefix_workspace_bytes(num_requests: int, num_heads: int, prefix_len: int) -> int:
+    """Bytes of workspace that attend_prefix() needs for these sizes."""
+    n = ctypes.c_int64()
+    _check(load_library().hisparse_attend_prefix_workspace(num_requests, num_heads, prefix_len,
+                                                           ctypes.byref(n)),
+           "hisparse_attend_prefix_workspace")
+    return n.value
+
+
+def attend_prefix(q, rows, table, block_size: int, prefix_len: int, out, scale: float, lse=None,
+                  part=None, part_lse=None, status=None, workspace=None, stream=None) -> None:
+    """hisparse_attend_prefix: attention of all requests over the prefix_len
+    tokens whose pages table (int32 [blocks]) names, joined with `part`.
+
+    q [R][H][576], out and part (or None) [R][H][512] in bf16 or f16; rows uint8
+    [count][416, 656 or 1152], the pool of pages of block_size rows; lse and
+    part_lse float32 [R][H] (lse may be None, part_lse goes with part; part and
+    part_lse may be out and lse); status int32 [R] or None; workspace a uint8
+    tensor of attend_prefix_workspace_bytes (None: allocated for this call, on
+    its stream).  All of them on the current device, table also in pinned host
+    memory."""
+    dt = _dtype16(q, "q")
+    shape, strides = q.shape, q.stride()
+    if len(shape) != 3 or shape[2] != ROW4_VALUES or strides[2] != 1:
+        raise ValueError(f"q must be [R][H][{ROW4_VALUES}] with contiguous heads")
+    R, H = shape[0], shape[1]
+    places = []
+    for name, x in (("out", out), ("part", part)):
+        places.append((0, 0, 0))
+        if x is not None:
+            s = x.stride()
+            if x.dtype is not q.dtype or x.shape != (R, H, ROW4_LATENT) or s[2] != 1:
+                raise ValueError(f"{name} must be [{R}][{H}][{ROW4_LATENT}] of q's type with contiguous heads")
+            places[-1] = (x.data_ptr(), s[0], s[1])
+    for name, x in (("lse", lse), ("part_lse", part_lse)):
+        if x is not None and (x.dtype is not _torch.float32 or x.shape != (R, H) or not x.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape ({R}, {H})")
+    if (part is None) != (part_lse is None):
+        raise ValueError("part and part_lse go together")
+    count, row_stride, row_bytes = _format_rows(rows, "rows")
+    if block_size < 1 or _line(table, "table") * block_size < prefix_len:
+        raise ValueError(f"table names fewer than {prefix_len} tokens")
+    words = _words(status, R)
+    device = _current_device()
+    _here(device, q=q, rows=rows, out=out, part=part, lse=lse, part_lse=part_lse, workspace=workspace,
+          status=None if isinstance(status, int) else status)
+    _reachable(device, table=table)
+    launch_stream = _stream(stream)
+    if workspace is None:
+        workspace = _allocate(attend_prefix_workspace_bytes(R, H, prefix_len), q.device, stream, launch_stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    args = _pack_attend_prefix_args(
+        R, H, dt, row_bytes, q.data_ptr(), strides[0], strides[1], rows.data_ptr(), row_stride, count,
+        table.data_ptr(), block_size, prefix_len, scale, *places[1], 0 if part_lse is None else part_lse.data_ptr(),
+        *places[0], 0 if lse is None else lse.data_ptr(), words, workspace.data_ptr(), workspace.nbytes)
+    _check((_lib or load_library()).hisparse_attend_prefix(args, launch_stream), "hisparse_attend_prefix")
 
 
 # -- measurement kernels (include/hisparse_measure.h) -----------------------
