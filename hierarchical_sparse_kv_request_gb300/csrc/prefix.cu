@@ -25,8 +25,8 @@
 // 576 values; in O += P V all keys, its own 256 values.  So a quarter of the tile is
 // used twice in one CTA, and 32 KB more come in for the second product, where the
 // first has freed shared memory:
-//   slots of 16 KB (64 keys by 128 values), four a tile, X0 Y0 X1 Y1, in a ring of
-//   ten; X_h are values 128 h, Y_h values 256 + 128 h and on, of the CTA's own keys.
+//   slots of 32 KB, two a tile (h = 0, 1), in a ring of five, of two parts: X_h are
+//   values 128 h, Y_h values 256 + 128 h and on, of the CTA's own 64 keys.
 //   After S the first CTA keeps X and gets, in Y, the other CTA's keys of its
 //   values X; the second keeps Y and gets, in X, the first one's keys of Y.  A
 //   descriptor is one for both CTAs: at X_h both have keys 0-63, at Y_h 64-127.
@@ -36,8 +36,8 @@
 // the other 192 in shared memory.
 //   warps 0-3  softmax: a thread a lane, that is a head and half of the tile's keys;
 //   warp 4     brings keys in, warp 5 the values of the other CTA's keys;
-//   warp 6     of the first CTA issues the MMAs, S of the next tile ahead of O of
-//              this one; that of the second says what has come in there.
+//   warp 6     of the first CTA issues the MMAs of S, warp 7 those of O; those of the
+//              second say what has come in there.
 // The heads' tiles in a row are cut evenly among the pairs, wherever a head ends.
 #include <atomic>
 #include <mutex>
@@ -50,25 +50,25 @@ namespace {
 constexpr int PAIR_HEADS = 128, CTA_HEADS = 64, KEYS = 128;
 constexpr int MAX_PAIRS = 76;                    // pairs of SMs of a GB300
 constexpr uint32_t BLOCK = 64 * 128;             // 64 values of 64 keys, swizzled
-constexpr uint32_t SLOT = 2 * BLOCK;
-constexpr uint32_t HALF_TILE = 9 * BLOCK;        // 64 keys: X0 Y0 X1 Y1 rope
+constexpr uint32_t PART = 2 * BLOCK, SLOT = 2 * PART;
+constexpr uint32_t HALF_TILE = 9 * BLOCK;        // 64 keys: X0 Y0 X1 Y1 rope, as they go into the slots
 constexpr uint32_t TILE_BYTES = 2 * HALF_TILE;
-constexpr int SLOTS = 10, ROPES = 3;
+constexpr int SLOTS = 5, ROPES = 3;
 constexpr int Q_TMEM = 6, Q_SMEM = 9 - Q_TMEM;   // blocks of the queries
 
 constexpr uint32_t ROPE_AT = SLOTS * SLOT, Q_AT = ROPE_AT + ROPES * BLOCK, P_AT = Q_AT + Q_SMEM * BLOCK;
 constexpr uint32_t MISC_AT = P_AT + 2 * BLOCK;
-constexpr int PX_NT = 256, SOFTMAX = 4, KEY_WARP = 4, VALUE_WARP = 5, MMA_WARP = 6;
+constexpr int PX_NT = 256, SOFTMAX = 4, KEY_WARP = 4, VALUE_WARP = 5, SCORE_WARP = 6;
 
 // columns of tensor memory
 constexpr uint32_t T_O = 0, T_S = 256, T_Q = 320;
 
 struct PrefixSmem {
-    uint64_t keys[SLOTS], ropes[ROPES], values[4];      // arrived (in the first CTA: in both)
+    uint64_t keys[SLOTS], values[2];                    // arrived (in the first CTA: in both)
     uint64_t slot_free[SLOTS], rope_free[ROPES];        // the products that read it are done
     uint64_t scored[2], added;                          // S is there; O is
     uint64_t queries, read, weighed;                    // (in the first CTA, from both) Q is there, S read, P there
-    uint64_t drained;
+    uint64_t drained[2];
     uint32_t tmem;
     int gave_up;
     float top[2][2][CTA_HEADS];      // [tile % 2][half of the keys]
@@ -114,6 +114,9 @@ __global__ void __launch_bounds__(EX_NT) expand_kernel(const __grid_constant__ P
     if (threadIdx.x == 0) there = 0, bad = 0;
     __syncthreads();
     after_launch_before();
+    // prefix_kernel may be placed now: after this wait, as it reads its queries ahead of
+    // its own
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int t0 = blockIdx.x * EX_KEYS + warp * EX_ROWS;
     int64_t row = -1;
     if (lane < EX_ROWS && t0 + lane < a.len) {
@@ -158,36 +161,12 @@ __global__ void __launch_bounds__(EX_NT) expand_kernel(const __grid_constant__ P
 
 // ---- pairs of CTAs ---------------------------------------------------------------
 
-__device__ __forceinline__ void arrive_in(uint32_t bar)      // in any CTA of the cluster
+// In any CTA of the cluster.  (Releases to the thread's own CTA: what the other's
+// tensor core reads is in that CTA's shared and tensor memory.  A release to the
+// cluster takes 900 cycles.)
+__device__ __forceinline__ void arrive_in(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool try_acquire(uint32_t bar, uint32_t parity)      // what another CTA has released
-{
-    uint32_t ok;
-    asm volatile("{\n"
-                 ".reg .pred p;\n"
-                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-                 "selp.u32 %0, 1, 0, p;\n"
-                 "}"
-                 : "=r"(ok)
-                 : "r"(bar), "r"(parity)
-                 : "memory");
-    return ok != 0;
-}
-
-__device__ __forceinline__ bool wait_acquire(uint32_t bar, uint32_t parity, volatile int *gave_up)
-{
-    if (try_acquire(bar, parity)) return true;
-    return mbar_wait_long(bar, parity, gave_up) && try_acquire(bar, parity);
-}
-
-__device__ __forceinline__ void pair_sync()
-{
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
@@ -221,9 +200,9 @@ __device__ __forceinline__ void pair_commit(uint32_t bar)
                  : "memory");
 }
 
+// The mbarrier expects the bytes already.
 __device__ __forceinline__ void bring(uint32_t dst, const uint8_t *src, uint32_t bytes, uint32_t bar)
 {
-    mbar_expect(bar, bytes);
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
                  "r"(bytes), "r"(bar)
                  : "memory");
@@ -257,30 +236,27 @@ __device__ __forceinline__ float add_part(float &m, float &l, float part_lse, fl
     return f;
 }
 
-// Where a head's values go, or come from.
+// A head's request and number.
 struct HeadPlace {
     int r, h;
-    int64_t n;
-    __device__ __forceinline__ HeadPlace(const PrefixLaunch &a, int64_t row) : r((int)(row / a.H)), h((int)(row - (int64_t)r * a.H)), n(row) {}
+    __device__ __forceinline__ HeadPlace(const PrefixLaunch &a, int64_t head) : r((int)(head / a.H)), h((int)(head - (int64_t)r * a.H)) {}
 };
 
-template <int DT>
-__device__ __forceinline__ uint4 weighted8(const float (&o)[8], float f, uint4 part, float weight, bool joined)
+// Whether all threads that meet at a named barrier go on.  (Nothing limits this
+// wait: all of them come here, whatever has gone wrong.)
+__device__ __forceinline__ bool meet(int id, int threads, bool go)
 {
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = o[j] * f;
-    if (joined) {
-        const uint32_t p[4] = {part.x, part.y, part.z, part.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 v = pair_to_float<DT>(p[j]);
-            x[2 * j] = fmaf(v.x, weight, x[2 * j]);
-            x[2 * j + 1] = fmaf(v.y, weight, x[2 * j + 1]);
-        }
-    }
-    return make_uint4(floats_to_pair<DT>(x[0], x[1]), floats_to_pair<DT>(x[2], x[3]), floats_to_pair<DT>(x[4], x[5]),
-                      floats_to_pair<DT>(x[6], x[7]));
+    uint32_t all;
+    asm volatile("{\n"
+                 ".reg .pred p, q;\n"
+                 "setp.ne.u32 p, %1, 0;\n"
+                 "barrier.cta.red.and.pred q, %2, %3, p;\n"
+                 "selp.u32 %0, 1, 0, q;\n"
+                 "}"
+                 : "=r"(all)
+                 : "r"((uint32_t)go), "r"(id), "r"(threads)
+                 : "memory");
+    return all != 0;
 }
 
 template <int DT>
@@ -296,19 +272,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
     const int count = (int)(u1 - u0);      // tiles of this pair, over all its groups of heads
     auto bar = [](const uint64_t &b) { return smem_u32(&b); };
 
-    if (warp == MMA_WARP) {
+    if (warp == SCORE_WARP) {
         if (lane == 0) {
             const int both = rank == 0 ? 2 : 1;      // the first CTA also hears of the second
             for (int s = 0; s < SLOTS; ++s) mbar_init(bar(sm.keys[s]), both), mbar_init(bar(sm.slot_free[s]), 1);
-            for (int s = 0; s < ROPES; ++s) mbar_init(bar(sm.ropes[s]), both), mbar_init(bar(sm.rope_free[s]), 1);
-            for (int s = 0; s < 4; ++s) mbar_init(bar(sm.values[s]), both);
-            mbar_init(bar(sm.scored[0]), 1);
-            mbar_init(bar(sm.scored[1]), 1);
+            for (int s = 0; s < ROPES; ++s) mbar_init(bar(sm.rope_free[s]), 1);
+            for (int s = 0; s < 2; ++s) mbar_init(bar(sm.values[s]), both), mbar_init(bar(sm.scored[s]), 1);
             mbar_init(bar(sm.added), 1);
             mbar_init(bar(sm.queries), 2 * SOFTMAX);
             mbar_init(bar(sm.read), 2 * SOFTMAX);
             mbar_init(bar(sm.weighed), 2 * SOFTMAX);
-            mbar_init(bar(sm.drained), 1);
+            for (int s = 0; s < 2; ++s) mbar_init(bar(sm.drained[s]), 1);
             sm.gave_up = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
@@ -318,159 +292,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
     }
     tc_fence_before();
     __syncthreads();
-    pair_sync();
+    cluster_arrive();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
     volatile int *gave_up = &sm.gave_up;
     auto all = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
     bool ok = true;
-    after_launch_before();
+    cluster_wait();      // the other CTA's mbarriers are there, and its tensor memory
+    // (the softmax warps read the queries ahead of this wait: see expand_kernel)
+    if (warp >= SOFTMAX) after_launch_before();
 
-    if (warp == KEY_WARP) {
-        // ---- this CTA's keys of every tile ------------------------------------------
-        int slot = 0, rope = 0, n = 0, tile = (int)(u0 % w.tiles);
-        uint32_t slot_phase = 1, rope_phase = 1;      // (nothing to wait for the first time round)
-        for (; ok && n < count; ++n) {
-            const uint8_t *src = w.image + ((int64_t)tile * 2 + rank) * HALF_TILE;
-            for (int p = 0; ok && p < 4; ++p) {
-                if (!(ok = all(mbar_wait(bar(sm.slot_free[slot]), slot_phase, gave_up)))) break;
-                if (elect_one()) bring(base + slot * SLOT, src + p * SLOT, SLOT, bar(sm.keys[slot]));
-                __syncwarp();
-                if (++slot == SLOTS) slot = 0, slot_phase ^= 1;
-            }
-            if (!ok || !(ok = all(mbar_wait(bar(sm.rope_free[rope]), rope_phase, gave_up)))) break;
-            if (elect_one()) bring(base + ROPE_AT + rope * BLOCK, src + 4 * SLOT, BLOCK, bar(sm.ropes[rope]));
-            __syncwarp();
-            if (++rope == ROPES) rope = 0, rope_phase ^= 1;
-            if (++tile == w.tiles) tile = 0;
-        }
-    } else if (warp == VALUE_WARP) {
-        // ---- the other CTA's keys, for this one's values --------------------------------
-        int slot = rank == 0 ? 1 : 0, tile = (int)(u0 % w.tiles);      // Y0 or X0
-        for (int n = 0; ok && n < count; ++n) {
-            if (!(ok = all(mbar_wait(bar(sm.scored[n & 1]), (n >> 1) & 1, gave_up)))) break;
-            const uint8_t *src = w.image + ((int64_t)tile * 2 + (rank ^ 1)) * HALF_TILE + rank * SLOT;
-            if (elect_one())
-                for (int h = 0; h < 2; ++h) {
-                    int s = slot + 2 * h;
-                    if (s >= SLOTS) s -= SLOTS;
-                    bring(base + s * SLOT, src + h * 2 * SLOT, SLOT, bar(sm.values[(n & 1) * 2 + h]));
-                }
-            __syncwarp();
-            slot += 4;
-            if (slot >= SLOTS) slot -= SLOTS;
-            if (++tile == w.tiles) tile = 0;
-        }
-    } else if (warp == MMA_WARP && rank == 1) {
-        // ---- what has come in here, to the first CTA --------------------------------------
-        int slot = 0, rope = 0, tile = (int)(u0 % w.tiles);
-        uint32_t slot_phase = 0, rope_phase = 0;
-        auto tell = [&](const uint64_t &b, uint32_t phase) {
-            if (!(ok = ok && all(mbar_wait(bar(b), phase, gave_up)))) return;
-            if (lane == 0) arrive_in(in_cta(bar(b), 0));
-        };
-        auto keys = [&]() {
-            for (int p = 0; p < 4; ++p) {
-                tell(sm.keys[slot], slot_phase);
-                if (++slot == SLOTS) slot = 0, slot_phase ^= 1;
-            }
-            tell(sm.ropes[rope], rope_phase);
-            if (++rope == ROPES) rope = 0, rope_phase ^= 1;
-        };
-        bool ahead = false;      // the keys of tile n have been told of
-        for (int n = 0; ok && n < count; ++n) {
-            if (!ahead) keys();
-            ahead = n + 1 < count && tile + 1 < w.tiles;
-            if (ahead) keys();
-            for (int h = 0; h < 2; ++h) tell(sm.values[(n & 1) * 2 + h], (n >> 1) & 1);
-            if (++tile == w.tiles) tile = 0;
-        }
-    } else if (warp == MMA_WARP) {
-        // ---- MMA issue ------------------------------------------------------------------
-        constexpr uint32_t qk = mma_desc(128, KEYS, DT == kBf16, false), pv = mma_desc(128, 256, DT == kBf16, true);
-        int slot = 0, rope = 0, tile = (int)(u0 % w.tiles), group = 0;
-        uint32_t slot_phase = 0, rope_phase = 0;
-        auto wait = [&](const uint64_t &b, uint32_t phase) {
-            ok = ok && all(wait_acquire(bar(b), phase, gave_up));
-            return ok;
-        };
-        auto scores = [&](int n) {            // S = Q K^T of tile n
-            if (n > 0 && !wait(sm.read, (n - 1) & 1)) return;
-            uint32_t q_col = tmem + T_Q;
-            uint64_t q_desc = smem_desc(base + Q_AT, 16, 1024);
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                if (!wait(sm.keys[slot], slot_phase)) return;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t k_desc = smem_desc(base + slot * SLOT, 16, 1024);
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) {      // 16 values a step: 32 bytes, 8 columns
-                        const uint64_t k = k_desc + (x >> 2) * (BLOCK >> 4) + (x & 3) * 2;
-                        if (p < Q_TMEM / 2)
-                            pair_mma_ts(tmem + T_S, q_col + x * 8, k, qk, p + x > 0);
-                        else
-                            pair_mma(tmem + T_S, q_desc + (x >> 2) * (BLOCK >> 4) + (x & 3) * 2, k, qk, true);
-                    }
-                }
-                __syncwarp();
-                q_col += 64;
-                if (++slot == SLOTS) slot = 0, slot_phase ^= 1;
-            }
-            if (!wait(sm.ropes[rope], rope_phase)) return;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t k_desc = smem_desc(base + ROPE_AT + rope * BLOCK, 16, 1024);
-                q_desc += 2 * (BLOCK >> 4);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) pair_mma(tmem + T_S, q_desc + x * 2, k_desc + x * 2, qk, true);
-                pair_commit(bar(sm.scored[n & 1]));
-                pair_commit(bar(sm.rope_free[rope]));
-            }
-            __syncwarp();
-            if (++rope == ROPES) rope = 0, rope_phase ^= 1;
-        };
-        int v_slot = 0;
-        bool ahead = false, begins = true;
-        for (int n = 0; ok && n < count; ++n) {
-            if (begins) {
-                if (!wait(sm.queries, group & 1)) break;
-                ++group;
-            }
-            if (!ahead) scores(n);
-            ahead = n + 1 < count && tile + 1 < w.tiles;
-            if (ok && ahead) scores(n + 1);
-            if (!ok || !wait(sm.weighed, n & 1)) break;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {            // O += P V, 256 values
-                if (!wait(sm.values[(n & 1) * 2 + h], (n >> 1) & 1)) break;
-                tc_fence_after();
-                const int x_slot = v_slot, y_slot = v_slot + 1;      // (the ring has an even number of them)
-                if (elect_one()) {
-                    const uint64_t p_desc = smem_desc(base + P_AT, 16, 1024);
-                    const uint64_t x_desc = smem_desc(base + x_slot * SLOT, BLOCK, 1024);
-                    const uint64_t y_desc = smem_desc(base + y_slot * SLOT, BLOCK, 1024);
-#pragma unroll
-                    for (int x = 0; x < 8; ++x)      // 16 keys a step
-                        pair_mma(tmem + T_O + h * 128, p_desc + (x >> 2) * (BLOCK >> 4) + (x & 3) * 2,
-                                 (x < 4 ? x_desc : y_desc) + (x & 3) * (2048 >> 4), pv, !begins || x > 0);
-                    pair_commit(bar(sm.slot_free[x_slot]));
-                    pair_commit(bar(sm.slot_free[y_slot]));
-                    if (h == 1) pair_commit(bar(sm.added));
-                }
-                __syncwarp();
-                v_slot += 2;
-                if (v_slot == SLOTS) v_slot = 0;
-            }
-            begins = ++tile == w.tiles;
-            if (begins) tile = 0;
-        }
-        if (!ok) {     // let what was issued end before the pair goes
-            if (elect_one()) pair_commit(bar(sm.drained));
-            for (int i = 0; i < (1 << 20) && !mbar_try(bar(sm.drained), 0); ++i) {}
-        }
-        __syncwarp();
-    } else if (warp < SOFTMAX) {
+    if (warp < SOFTMAX) {
         // ---- softmax: a thread has head (warp % 2) 32 + lane of the CTA's, and half of
         // the keys, and in the end half of the values -----------------------------------
         const int i = (warp & 1) * 32 + lane, half = warp >> 1;
@@ -480,63 +312,93 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
             __syncwarp();
             if (lane == 0) arrive_in(at);
         };
-        // With the warp that has the heads' other half: whether both go on.  (Nothing
-        // limits this wait: both warps come here, whatever has gone wrong.)
-        auto meet = [&](bool go) {
-            uint32_t both;
-            asm volatile("{\n"
-                         ".reg .pred p, q;\n"
-                         "setp.ne.u32 p, %1, 0;\n"
-                         "barrier.cta.red.and.pred q, %2, 64, p;\n"
-                         "selp.u32 %0, 1, 0, q;\n"
-                         "}"
-                         : "=r"(both)
-                         : "r"((uint32_t)go), "r"(1 + (warp & 1))
-                         : "memory");
-            return both != 0;
-        };
+        auto meet_half = [&](bool go) { return meet(1 + (warp & 1), 64, go); };      // the warp with the heads' other half
+        auto meet_all = [&](bool go) { return meet(3, SOFTMAX * 32, go); };
         // (scale 0: not 0 times the -inf of a row that is not there)
         const bool nan = a.scale != a.scale;
         const float f = nan ? 1.0f : fmaxf(fabsf(a.scale) * kLog2e, FLT_MIN);
+        // The queries of a group, with the sign of the scale (or NaN): eight threads a
+        // head's 128 bytes, all of it on its way at once; then through P's place, 16 KB at
+        // a time, to a thread's lane.  (A thread its own head's, 16 bytes of 32 heads a
+        // load: 11 thousand cycles against 5.)
+        auto place_queries = [&](int group) {
+            const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, set = nan ? 0x7FFF7FFFu : 0u;
+            const int unit = lane & 7, first = warp * 4 + (lane >> 3);      // heads first + 16 k
+            uint4 v[9][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t head = (int64_t)group * PAIR_HEADS + rank * CTA_HEADS + first + 16 * k;
+                const bool on = head < (int64_t)a.R * a.H;
+                const HeadPlace at(a, on ? head : 0);
+                const uint8_t *q = a.q + at.r * a.q_rs + at.h * a.q_hs + unit * 16;
+#pragma unroll
+                for (int b = 0; b < 9; ++b) {
+                    v[b][k] = make_uint4(0, 0, 0, 0);
+                    if (on) v[b][k] = ld_dev_v4(q + block_at(b) * 128);
+                }
+            }
+            auto put = [&](uint32_t block, const uint4 (&x)[4]) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int h = first + 16 * k;
+                    st_smem_v4(block + h * 128 + ((unit ^ (h & 7)) << 4),
+                               make_uint4((x[k].x ^ flip) | set, (x[k].y ^ flip) | set, (x[k].z ^ flip) | set, (x[k].w ^ flip) | set));
+                }
+            };
+#pragma unroll
+            for (int b = 0; b < Q_SMEM; ++b) put(base + Q_AT + b * BLOCK, v[Q_TMEM + b]);
+#pragma unroll
+            for (int b = 0; b < Q_TMEM; b += 2) {
+                put(base + P_AT, v[b]);
+                put(base + P_AT + BLOCK, v[b + 1]);
+                meet_all(true);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t y[32];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const uint4 z = ld_smem_v4(base + P_AT + k * BLOCK + i * 128 + ((x ^ (i & 7)) << 4));
+                        y[4 * x] = z.x, y[4 * x + 1] = z.y, y[4 * x + 2] = z.z, y[4 * x + 3] = z.w;
+                    }
+                    tmem_st_32(lanes + T_Q + (b + k) * 32, y);
+                }
+                meet_all(true);
+            }
+            tmem_wait_st();
+            fence_async_smem();
+            tc_fence_before();
+            tell(queries_at);
+        };
+        // 32 columns of O of the warp's 32 heads, so that eight threads have 128 bytes of
+        // a head: take(k, the four at columns 4 (lane % 8) of head 4 k + lane / 8).  By way
+        // of the warp's quarter of P's place.
+        const uint32_t stage = base + P_AT + warp * 4096;
+        auto columns = [&](int c, auto take) {
+            uint32_t o[32];
+            tmem_ld_32(lanes + T_O + c, o);
+            tmem_wait_ld();
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                st_smem_v4(stage + lane * 128 + ((x ^ (lane & 7)) << 4), make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int h = k * 4 + (lane >> 3);
+                take(k, ld_smem_v4(stage + h * 128 + (((lane & 7) ^ (h & 7)) << 4)));
+            }
+        };
         int n = 0;
         int64_t u = u0;
-        for (int part = 0; ok && u < u1; ++part) {
+        for (bool begins = true; u < u1; begins = false) {
+            if (!(ok = meet_all(ok))) break;      // (P's place is free, too)
             const int group = (int)(u / w.tiles), t0 = (int)(u - (int64_t)group * w.tiles);
             const int t1 = (int)min((int64_t)w.tiles, t0 + (u1 - u));
             u += t1 - t0;
             const int64_t head = (int64_t)group * PAIR_HEADS + rank * CTA_HEADS + i;
             const bool on = head < (int64_t)a.R * a.H;
-            const HeadPlace at(a, on ? head : 0);
-            {      // the queries, with the sign of the scale (or NaN)
-                const uint8_t *q = a.q + at.r * a.q_rs + at.h * a.q_hs;
-                const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, set = nan ? 0x7FFF7FFFu : 0u;
-                auto load = [&](int unit) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (on) v = ld_dev_v4(q + unit * 16);
-                    return make_uint4((v.x ^ flip) | set, (v.y ^ flip) | set, (v.z ^ flip) | set, (v.w ^ flip) | set);
-                };
-#pragma unroll
-                for (int b = 0; b < Q_TMEM; ++b) {
-                    uint32_t v[32];
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const uint4 y = load(block_at(b) * 8 + x);
-                        v[4 * x] = y.x, v[4 * x + 1] = y.y, v[4 * x + 2] = y.z, v[4 * x + 3] = y.w;
-                    }
-                    tmem_st_32(lanes + T_Q + b * 32, v);
-                }
-#pragma unroll
-                for (int b = 0; b < Q_SMEM; ++b)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {      // (each of a head's two threads half of it)
-                        const int unit = half * 4 + x;
-                        st_smem_v4(base + Q_AT + b * BLOCK + i * 128 + ((unit ^ (i & 7)) << 4), load(block_at(Q_TMEM + b) * 8 + unit));
-                    }
-                tmem_wait_st();
-                fence_async_smem();
-                tc_fence_before();
-                tell(queries_at);
-            }
+            place_queries(group);
+            if (begins) after_launch_before();
             float m = -INFINITY, l = 0.0f;
             const uint32_t *there = w.there + half * 2;
             uint2 next = *reinterpret_cast<const uint2 *>(there + (int64_t)t0 * 4);
@@ -569,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
                 }
                 float s = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
                 sm.top[n & 1][half][i] = s;
-                if (!(ok = meet(ok))) break;
+                if (!(ok = meet_half(ok))) break;
                 s = fmaxf(s, sm.top[n & 1][half ^ 1][i]);
                 float d = 1.0f;
                 const bool moves = __any_sync(0xffffffffu, s > m + kMoveAbove);
@@ -579,6 +441,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
                     m = to;
                     l *= d;
                 }
+                // P and O are free once the product before is done (asked ahead of the
+                // exponentials, which hide how long that takes)
+                const bool is_free = n == 0 || mbar_try(bar(sm.added), (n - 1) & 1);
                 const float r = m == -INFINITY ? 0.0f : -m;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -590,8 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
                         v[k][j >> 1] = floats_to_pair<DT>(p0, p1);
                     }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                // P and O are free once the product before is done
-                if (n > 0 && !(ok = all(mbar_wait(bar(sm.added), (n - 1) & 1, gave_up)))) continue;
+                if (!all(is_free) && !(ok = all(mbar_wait(bar(sm.added), (n - 1) & 1, gave_up)))) continue;
                 if (moves && t > t0) {
                     tc_fence_after();
 #pragma unroll 1
@@ -609,22 +473,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int x4 = 0; x4 < 4; ++x4)
-                        st_smem_v4(p_at + (((k * 4 + x4) ^ (i & 7)) << 4),
-                                   make_uint4(v[k][4 * x4], v[k][4 * x4 + 1], v[k][4 * x4 + 2], v[k][4 * x4 + 3]));
+                    for (int y = 0; y < 4; ++y)
+                        st_smem_v4(p_at + (((k * 4 + y) ^ (i & 7)) << 4),
+                                   make_uint4(v[k][4 * y], v[k][4 * y + 1], v[k][4 * y + 2], v[k][4 * y + 3]));
                 fence_async_smem();
                 tc_fence_before();
                 tell(weighed_at);
             }
-            // (a break leaves the loop with both warps, and so does this)
             ok = ok && all(mbar_wait(bar(sm.added), (n - 1) & 1, gave_up));
             tc_fence_after();
-            const float part_lse = a.part ? a.part_lse[at.n] : 0.0f;      // (lse may be the same)
+            const float part_lse = a.part && on ? a.part_lse[head] : -INFINITY;      // (lse may be the same)
             sm.sum[half][i] = l;
-            if (!(ok = meet(ok))) break;
+            if (!(ok = meet_half(ok))) continue;      // (to the barrier of all)
             l += sm.sum[half ^ 1][i];
-            meet(true);
-            if (t0 == 0 && t1 == w.tiles) {      // the heads' whole sums
+            meet_half(true);
+            if (t0 == 0 && t1 == w.tiles) {      // all of the heads' rows: out
+                const HeadPlace at(a, on ? head : 0);
                 float weight = 0.0f, scale = 1.0f;
                 const uint8_t *part = nullptr;
                 if (a.part) {
@@ -632,45 +496,177 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
                     if (weight != 0.0f) part = a.part + at.r * a.part_rs + at.h * a.part_hs + half * 512;
                 }
                 const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
-                if (on && half == 0 && a.lse) a.lse[at.n] = log2_sum(m, l) * kLn2;
+                if (on && half == 0 && a.lse) a.lse[head] = log2_sum(m, l) * kLn2;
                 scale *= inv;
                 weight *= inv;
-                uint8_t *out = a.out + at.r * a.out_rs + at.h * a.out_hs + half * 512;
+                const unsigned long long to = reinterpret_cast<unsigned long long>(on ? a.out + at.r * a.out_rs + at.h * a.out_hs + half * 512 : nullptr);
+                const unsigned long long from = reinterpret_cast<unsigned long long>(part);
 #pragma unroll 1
-                for (int c = 0; c < 256; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld_32(lanes + T_O + c, o);
-                    tmem_wait_ld();
-                    if (!on) continue;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float x[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[8 * j + k]);
-                        uint4 p = make_uint4(0, 0, 0, 0);
-                        if (part) p = ld_dev_v4(part + c * 2 + j * 16);
-                        st_v4(out + c * 2 + j * 16, weighted8<DT>(x, scale, p, weight, part != nullptr));
-                    }
-                }
+                for (int c = 0; c < 256; c += 32)
+                    columns(c, [&](int k, uint4 o) {
+                        const int h = k * 4 + (lane >> 3);
+                        const float fo = __shfl_sync(0xffffffffu, scale, h), fp = __shfl_sync(0xffffffffu, weight, h);
+                        uint8_t *dst = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, to, h));
+                        const uint8_t *src = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, from, h));
+                        if (!dst) return;
+                        const int64_t off = c * 2 + (lane & 7) * 8;
+                        float2 x = make_float2(__uint_as_float(o.x) * fo, __uint_as_float(o.y) * fo);
+                        float2 y = make_float2(__uint_as_float(o.z) * fo, __uint_as_float(o.w) * fo);
+                        if (src) {
+                            const uint2 p = *reinterpret_cast<const uint2 *>(src + off);
+                            const float2 px = pair_to_float<DT>(p.x), py = pair_to_float<DT>(p.y);
+                            x = make_float2(fmaf(px.x, fp, x.x), fmaf(px.y, fp, x.y));
+                            y = make_float2(fmaf(py.x, fp, y.x), fmaf(py.y, fp, y.y));
+                        }
+                        *reinterpret_cast<uint2 *>(dst + off) = make_uint2(floats_to_pair<DT>(x.x, x.y), floats_to_pair<DT>(y.x, y.y));
+                    });
             } else {
-                const int64_t place = ((int64_t)pair * 2 + (t0 == 0)) * PAIR_HEADS + rank * CTA_HEADS + i;
-                if (half == 0) w.ml[place] = make_float2(m, l);
-                float *o_at = w.o + place * kLatent + half * 256;
+                const int64_t place = ((int64_t)pair * 2 + (t0 == 0)) * PAIR_HEADS + rank * CTA_HEADS;
+                if (half == 0) w.ml[place + i] = make_float2(m, l);
+                float *o_at = w.o + (place + (warp & 1) * 32 + (lane >> 3)) * kLatent + half * 256 + (lane & 7) * 4;
 #pragma unroll 1
-                for (int c = 0; c < 256; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld_32(lanes + T_O + c, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        *reinterpret_cast<uint4 *>(o_at + c + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-                }
+                for (int c = 0; c < 256; c += 32)
+                    columns(c, [&](int k, uint4 o) { st_v4(o_at + (int64_t)k * 4 * kLatent + c, o); });
             }
             tc_fence_before();
         }
+    } else if (warp == KEY_WARP) {
+        // ---- this CTA's keys of every tile ------------------------------------------
+        int slot = 0, rope = 0, tile = (int)(u0 % w.tiles);
+        uint32_t slot_phase = 1, rope_phase = 1;      // (nothing to wait for the first time round)
+        for (int n = 0; ok && n < count; ++n) {
+            const uint8_t *src = w.image + ((int64_t)tile * 2 + rank) * HALF_TILE;
+            for (int h = 0; h < 2; ++h) {      // the rope part with the second half
+                ok = ok && all(mbar_wait(bar(sm.slot_free[slot]), slot_phase, gave_up));
+                if (h == 1) ok = ok && all(mbar_wait(bar(sm.rope_free[rope]), rope_phase, gave_up));
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint32_t here = bar(sm.keys[slot]);
+                    mbar_expect(here, h == 0 ? SLOT : SLOT + BLOCK);
+                    bring(base + slot * SLOT, src + h * SLOT, SLOT, here);
+                    if (h == 1) bring(base + ROPE_AT + rope * BLOCK, src + 2 * SLOT, BLOCK, here);
+                }
+                __syncwarp();
+                if (++slot == SLOTS) slot = 0, slot_phase ^= 1;
+            }
+            if (++rope == ROPES) rope = 0, rope_phase ^= 1;
+            if (++tile == w.tiles) tile = 0;
+        }
+    } else if (warp == VALUE_WARP) {
+        // ---- the other CTA's keys, for this one's values --------------------------------
+        int slot = 0, tile = (int)(u0 % w.tiles);
+        const uint32_t to = rank == 0 ? PART : 0;      // Y or X
+        for (int n = 0; ok && n < count; ++n) {
+            if (!(ok = all(mbar_wait(bar(sm.scored[n & 1]), (n >> 1) & 1, gave_up)))) break;
+            const uint8_t *src = w.image + ((int64_t)tile * 2 + (rank ^ 1)) * HALF_TILE + rank * PART;
+            if (elect_one()) {
+                const uint32_t here = bar(sm.values[n & 1]);
+                mbar_expect(here, 2 * PART);
+                for (int h = 0; h < 2; ++h) {
+                    const int s = slot + h < SLOTS ? slot + h : 0;
+                    bring(base + s * SLOT + to, src + h * SLOT, PART, here);
+                }
+            }
+            __syncwarp();
+            slot += 2;
+            if (slot >= SLOTS) slot -= SLOTS;
+            if (++tile == w.tiles) tile = 0;
+        }
+    } else if (rank == 1) {
+        // ---- what has come in here, to the first CTA --------------------------------------
+        auto tell = [&](const uint64_t &b, uint32_t phase) {
+            ok = ok && all(mbar_wait(bar(b), phase, gave_up));
+            if (ok && lane == 0) arrive_in(in_cta(bar(b), 0));
+        };
+        int slot = 0;
+        uint32_t slot_phase = 0;
+        for (int n = 0; ok && n < count; ++n) {
+            if (warp == SCORE_WARP) {
+                for (int h = 0; h < 2; ++h) {
+                    tell(sm.keys[slot], slot_phase);
+                    if (++slot == SLOTS) slot = 0, slot_phase ^= 1;
+                }
+            } else {
+                tell(sm.values[n & 1], (n >> 1) & 1);
+            }
+        }
+    } else if (elect_one()) {
+        // ---- MMA issue, by one thread from the first wait to the last (leaving and
+        // entering an elected thread's part around each wait cost 300 cycles), in short
+        // loops: one for S, one for O, so that neither waits for the other to be issued --
+        auto wait = [&](const uint64_t &b, uint32_t phase) { return ok = ok && mbar_wait(bar(b), phase, gave_up); };
+        int slot = 0, tile = (int)(u0 % w.tiles);
+        bool begins = true;      // a group of heads
+        if (warp == SCORE_WARP) {
+            constexpr uint32_t qk = mma_desc(128, KEYS, DT == kBf16, false);
+            int rope = 0, group = 0;
+            uint32_t slot_phase = 0;
+#pragma unroll 1
+            for (int n = 0; ok && n < count; ++n) {
+                // (what is likely there comes first: a wait takes time even so)
+                wait(sm.keys[slot], slot_phase);
+                if (begins) wait(sm.queries, group++ & 1);
+                if (n > 0) wait(sm.read, (n - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t q_col = tmem + T_Q;
+                uint64_t k_desc = smem_desc(base + slot * SLOT, 16, 1024), q_desc = smem_desc(base + Q_AT, 16, 1024);
+                if (++slot == SLOTS) slot = 0, slot_phase ^= 1;
+#pragma unroll 1
+                for (int b = 0; b < Q_TMEM; ++b, k_desc += BLOCK >> 4, q_col += 32) {
+                    if (b == 4) {
+                        if (!wait(sm.keys[slot], slot_phase)) break;
+                        k_desc = smem_desc(base + slot * SLOT, 16, 1024);
+                        if (++slot == SLOTS) slot = 0, slot_phase ^= 1;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)      // 16 values a step: 32 bytes, 8 columns
+                        pair_mma_ts(tmem + T_S, q_col + x * 8, k_desc + x * 2, qk, b + x > 0);
+                }
+                if (!ok) break;
+#pragma unroll 1
+                for (int b = Q_TMEM; b < 9; ++b, k_desc += BLOCK >> 4, q_desc += BLOCK >> 4) {
+                    if (b == 8) k_desc = smem_desc(base + ROPE_AT + rope * BLOCK, 16, 1024);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) pair_mma(tmem + T_S, q_desc + x * 2, k_desc + x * 2, qk, true);
+                }
+                pair_commit(bar(sm.scored[n & 1]));
+                pair_commit(bar(sm.rope_free[rope]));
+                if (++rope == ROPES) rope = 0;
+                begins = ++tile == w.tiles;
+                if (begins) tile = 0;
+            }
+        } else {
+            constexpr uint32_t pv = mma_desc(128, 256, DT == kBf16, true);
+#pragma unroll 1
+            for (int n = 0; ok && n < count; ++n) {
+                wait(sm.values[n & 1], (n >> 1) & 1);
+                if (!wait(sm.weighed, n & 1)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {            // 256 values a time
+                    uint64_t p_desc = smem_desc(base + P_AT, 16, 1024), v_desc = smem_desc(base + slot * SLOT, BLOCK, 1024);
+#pragma unroll 1
+                    for (int y = 0; y < 2; ++y, p_desc += BLOCK >> 4, v_desc += PART >> 4)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)      // 16 keys a step
+                            pair_mma(tmem + T_O + h * 128, p_desc + x * 2, v_desc + x * (2048 >> 4), pv, !begins || y + x > 0);
+                    pair_commit(bar(sm.slot_free[slot]));
+                    if (h == 1) pair_commit(bar(sm.added));
+                    if (++slot == SLOTS) slot = 0;
+                }
+                begins = ++tile == w.tiles;
+                if (begins) tile = 0;
+            }
+        }
+        if (!ok) {     // let what was issued end before the pair goes
+            const uint32_t drained = bar(sm.drained[warp - SCORE_WARP]);
+            pair_commit(drained);
+            for (int i = 0; i < (1 << 20) && !mbar_try(drained, 0); ++i) {}
+        }
     }
     __syncwarp();
-    if (sm.gave_up) {      // let copies in flight come in (16 KB each, microseconds)
+    if (*gave_up) {      // let copies in flight come in (32 KB each, microseconds)
         uint64_t t0, t;
         asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
         do {
@@ -679,24 +675,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
     }
     tc_fence_before();
     __syncthreads();
-    pair_sync();      // no CTA leaves before the other has done with it
+    cluster_arrive();      // no CTA leaves before the other has done with it
+    cluster_wait();
     if (tid == 0 && sm.gave_up && a.status)
         for (int r = 0; r < a.R; ++r) record_status(a.status, r, kStatusAttendTimeout);
-    if (warp == MMA_WARP) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    if (warp == SCORE_WARP) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 // ---- join ------------------------------------------------------------------------------
 
 constexpr int JOIN_NT = 128;
 
-// A warp a head: its parts from the pairs that have some of its tiles.
+// A CTA a head, four values a thread: its parts from the pairs that have some of its
+// tiles.
 template <int DT>
 __global__ void __launch_bounds__(JOIN_NT) join_kernel(const __grid_constant__ PrefixLaunch a, const __grid_constant__ PrefixParts w)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t head = (int64_t)blockIdx.x * (JOIN_NT / 32) + (threadIdx.x >> 5);
     after_launch_before();
-    if (head >= (int64_t)a.R * a.H) return;
+    const int tid = threadIdx.x;
+    const int64_t head = blockIdx.x;
     const HeadPlace at(a, head);
     const int group = (int)(head / PAIR_HEADS), i = (int)(head % PAIR_HEADS);
     const int64_t begin = (int64_t)group * w.tiles;
@@ -706,42 +703,49 @@ __global__ void __launch_bounds__(JOIN_NT) join_kernel(const __grid_constant__ P
         p1 = pair_of(w, begin + w.tiles - 1);
         if (p0 == p1) return;      // (that pair has written it)
     }
-    auto place = [&](int p) { return ((int64_t)p * 2 + (first_unit(w, p) <= begin)) * PAIR_HEADS + i; };
-    float m = -INFINITY;
-    for (int p = p0; p <= p1; ++p) m = fmaxf(m, w.ml[place(p)].x);
-    const float base = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, o[2][8] = {};
+    float other = -INFINITY;
+    uint2 part = make_uint2(0, 0);
+    if (a.part) {
+        other = a.part_lse[head];
+        part = *reinterpret_cast<const uint2 *>(a.part + at.r * a.part_rs + at.h * a.part_hs + tid * 8);
+    }
+    __syncthreads();      // (part may be out, part_lse lse)
+    const float2 *ml = w.ml + i;
+    const float *src = w.o + (int64_t)i * kLatent + tid * 4;
+    // (a pair's second place is for the group that it begins with)
+    auto place = [&](int p) { return ((int64_t)p * 2 + (first_unit(w, p) <= begin)) * PAIR_HEADS; };
+    float m = -INFINITY, l = 0.0f, o[4] = {};
+#pragma unroll 4
     for (int p = p0; p <= p1; ++p) {
-        const float2 ml = w.ml[place(p)];
-        const float f = ex2(ml.x - base);
-        l = fmaf(f, ml.y, l);
-        const float *src = w.o + place(p) * kLatent + lane * 8;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(src + k * 256 + j);
-                o[k][j] = fmaf(f, x.x, o[k][j]);
-                o[k][j + 1] = fmaf(f, x.y, o[k][j + 1]);
-                o[k][j + 2] = fmaf(f, x.z, o[k][j + 2]);
-                o[k][j + 3] = fmaf(f, x.w, o[k][j + 3]);
-            }
+        const int64_t n = place(p);
+        const float2 x = ml[n];
+        const float4 v = *reinterpret_cast<const float4 *>(src + n * kLatent);
+        const float to = fmaxf(m, x.x), base = to == -INFINITY ? 0.0f : to;
+        const float f = ex2(m - base), g = ex2(x.x - base);
+        m = to;
+        l = l * f + x.y * g;
+        o[0] = o[0] * f + v.x * g;
+        o[1] = o[1] * f + v.y * g;
+        o[2] = o[2] * f + v.z * g;
+        o[3] = o[3] * f + v.w * g;
     }
     float weight = 0.0f, scale = 1.0f;
-    uint4 part[2] = {};
-    if (a.part) {
-        const uint8_t *src = a.part + at.r * a.part_rs + at.h * a.part_hs + lane * 16;
-        part[0] = ld_dev_v4(src);
-        part[1] = ld_dev_v4(src + 512);
-        scale = add_part(m, l, a.part_lse[at.n], &weight);
-    }
+    if (a.part) scale = add_part(m, l, other, &weight);
     const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
-    uint8_t *out = a.out + at.r * a.out_rs + at.h * a.out_hs + lane * 16;
-    __syncwarp();      // (part may be out, part_lse lse)
+    scale *= inv;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-        st_v4(out + k * 512, weighted8<DT>(o[k], scale * inv, part[k], weight * inv, weight != 0.0f));
-    if (lane == 0 && a.lse) a.lse[at.n] = log2_sum(m, l) * kLn2;
+    for (int j = 0; j < 4; ++j) o[j] *= scale;
+    if (weight != 0.0f) {
+        weight *= inv;
+        const float2 x = pair_to_float<DT>(part.x), y = pair_to_float<DT>(part.y);
+        o[0] = fmaf(x.x, weight, o[0]);
+        o[1] = fmaf(x.y, weight, o[1]);
+        o[2] = fmaf(y.x, weight, o[2]);
+        o[3] = fmaf(y.y, weight, o[3]);
+    }
+    *reinterpret_cast<uint2 *>(a.out + at.r * a.out_rs + at.h * a.out_hs + tid * 8) =
+        make_uint2(floats_to_pair<DT>(o[0], o[1]), floats_to_pair<DT>(o[2], o[3]));
+    if (tid == 0 && a.lse) a.lse[head] = log2_sum(m, l) * kLn2;
 }
 
 // ---- host ------------------------------------------------------------------------------
@@ -798,7 +802,7 @@ cudaError_t launch(const PrefixLaunch &a, const PrefixParts &w, cudaStream_t s)
         for (int p = 1; p < w.pairs; ++p) split = split || first_unit(w, p) % w.tiles != 0;
         if (!split) return e;
     }
-    return launch_behind(join_kernel<DT>, dim3((unsigned)(((int64_t)a.R * a.H + JOIN_NT / 32 - 1) / (JOIN_NT / 32))), JOIN_NT, 0, 1, s, a, w);
+    return launch_behind(join_kernel<DT>, dim3((unsigned)((int64_t)a.R * a.H)), JOIN_NT, 0, 1, s, a, w);
 }
 
 }  // namespace
