@@ -30,14 +30,14 @@
 //   After S the first CTA keeps X and gets, in Y, the other CTA's keys of its
 //   values X; the second keeps Y and gets, in X, the first one's keys of Y.  A
 //   descriptor is one for both CTAs: at X_h both have keys 0-63, at Y_h 64-127.
-//   The rope part (8 KB) has a ring of three.
+//   The rope part (8 KB) has a slot of its own.
 // The queries do not fit either shared memory or what O and S leave of tensor
-// memory (192 columns): 384 of their values are there, in both halves of the lanes,
-// the other 192 in shared memory.
+// memory (128 columns, S being there twice): 256 of their values are there, in both
+// halves of the lanes, the other 320 in shared memory.
 //   warps 0-3  softmax: a thread a lane, that is a head and half of the tile's keys;
 //   warp 4     brings keys in, warp 5 the values of the other CTA's keys;
-//   warp 6     of the first CTA issues the MMAs of S, warp 7 those of O; those of the
-//              second say what has come in there.
+//   warp 6     of the first CTA issues the MMAs of S, up to two tiles ahead of warp 7,
+//              which issues those of O; those of the second say what has come in there.
 // The heads' tiles in a row are cut evenly among the pairs, wherever a head ends.
 #include <atomic>
 #include <mutex>
@@ -53,21 +53,21 @@ constexpr uint32_t BLOCK = 64 * 128;             // 64 values of 64 keys, swizzl
 constexpr uint32_t PART = 2 * BLOCK, SLOT = 2 * PART;
 constexpr uint32_t HALF_TILE = 9 * BLOCK;        // 64 keys: X0 Y0 X1 Y1 rope, as they go into the slots
 constexpr uint32_t TILE_BYTES = 2 * HALF_TILE;
-constexpr int SLOTS = 5, ROPES = 3;
-constexpr int Q_TMEM = 6, Q_SMEM = 9 - Q_TMEM;   // blocks of the queries
+constexpr int SLOTS = 5;
+constexpr int Q_TMEM = 4, Q_SMEM = 9 - Q_TMEM;   // blocks of the queries
 
-constexpr uint32_t ROPE_AT = SLOTS * SLOT, Q_AT = ROPE_AT + ROPES * BLOCK, P_AT = Q_AT + Q_SMEM * BLOCK;
+constexpr uint32_t ROPE_AT = SLOTS * SLOT, Q_AT = ROPE_AT + BLOCK, P_AT = Q_AT + Q_SMEM * BLOCK;
 constexpr uint32_t MISC_AT = P_AT + 2 * BLOCK;
-constexpr int PX_NT = 256, SOFTMAX = 4, KEY_WARP = 4, VALUE_WARP = 5, SCORE_WARP = 6;
+constexpr int PX_NT = 256, SOFTMAX = 4, KEY_WARP = 4, VALUE_WARP = 5, MMA_WARP = 6;
 
 // columns of tensor memory
-constexpr uint32_t T_O = 0, T_S = 256, T_Q = 320;
+constexpr uint32_t T_O = 0, T_S = 256, T_Q = 384;      // (S of two tiles)
 
 struct PrefixSmem {
-    uint64_t keys[SLOTS], values[2];                    // arrived (in the first CTA: in both)
-    uint64_t slot_free[SLOTS], rope_free[ROPES];        // the products that read it are done
+    uint64_t keys[SLOTS], rope, values[2];              // arrived (in the first CTA: in both)
+    uint64_t slot_free[SLOTS];                          // the products that read it are done
     uint64_t scored[2], added;                          // S is there; O is
-    uint64_t queries, read, weighed;                    // (in the first CTA, from both) Q is there, S read, P there
+    uint64_t queries, read[2], weighed;                 // (in the first CTA, from both) Q is there, S read, P there
     uint64_t drained[2];
     uint32_t tmem;
     int gave_up;
@@ -272,17 +272,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
     const int count = (int)(u1 - u0);      // tiles of this pair, over all its groups of heads
     auto bar = [](const uint64_t &b) { return smem_u32(&b); };
 
-    if (warp == SCORE_WARP) {
+    if (warp == MMA_WARP) {
         if (lane == 0) {
             const int both = rank == 0 ? 2 : 1;      // the first CTA also hears of the second
             for (int s = 0; s < SLOTS; ++s) mbar_init(bar(sm.keys[s]), both), mbar_init(bar(sm.slot_free[s]), 1);
-            for (int s = 0; s < ROPES; ++s) mbar_init(bar(sm.rope_free[s]), 1);
-            for (int s = 0; s < 2; ++s) mbar_init(bar(sm.values[s]), both), mbar_init(bar(sm.scored[s]), 1);
+            mbar_init(bar(sm.rope), both);
+            for (int s = 0; s < 2; ++s) {
+                mbar_init(bar(sm.values[s]), both);
+                mbar_init(bar(sm.scored[s]), 1);
+                mbar_init(bar(sm.read[s]), 2 * SOFTMAX);
+            }
             mbar_init(bar(sm.added), 1);
             mbar_init(bar(sm.queries), 2 * SOFTMAX);
-            mbar_init(bar(sm.read), 2 * SOFTMAX);
             mbar_init(bar(sm.weighed), 2 * SOFTMAX);
-            for (int s = 0; s < 2; ++s) mbar_init(bar(sm.drained[s]), 1);
+            mbar_init(bar(sm.drained[0]), 1);
+            mbar_init(bar(sm.drained[1]), 1);
             sm.gave_up = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
@@ -307,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
         // the keys, and in the end half of the values -----------------------------------
         const int i = (warp & 1) * 32 + lane, half = warp >> 1;
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-        const uint32_t queries_at = in_cta(bar(sm.queries), 0), read_at = in_cta(bar(sm.read), 0), weighed_at = in_cta(bar(sm.weighed), 0);
+        const uint32_t queries_at = in_cta(bar(sm.queries), 0), read_at = in_cta(bar(sm.read[0]), 0), weighed_at = in_cta(bar(sm.weighed), 0);
         auto tell = [&](uint32_t at) {
             __syncwarp();
             if (lane == 0) arrive_in(at);
@@ -408,11 +412,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
                 ok = ok && all(mbar_wait(bar(sm.scored[n & 1]), (n >> 1) & 1, gave_up));
                 tc_fence_after();
                 uint32_t v[2][32];
-                tmem_ld_32(lanes + T_S, v[0]);
-                tmem_ld_32(lanes + T_S + 32, v[1]);
+                tmem_ld_32(lanes + T_S + (n & 1) * 64, v[0]);
+                tmem_ld_32(lanes + T_S + (n & 1) * 64 + 32, v[1]);
                 tmem_wait_ld();
                 tc_fence_before();
-                tell(read_at);
+                tell(read_at + (n & 1) * 8);
                 float (&x)[2][32] = reinterpret_cast<float (&)[2][32]>(v);
                 if ((named.x & named.y) != 0xFFFFFFFFu) {
 #pragma unroll
@@ -532,30 +536,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
         }
     } else if (warp == KEY_WARP) {
         // ---- this CTA's keys of every tile ------------------------------------------
-        int slot = 0, rope = 0, tile = (int)(u0 % w.tiles);
-        uint32_t slot_phase = 1, rope_phase = 1;      // (nothing to wait for the first time round)
+        int slot = 0, tile = (int)(u0 % w.tiles);
+        uint32_t slot_phase = 1;      // (nothing to wait for the first time round)
         for (int n = 0; ok && n < count; ++n) {
             const uint8_t *src = w.image + ((int64_t)tile * 2 + rank) * HALF_TILE;
-            for (int h = 0; h < 2; ++h) {      // the rope part with the second half
-                ok = ok && all(mbar_wait(bar(sm.slot_free[slot]), slot_phase, gave_up));
-                if (h == 1) ok = ok && all(mbar_wait(bar(sm.rope_free[rope]), rope_phase, gave_up));
-                if (!ok) break;
+            for (int h = 0; h < 2; ++h) {
+                if (!(ok = ok && all(mbar_wait(bar(sm.slot_free[slot]), slot_phase, gave_up)))) break;
                 if (elect_one()) {
                     const uint32_t here = bar(sm.keys[slot]);
-                    mbar_expect(here, h == 0 ? SLOT : SLOT + BLOCK);
+                    mbar_expect(here, SLOT);
                     bring(base + slot * SLOT, src + h * SLOT, SLOT, here);
-                    if (h == 1) bring(base + ROPE_AT + rope * BLOCK, src + 2 * SLOT, BLOCK, here);
                 }
                 __syncwarp();
                 if (++slot == SLOTS) slot = 0, slot_phase ^= 1;
             }
-            if (++rope == ROPES) rope = 0, rope_phase ^= 1;
             if (++tile == w.tiles) tile = 0;
         }
     } else if (warp == VALUE_WARP) {
         // ---- the other CTA's keys, for this one's values --------------------------------
         int slot = 0, tile = (int)(u0 % w.tiles);
         const uint32_t to = rank == 0 ? PART : 0;      // Y or X
+        auto rope = [&](int tile) {
+            if (elect_one()) {
+                mbar_expect(bar(sm.rope), BLOCK);
+                bring(base + ROPE_AT, w.image + ((int64_t)tile * 2 + rank) * HALF_TILE + 2 * SLOT, BLOCK, bar(sm.rope));
+            }
+            __syncwarp();
+        };
+        rope(tile);
         for (int n = 0; ok && n < count; ++n) {
             if (!(ok = all(mbar_wait(bar(sm.scored[n & 1]), (n >> 1) & 1, gave_up)))) break;
             const uint8_t *src = w.image + ((int64_t)tile * 2 + (rank ^ 1)) * HALF_TILE + rank * PART;
@@ -571,6 +579,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
             slot += 2;
             if (slot >= SLOTS) slot -= SLOTS;
             if (++tile == w.tiles) tile = 0;
+            if (n + 1 < count) rope(tile);
         }
     } else if (rank == 1) {
         // ---- what has come in here, to the first CTA --------------------------------------
@@ -581,58 +590,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
         int slot = 0;
         uint32_t slot_phase = 0;
         for (int n = 0; ok && n < count; ++n) {
-            if (warp == SCORE_WARP) {
+            if (warp == MMA_WARP) {
                 for (int h = 0; h < 2; ++h) {
                     tell(sm.keys[slot], slot_phase);
                     if (++slot == SLOTS) slot = 0, slot_phase ^= 1;
                 }
+                tell(sm.rope, n & 1);
             } else {
                 tell(sm.values[n & 1], (n >> 1) & 1);
             }
         }
     } else if (elect_one()) {
-        // ---- MMA issue, by one thread from the first wait to the last (leaving and
-        // entering an elected thread's part around each wait cost 300 cycles), in short
-        // loops: one for S, one for O, so that neither waits for the other to be issued --
+        // ---- MMA issue, of S and of O by one thread each, from its first wait to its last
+        // (leaving and entering an elected thread's part around each wait cost 300 cycles),
+        // in short loops.  A thread's waits, and the fences behind them, take some hundred
+        // cycles, in which the other's MMAs go on. -----------------------------------------
         auto wait = [&](const uint64_t &b, uint32_t phase) { return ok = ok && mbar_wait(bar(b), phase, gave_up); };
         int slot = 0, tile = (int)(u0 % w.tiles);
         bool begins = true;      // a group of heads
-        if (warp == SCORE_WARP) {
+        if (warp == MMA_WARP) {
             constexpr uint32_t qk = mma_desc(128, KEYS, DT == kBf16, false);
-            int rope = 0, group = 0;
+            int group = 0;
             uint32_t slot_phase = 0;
+            auto next_slot = [&]() {
+                const uint64_t k_desc = smem_desc(base + slot * SLOT, 16, 1024);
+                if (++slot == SLOTS) slot = 0, slot_phase ^= 1;
+                return k_desc;
+            };
 #pragma unroll 1
             for (int n = 0; ok && n < count; ++n) {
-                // (what is likely there comes first: a wait takes time even so)
                 wait(sm.keys[slot], slot_phase);
                 if (begins) wait(sm.queries, group++ & 1);
-                if (n > 0) wait(sm.read, (n - 1) & 1);
+                if (n > 1) wait(sm.read[n & 1], ((n >> 1) - 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
+                const uint32_t d = tmem + T_S + (n & 1) * 64;
                 uint32_t q_col = tmem + T_Q;
-                uint64_t k_desc = smem_desc(base + slot * SLOT, 16, 1024), q_desc = smem_desc(base + Q_AT, 16, 1024);
-                if (++slot == SLOTS) slot = 0, slot_phase ^= 1;
+                uint64_t k_desc = next_slot(), q_desc = smem_desc(base + Q_AT, 16, 1024);
 #pragma unroll 1
-                for (int b = 0; b < Q_TMEM; ++b, k_desc += BLOCK >> 4, q_col += 32) {
-                    if (b == 4) {
-                        if (!wait(sm.keys[slot], slot_phase)) break;
-                        k_desc = smem_desc(base + slot * SLOT, 16, 1024);
-                        if (++slot == SLOTS) slot = 0, slot_phase ^= 1;
-                    }
+                for (int b = 0; b < Q_TMEM; ++b, k_desc += BLOCK >> 4, q_col += 32)
 #pragma unroll
                     for (int x = 0; x < 4; ++x)      // 16 values a step: 32 bytes, 8 columns
-                        pair_mma_ts(tmem + T_S, q_col + x * 8, k_desc + x * 2, qk, b + x > 0);
-                }
-                if (!ok) break;
+                        pair_mma_ts(d, q_col + x * 8, k_desc + x * 2, qk, b + x > 0);
+                if (!wait(sm.keys[slot], slot_phase)) break;
+                k_desc = next_slot();
 #pragma unroll 1
                 for (int b = Q_TMEM; b < 9; ++b, k_desc += BLOCK >> 4, q_desc += BLOCK >> 4) {
-                    if (b == 8) k_desc = smem_desc(base + ROPE_AT + rope * BLOCK, 16, 1024);
+                    if (b == 8) {
+                        if (!wait(sm.rope, n & 1)) break;
+                        k_desc = smem_desc(base + ROPE_AT, 16, 1024);
+                    }
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) pair_mma(tmem + T_S, q_desc + x * 2, k_desc + x * 2, qk, true);
+                    for (int x = 0; x < 4; ++x) pair_mma(d, q_desc + x * 2, k_desc + x * 2, qk, true);
                 }
+                if (!ok) break;
                 pair_commit(bar(sm.scored[n & 1]));
-                pair_commit(bar(sm.rope_free[rope]));
-                if (++rope == ROPES) rope = 0;
                 begins = ++tile == w.tiles;
                 if (begins) tile = 0;
             }
@@ -660,7 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
             }
         }
         if (!ok) {     // let what was issued end before the pair goes
-            const uint32_t drained = bar(sm.drained[warp - SCORE_WARP]);
+            const uint32_t drained = bar(sm.drained[warp - MMA_WARP]);
             pair_commit(drained);
             for (int i = 0; i < (1 << 20) && !mbar_try(drained, 0); ++i) {}
         }
@@ -679,7 +691,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
     cluster_wait();
     if (tid == 0 && sm.gave_up && a.status)
         for (int r = 0; r < a.R; ++r) record_status(a.status, r, kStatusAttendTimeout);
-    if (warp == SCORE_WARP) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    if (warp == MMA_WARP) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 // ---- join ------------------------------------------------------------------------------
