@@ -88,7 +88,7 @@ struct PrefixParts {
     int64_t units;           // tiles * groups; pair p takes units p * units / pairs to (p + 1) * units / pairs
     uint8_t *image;          // [tiles][2] half tiles
     uint32_t *there;         // [tiles][4] a bit a key
-    float *o;                // [pairs][2][128][512]: parts of heads that a pair does not have whole
+    uint8_t *o;              // [pairs][2] parts of O of 128 heads that a pair does not have whole (see part_at)
     float2 *ml;              // [pairs][2][128] reference and sum
 };
 
@@ -99,6 +99,16 @@ __host__ __device__ __forceinline__ int pair_of(const PrefixParts &w, int64_t un
 {
     int p = (int)(((unit + 1) * w.pairs - 1) / w.units);
     return p;
+}
+
+// A part of O: per CTA and warp of 32 heads by 256 values, 8 images of 32 values, the
+// 16-byte units of a head's 128 bytes swizzled.  Where values 4 n to 4 n + 3 of head i
+// of the pair's 128 are.
+constexpr int PART_IMAGE = 32 * 128;
+__device__ __forceinline__ int part_at(int i, int n)
+{
+    const int warp = (i >> 6) * 4 + (n >> 6) * 2 + (i >> 5 & 1), h = i & 31;
+    return (warp * 8 + (n >> 3 & 7)) * PART_IMAGE + h * 128 + (((n ^ h) & 7) << 4);
 }
 
 // ---- expand ------------------------------------------------------------------------
@@ -236,10 +246,10 @@ __device__ __forceinline__ float add_part(float &m, float &l, float part_lse, fl
     return f;
 }
 
-// A head's request and number.
+// A head's request and number.  (At most 2^13 requests of 2^10 heads.)
 struct HeadPlace {
     int r, h;
-    __device__ __forceinline__ HeadPlace(const PrefixLaunch &a, int64_t head) : r((int)(head / a.H)), h((int)(head - (int64_t)r * a.H)) {}
+    __device__ __forceinline__ HeadPlace(const PrefixLaunch &a, int head) : r(head / a.H), h(head - r * a.H) {}
 };
 
 // Whether all threads that meet at a named barrier go on.  (Nothing limits this
@@ -305,6 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
     cluster_wait();      // the other CTA's mbarriers are there, and its tensor memory
     // (the softmax warps read the queries ahead of this wait: see expand_kernel)
     if (warp >= SOFTMAX) after_launch_before();
+    if (warp == MMA_WARP) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");      // (join_kernel waits itself)
 
     if (warp < SOFTMAX) {
         // ---- softmax: a thread has head (warp % 2) 32 + lane of the CTA's, and half of
@@ -331,8 +342,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
             uint4 v[9][4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int64_t head = (int64_t)group * PAIR_HEADS + rank * CTA_HEADS + first + 16 * k;
-                const bool on = head < (int64_t)a.R * a.H;
+                const int head = group * PAIR_HEADS + rank * CTA_HEADS + first + 16 * k;
+                const bool on = head < a.R * a.H;
                 const HeadPlace at(a, on ? head : 0);
                 const uint8_t *q = a.q + at.r * a.q_rs + at.h * a.q_hs + unit * 16;
 #pragma unroll
@@ -373,23 +384,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
             tc_fence_before();
             tell(queries_at);
         };
-        // 32 columns of O of the warp's 32 heads, so that eight threads have 128 bytes of
-        // a head: take(k, the four at columns 4 (lane % 8) of head 4 k + lane / 8).  By way
-        // of the warp's quarter of P's place.
+        // O of the warp's 32 heads, 32 columns from c on at a time, so that eight threads
+        // have 128 bytes of a head: take(c, k, the four at columns c + 4 (lane % 8) of
+        // head 4 k + lane / 8).  By way of the warp's quarter of P's place.
         const uint32_t stage = base + P_AT + warp * 4096;
-        auto columns = [&](int c, auto take) {
+        auto all_columns = [&](auto take) {
             uint32_t o[32];
-            tmem_ld_32(lanes + T_O + c, o);
-            tmem_wait_ld();
-            __syncwarp();
+            tmem_ld_32(lanes + T_O, o);
+#pragma unroll 1
+            for (int c = 0; c < 256; c += 32) {
+                tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-                st_smem_v4(stage + lane * 128 + ((x ^ (lane & 7)) << 4), make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
-            __syncwarp();
+                for (int x = 0; x < 8; ++x)
+                    st_smem_v4(stage + lane * 128 + ((x ^ (lane & 7)) << 4), make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
+                if (c < 224) tmem_ld_32(lanes + T_O + c + 32, o);
+                __syncwarp();
+                uint4 v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int h = k * 4 + (lane >> 3);
-                take(k, ld_smem_v4(stage + h * 128 + (((lane & 7) ^ (h & 7)) << 4)));
+                for (int k = 0; k < 8; ++k) {
+                    const int h = k * 4 + (lane >> 3);
+                    v[k] = ld_smem_v4(stage + h * 128 + (((lane & 7) ^ (h & 7)) << 4));
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) take(c, k, v[k]);
             }
         };
         int n = 0;
@@ -399,8 +417,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
             const int group = (int)(u / w.tiles), t0 = (int)(u - (int64_t)group * w.tiles);
             const int t1 = (int)min((int64_t)w.tiles, t0 + (u1 - u));
             u += t1 - t0;
-            const int64_t head = (int64_t)group * PAIR_HEADS + rank * CTA_HEADS + i;
-            const bool on = head < (int64_t)a.R * a.H;
+            const int head = group * PAIR_HEADS + rank * CTA_HEADS + i;
+            const bool on = head < a.R * a.H;
             place_queries(group);
             if (begins) after_launch_before();
             float m = -INFINITY, l = 0.0f;
@@ -505,32 +523,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
                 weight *= inv;
                 const unsigned long long to = reinterpret_cast<unsigned long long>(on ? a.out + at.r * a.out_rs + at.h * a.out_hs + half * 512 : nullptr);
                 const unsigned long long from = reinterpret_cast<unsigned long long>(part);
-#pragma unroll 1
-                for (int c = 0; c < 256; c += 32)
-                    columns(c, [&](int k, uint4 o) {
-                        const int h = k * 4 + (lane >> 3);
-                        const float fo = __shfl_sync(0xffffffffu, scale, h), fp = __shfl_sync(0xffffffffu, weight, h);
-                        uint8_t *dst = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, to, h));
-                        const uint8_t *src = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, from, h));
-                        if (!dst) return;
-                        const int64_t off = c * 2 + (lane & 7) * 8;
-                        float2 x = make_float2(__uint_as_float(o.x) * fo, __uint_as_float(o.y) * fo);
-                        float2 y = make_float2(__uint_as_float(o.z) * fo, __uint_as_float(o.w) * fo);
-                        if (src) {
-                            const uint2 p = *reinterpret_cast<const uint2 *>(src + off);
-                            const float2 px = pair_to_float<DT>(p.x), py = pair_to_float<DT>(p.y);
-                            x = make_float2(fmaf(px.x, fp, x.x), fmaf(px.y, fp, x.y));
-                            y = make_float2(fmaf(py.x, fp, y.x), fmaf(py.y, fp, y.y));
-                        }
-                        *reinterpret_cast<uint2 *>(dst + off) = make_uint2(floats_to_pair<DT>(x.x, x.y), floats_to_pair<DT>(y.x, y.y));
-                    });
+                all_columns([&](int c, int k, uint4 o) {
+                    const int h = k * 4 + (lane >> 3);
+                    const float fo = __shfl_sync(0xffffffffu, scale, h), fp = __shfl_sync(0xffffffffu, weight, h);
+                    uint8_t *dst = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, to, h));
+                    const uint8_t *src = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, from, h));
+                    if (!dst) return;
+                    const int64_t off = c * 2 + (lane & 7) * 8;
+                    float2 x = make_float2(__uint_as_float(o.x) * fo, __uint_as_float(o.y) * fo);
+                    float2 y = make_float2(__uint_as_float(o.z) * fo, __uint_as_float(o.w) * fo);
+                    if (src) {
+                        const uint2 p = *reinterpret_cast<const uint2 *>(src + off);
+                        const float2 px = pair_to_float<DT>(p.x), py = pair_to_float<DT>(p.y);
+                        x = make_float2(fmaf(px.x, fp, x.x), fmaf(px.y, fp, x.y));
+                        y = make_float2(fmaf(py.x, fp, y.x), fmaf(py.y, fp, y.y));
+                    }
+                    *reinterpret_cast<uint2 *>(dst + off) = make_uint2(floats_to_pair<DT>(x.x, x.y), floats_to_pair<DT>(y.x, y.y));
+                });
             } else {
-                const int64_t place = ((int64_t)pair * 2 + (t0 == 0)) * PAIR_HEADS + rank * CTA_HEADS;
-                if (half == 0) w.ml[place + i] = make_float2(m, l);
-                float *o_at = w.o + (place + (warp & 1) * 32 + (lane >> 3)) * kLatent + half * 256 + (lane & 7) * 4;
+                // As images of 32 columns of the warp's 32 heads (see part_at), by bulk copies:
+                // an SM's own stores take twice as long.  In P's place and, for the others to
+                // go out meanwhile, in the queries', which no product reads any more.
+                const int64_t place = (int64_t)pair * 2 + (t0 == 0);
+                if (half == 0) w.ml[place * PAIR_HEADS + rank * CTA_HEADS + i] = make_float2(m, l);
+                uint8_t *to = w.o + (place * 8 + rank * 4 + warp) * (8 * PART_IMAGE);
+                uint32_t o[32];
+                tmem_ld_32(lanes + T_O, o);
 #pragma unroll 1
-                for (int c = 0; c < 256; c += 32)
-                    columns(c, [&](int k, uint4 o) { st_v4(o_at + (int64_t)k * 4 * kLatent + c, o); });
+                for (int c = 0; c < 8; ++c) {
+                    const uint32_t image = c % 3 == 2 ? base + P_AT + warp * PART_IMAGE : base + Q_AT + (warp * 2 + c % 3) * PART_IMAGE;
+                    if (c >= 3) asm volatile("cp.async.bulk.wait_group.read 2;" ::: "memory");      // (lane 0's)
+                    __syncwarp();
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        st_smem_v4(image + lane * 128 + ((x ^ (lane & 7)) << 4), make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
+                    if (c < 7) tmem_ld_32(lanes + T_O + (c + 1) * 32, o);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n"
+                                     "cp.async.bulk.commit_group;" ::"l"(to + c * PART_IMAGE),
+                                     "r"(image), "n"(PART_IMAGE)
+                                     : "memory");
+                }
+                asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
             }
             tc_fence_before();
         }
@@ -699,47 +736,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
 constexpr int JOIN_NT = 128;
 
 // A CTA a head, four values a thread: its parts from the pairs that have some of its
-// tiles.
+// tiles.  Bound by latency with few heads: so the parts' factors come first, and their
+// values, eight at a time, wait for nothing but their loads.
 template <int DT>
 __global__ void __launch_bounds__(JOIN_NT) join_kernel(const __grid_constant__ PrefixLaunch a, const __grid_constant__ PrefixParts w)
 {
+    __shared__ float factors[MAX_PAIRS];
     after_launch_before();
-    const int tid = threadIdx.x;
-    const int64_t head = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, head = blockIdx.x;
     const HeadPlace at(a, head);
-    const int group = (int)(head / PAIR_HEADS), i = (int)(head % PAIR_HEADS);
+    const int group = head / PAIR_HEADS, i = head % PAIR_HEADS;
     const int64_t begin = (int64_t)group * w.tiles;
-    int p0 = 0, p1 = -1;
+    int p0 = 0, parts = 0;
     if (w.units > 0) {
         p0 = pair_of(w, begin);
-        p1 = pair_of(w, begin + w.tiles - 1);
-        if (p0 == p1) return;      // (that pair has written it)
+        parts = pair_of(w, begin + w.tiles - 1) - p0 + 1;
+        if (parts == 1) return;      // (that pair has written it)
     }
+    // (a pair's second place is for the group that it begins with)
+    const int64_t first = (int64_t)p0 * 2 + (first_unit(w, p0) <= begin);
+    auto place = [&](int p) { return p == 0 ? first : (int64_t)(p0 + p) * 2; };
+    const uint8_t *src = w.o + part_at(i, tid);
+    auto values = [&](int p) { return *reinterpret_cast<const float4 *>(src + place(p) * (PAIR_HEADS * kLatent * 4)); };
     float other = -INFINITY;
     uint2 part = make_uint2(0, 0);
     if (a.part) {
         other = a.part_lse[head];
         part = *reinterpret_cast<const uint2 *>(a.part + at.r * a.part_rs + at.h * a.part_hs + tid * 8);
     }
-    __syncthreads();      // (part may be out, part_lse lse)
-    const float2 *ml = w.ml + i;
-    const float *src = w.o + (int64_t)i * kLatent + tid * 4;
-    // (a pair's second place is for the group that it begins with)
-    auto place = [&](int p) { return ((int64_t)p * 2 + (first_unit(w, p) <= begin)) * PAIR_HEADS; };
-    float m = -INFINITY, l = 0.0f, o[4] = {};
-#pragma unroll 4
-    for (int p = p0; p <= p1; ++p) {
-        const int64_t n = place(p);
-        const float2 x = ml[n];
-        const float4 v = *reinterpret_cast<const float4 *>(src + n * kLatent);
-        const float to = fmaxf(m, x.x), base = to == -INFINITY ? 0.0f : to;
-        const float f = ex2(m - base), g = ex2(x.x - base);
-        m = to;
-        l = l * f + x.y * g;
-        o[0] = o[0] * f + v.x * g;
-        o[1] = o[1] * f + v.y * g;
-        o[2] = o[2] * f + v.z * g;
-        o[3] = o[3] * f + v.w * g;
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k < parts) v[k] = values(k);
+    // every warp for itself: reference and sum of all parts
+    float2 ml[(MAX_PAIRS + 31) / 32];
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < (MAX_PAIRS + 31) / 32; ++k) {
+        const int p = k * 32 + lane;
+        ml[k] = p < parts ? w.ml[place(p) * PAIR_HEADS + i] : make_float2(-INFINITY, 0.0f);
+        m = fmaxf(m, ml[k].x);
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+#pragma unroll
+    for (int k = 0; k < (MAX_PAIRS + 31) / 32; ++k) {
+        const float f = ex2(ml[k].x - (m == -INFINITY ? 0.0f : m));
+        if (k * 32 + lane < parts && tid < 32) factors[k * 32 + lane] = f;
+        if (k * 32 + lane < parts) l = fmaf(f, ml[k].y, l);
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+    __syncthreads();      // (also: part may be out, part_lse lse)
+    float o[4] = {};
+    for (int p = 0; p < parts; p += 8) {
+        if (p > 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (p + k < parts) v[k] = values(p + k);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (p + k < parts) {
+                const float f = factors[p + k];
+                o[0] = fmaf(f, v[k].x, o[0]);
+                o[1] = fmaf(f, v[k].y, o[1]);
+                o[2] = fmaf(f, v[k].z, o[2]);
+                o[3] = fmaf(f, v[k].w, o[3]);
+            }
     }
     float weight = 0.0f, scale = 1.0f;
     if (a.part) scale = add_part(m, l, other, &weight);
@@ -770,7 +834,7 @@ PrefixParts lay_out(int32_t R, int32_t H, int32_t len, uint8_t *ws, int64_t *byt
     w.units = (int64_t)w.tiles * w.groups;
     w.pairs = (int)(w.units < MAX_PAIRS ? w.units : MAX_PAIRS);
     int64_t n = 16;      // never empty
-    w.o = reinterpret_cast<float *>(ws + n);
+    w.o = ws + n;
     n += (int64_t)w.pairs * 2 * PAIR_HEADS * kLatent * 4;
     w.ml = reinterpret_cast<float2 *>(ws + n);
     n += (int64_t)w.pairs * 2 * PAIR_HEADS * 8;
@@ -814,7 +878,7 @@ cudaError_t launch(const PrefixLaunch &a, const PrefixParts &w, cudaStream_t s)
         for (int p = 1; p < w.pairs; ++p) split = split || first_unit(w, p) % w.tiles != 0;
         if (!split) return e;
     }
-    return launch_behind(join_kernel<DT>, dim3((unsigned)((int64_t)a.R * a.H)), JOIN_NT, 0, 1, s, a, w);
+    return launch_behind(join_kernel<DT>, dim3(a.R * a.H), JOIN_NT, 0, 1, s, a, w);
 }
 
 }  // namespace

@@ -44,18 +44,22 @@ __device__ __forceinline__ int32_t pages_needed(const TablesLaunch &a, const Div
     return need <= a.W ? need : -1;
 }
 
-// The slot and position of a place: token i of request r, which begins at first.
-__device__ __forceinline__ void map_token(const TablesLaunch &a, const Divider &by, int r, int32_t first, int32_t i)
+// The position of a request's first new token, or LEFT if its tokens have no slots: it is
+// left as it is, or they are more than its length.  (held: as the call leaves it)
+constexpr int32_t LEFT = INT_MIN;
+__device__ __forceinline__ int32_t first_position(const TablesLaunch &a, int32_t len, int32_t held, int32_t n)
 {
-    const int32_t len = a.lens[r], held = a.held[r], n = a.new_tokens[r];
+    return len >= 0 && n <= len && held >= 0 && held <= a.W && (int64_t)held * a.bs >= len ? len - max(n, 0) : LEFT;
+}
+
+// The slot and position of token p of request r (p below 0: none), to place i.
+__device__ __forceinline__ void map_token(const TablesLaunch &a, const Divider &by, int r, int32_t p, int32_t i)
+{
     int32_t slot = -1, pos = -1;
-    // (a request that is left as it is: its entries do not cover its length)
-    if (len >= 0 && n <= len && held >= 0 && held <= a.W && (int64_t)held * a.bs >= len) {
-        const int32_t p = len - n + (i - first), b = by.over(p);
-        const int32_t page = a.tables[(int64_t)r * a.tables_stride + b];
-        const int64_t s = (int64_t)page * a.bs + (p - b * a.bs);
+    if (p >= 0) {
+        const int32_t b = by.over(p), page = a.tables[(int64_t)r * a.tables_stride + b];
         if (page >= 0 && ((int64_t)page + 1) * a.bs <= kResidentFlag) {
-            slot = (int32_t)s;
+            slot = page * a.bs + (p - b * a.bs);
             pos = p;
         } else if (page >= 0 && a.status) {
             record_status(a.status, r, kStatusBadResident);
@@ -135,20 +139,48 @@ __device__ Sums scan(const Sums &x, Sums *warp_sums, Sums *total)
     return lane > 0 ? plus(before, z) : before;
 }
 
-// Per request, in shared memory.
-struct Request {
-    int32_t held, need;      // need -1: left as it is
-    int32_t from;            // its first page given back or taken, from the end of the list; -1: none
+// Pages j of the call from j0 on in steps: eight at a time, so that their loads do not
+// wait for one another.
+template <class Load, class Store>
+__device__ __forceinline__ void move_pages(int32_t j0, int32_t step, int32_t end, Load load, Store store)
+{
+    constexpr int AT_ONCE = 8;
+    for (int32_t j = j0; j < end; j += AT_ONCE * step) {
+        int32_t page[AT_ONCE];
+        int64_t to[AT_ONCE];
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k)
+            if ((int64_t)j + (int64_t)k * step < end) load(j + k * step, page[k], to[k]);
+#pragma unroll
+        for (int k = 0; k < AT_ONCE; ++k)
+            if ((int64_t)j + (int64_t)k * step < end) store(page[k], to[k]);
+    }
+}
+
+// Per request, in shared memory: entries in use and needed (-1: left as it is), the
+// first page that it gives back or takes, from the end of the list, its first place and
+// the position there.
+struct Requests {
+    int32_t *held, *need, *freed, *grown, *start, *first;
+    __device__ __forceinline__ Requests(uint8_t *smem, int R)
+    {
+        held = reinterpret_cast<int32_t *>(smem);
+        need = held + R;
+        freed = need + R;
+        grown = freed + R;
+        start = grown + R;      // with MAP
+        first = start + R;      // [R + 1], with MAP
+    }
 };
+size_t requests_bytes(int R, bool map) { return ((size_t)R * (map ? 6 : 4) + 1) * 4; }
 
 template <bool MAP>
 __global__ void __launch_bounds__(TB_NT, 1) tables_kernel(const __grid_constant__ TablesLaunch a, const __grid_constant__ Divider by)
 {
     extern __shared__ __align__(16) uint8_t smem[];
-    Request *req = reinterpret_cast<Request *>(smem);
-    int32_t *first = reinterpret_cast<int32_t *>(req + a.R);      // [R + 1], with MAP
     __shared__ Sums warp_sums[TB_WARPS];
     __shared__ int32_t taken;
+    const Requests q(smem, a.R);
     const int tid = threadIdx.x, lane = tid & 31;
     const int rank = blockIdx.x, ctas = gridDim.x;
     const bool alone = ctas == 1;
@@ -157,15 +189,16 @@ __global__ void __launch_bounds__(TB_NT, 1) tables_kernel(const __grid_constant_
 
     // ---- sums over the requests -------------------------------------------------
     const int per = (a.R + TB_NT - 1) / TB_NT, r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+    auto own = [&](int32_t n) { return max(n - a.shared_count, 0); };      // of n entries
     Sums mine = {0, 0, 0};
     for (int r = r0; r < r1; ++r) {
         const int32_t len = a.lens[r], held = a.held[r], n = a.new_tokens ? a.new_tokens[r] : 0;
         const int32_t need = pages_needed(a, by, len, held);
-        req[r] = {held, need, -1};
+        q.held[r] = held;
+        q.need[r] = need;
         if (need >= 0) {
-            const int32_t own = max(need - a.shared_count, 0), had = max(held - a.shared_count, 0);
-            mine.freed += max(had - own, 0);
-            mine.grown += max(own - had, 0);
+            mine.freed += max(own(held) - own(need), 0);
+            mine.grown += max(own(need) - own(held), 0);
         }
         mine.tokens += max(n, 0);
         if (rank == 0 && a.status) {
@@ -182,26 +215,26 @@ __global__ void __launch_bounds__(TB_NT, 1) tables_kernel(const __grid_constant_
     // (a list without room for all that comes back keeps as much as it holds)
     const int32_t there = (int32_t)min((int64_t)count + total.freed, (int64_t)a.free_capacity);
     for (int r = r0; r < r1; ++r) {
-        Request &q = req[r];
-        if (q.need >= 0) {
-            const int32_t own = max(q.need - a.shared_count, 0), had = max(q.held - a.shared_count, 0);
-            if (own <= had) {
-                q.from = at.freed;
-                at.freed += had - own;
-            } else {
-                q.from = at.grown;
-                at.grown += own - had;
-                if (at.grown <= there) {
-                    atomicMax(&taken, at.grown);
-                } else {
-                    q.need = -1;
-                    if (rank == 0 && a.status) record_status(a.status, r, kStatusCapacity);
-                }
+        const int32_t held = q.held[r], need = q.need[r];
+        q.freed[r] = at.freed;
+        q.grown[r] = at.grown;
+        if (need >= 0) {
+            const int32_t more = max(own(need) - own(held), 0);
+            at.freed += max(own(held) - own(need), 0);
+            at.grown += more;
+            if (more > 0 && at.grown > there) {
+                q.need[r] = -1;
+                if (rank == 0 && a.status) record_status(a.status, r, kStatusCapacity);
+            } else if (more > 0) {
+                atomicMax(&taken, at.grown);
             }
         }
         if (a.new_tokens) {
-            const int32_t n = max(a.new_tokens[r], 0), f = (int32_t)min(at.tokens, (int64_t)INT_MAX);
-            if (MAP) first[r] = f;
+            const int32_t news = a.new_tokens[r], n = max(news, 0), f = (int32_t)min(at.tokens, (int64_t)INT_MAX);
+            if (MAP) {
+                q.first[r] = f;
+                q.start[r] = first_position(a, a.lens[r], q.need[r] >= 0 ? q.need[r] : held, news);
+            }
             if (rank == 0) {
                 a.offsets[r] = f;
                 if (a.status && n > 0 && at.tokens + n > a.tokens) record_status(a.status, r, kStatusCapacity);
@@ -211,53 +244,65 @@ __global__ void __launch_bounds__(TB_NT, 1) tables_kernel(const __grid_constant_
     }
     if (a.new_tokens && tid == 0) {
         const int32_t end = (int32_t)min(total.tokens, (int64_t)INT_MAX);
-        if (MAP) first[a.R] = end;
+        if (MAP) q.first[a.R] = end;
         if (rank == 0) a.offsets[a.R] = end;
     }
     __syncthreads();
 
-    // ---- pages given back ------------------------------------------------------------
-    const int warp = rank * TB_WARPS + (tid >> 5), warps = ctas * TB_WARPS;
-    if (total.freed > 0 || a.shared_count > 0) {
-        for (int r = warp; r < a.R; r += warps) {
-            const Request q = req[r];
-            if (q.need < 0 || q.need >= q.held) continue;
+    // ---- pages given back: the j-th of all is request r's (j - freed[r])-th -----------------
+    const int32_t j0 = rank * TB_NT + tid, step = ctas * TB_NT;
+    move_pages(
+        j0, step, total.freed,
+        [&](int32_t j, int32_t &page, int64_t &to) {
+            const int r = find_request(q.freed, 0, a.R - 1, j);
+            int32_t *entry = a.tables + (int64_t)r * a.tables_stride + max(q.need[r], a.shared_count) + (j - q.freed[r]);
+            page = *entry;
+            *entry = -1;
+            to = there - 1 - j;
+        },
+        [&](int32_t page, int64_t to) {
+            if (to >= 0) a.free_list[to] = page;
+        });
+    // entries of the shared prefix, a warp a request
+    auto shared_entries = [&](bool back) {
+        if (a.shared_count == 0) return;
+        for (int r = rank * TB_WARPS + (tid >> 5); r < a.R; r += ctas * TB_WARPS) {
+            const int32_t held = q.held[r], need = q.need[r];
+            if (need < 0) continue;
             int32_t *row = a.tables + (int64_t)r * a.tables_stride;
-            for (int32_t e = q.need + lane; e < q.held; e += 32) {
-                const int32_t page = row[e], to = there - 1 - (q.from + e - max(q.need, a.shared_count));
-                row[e] = -1;
-                if (e >= a.shared_count && to >= 0) a.free_list[to] = page;
-            }
+            const int32_t from = back ? need : held, to = min(back ? held : need, a.shared_count);
+            for (int32_t e = from + lane; e < to; e += 32) row[e] = back ? -1 : a.shared[e];
         }
-    }
+    };
+    shared_entries(true);
     // (also: every CTA has read the lengths and counts that are written below)
     cluster_sync(alone);
 
     // ---- pages taken -----------------------------------------------------------------
-    for (int r = warp; r < a.R; r += warps) {
-        const Request q = req[r];
-        if (q.need < 0) continue;
-        int32_t *row = a.tables + (int64_t)r * a.tables_stride;
-        for (int32_t e = q.held + lane; e < q.need; e += 32) {
-            const int32_t at = there - 1 - (q.from + e - max(q.held, a.shared_count));
-            row[e] = e < a.shared_count ? a.shared[e] : a.free_list[at];
-        }
-        if (lane == 0 && q.need != q.held) a.held[r] = q.need;
+    const int32_t takes = taken;
+    move_pages(
+        j0, step, takes,
+        [&](int32_t j, int32_t &page, int64_t &to) {
+            const int r = find_request(q.grown, 0, a.R - 1, j);
+            to = (int64_t)r * a.tables_stride + max(q.held[r], a.shared_count) + (j - q.grown[r]);
+            page = a.free_list[there - 1 - j];
+        },
+        [&](int32_t page, int64_t to) { a.tables[to] = page; });
+    shared_entries(false);
+    if (rank == 0) {
+        for (int r = tid; r < a.R; r += TB_NT)
+            if (q.need[r] >= 0 && q.need[r] != q.held[r]) a.held[r] = q.need[r];
+        if (tid == 0) *a.free_count = there - takes;
     }
-    if (rank == 0 && tid == 0) *a.free_count = there - taken;
 
     // ---- slots -----------------------------------------------------------------------
     if (MAP) {
         cluster_sync(alone);
-        const int32_t end = min(first[a.R], a.tokens);
-        for (int32_t i = rank * TB_NT + tid; i < a.tokens; i += ctas * TB_NT) {
-            if (i < end) {
-                const int r = find_request(first, 0, a.R - 1, i);
-                map_token(a, by, r, first[r], i);
-            } else {
-                a.slots[i] = -1;
-                if (a.positions) a.positions[i] = -1;
-            }
+        const int32_t end = min(q.first[a.R], a.tokens);
+        for (int32_t i = j0; i < a.tokens; i += step) {
+            const int r = i < end ? find_request(q.first, 0, a.R - 1, i) : 0;
+            const int32_t start = i < end ? q.start[r] : LEFT;
+            map_token(a, by, r, start == LEFT ? -1 : start + (i - q.first[r]), i);
         }
     }
 }
@@ -273,14 +318,23 @@ __global__ void __launch_bounds__(MAP_NT) map_kernel(const __grid_constant__ Tab
         lo = find_request(a.offsets, 0, a.R - 1, begin);
         hi = find_request(a.offsets, lo, a.R - 1, min(last, end - 1));
     }
+    auto look = [&](int r) {
+        const int32_t start = first_position(a, a.lens[r], a.held[r], a.new_tokens[r]);
+        return start == LEFT ? LEFT : start - a.offsets[r];
+    };
+    if (lo == hi && begin < end) {      // one request (or none behind the last token)
+        const int32_t start = look(lo);
+#pragma unroll
+        for (int k = 0; k < MAP_TOKENS / MAP_NT; ++k) {
+            const int32_t i = begin + k * MAP_NT + threadIdx.x;
+            if (i <= last) map_token(a, by, lo, i < end && start != LEFT ? start + i : -1, i);
+        }
+    } else {
 #pragma unroll 4
-    for (int32_t i = begin + threadIdx.x; i <= last; i += MAP_NT) {
-        if (i < end) {
-            const int r = find_request(a.offsets, lo, hi, i);
-            map_token(a, by, r, a.offsets[r], i);
-        } else {
-            a.slots[i] = -1;
-            if (a.positions) a.positions[i] = -1;
+        for (int32_t i = begin + threadIdx.x; i <= last; i += MAP_NT) {
+            const int r = i < end ? find_request(a.offsets, lo, hi, i) : 0;
+            const int32_t start = i < end ? look(r) : LEFT;
+            map_token(a, by, r, start == LEFT ? -1 : start + i, i);
         }
     }
 }
@@ -292,7 +346,7 @@ cudaError_t launch_page_tables(const TablesLaunch &a, cudaStream_t s)
     const Divider by(a.bs);
     const bool map = a.new_tokens && a.tokens <= 16384;
     const unsigned ctas = a.R > 32 ? 8 : 1;
-    const size_t smem = (size_t)a.R * sizeof(Request) + ((size_t)a.R + 1) * 4;
+    const size_t smem = requests_bytes(a.R, map);
     auto kernel = map ? tables_kernel<true> : tables_kernel<false>;
     if (smem > 40000) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
