@@ -16,7 +16,7 @@
 namespace hs {
 namespace {
 
-constexpr int ROWS_NT = 128, ROWS_CTAS = 12;     // threads a CTA, CTAs an SM
+constexpr int ROWS_NT = 128, ROWS_CTAS = 14;     // threads a CTA, CTAs an SM
 constexpr int ROWS_A_CTA = ROWS_NT / 32;
 
 template <int DT>

@@ -20,7 +20,6 @@
 namespace hs {
 namespace {
 
-constexpr int TB_NT = 1024, TB_WARPS = TB_NT / 32;
 constexpr int MAP_NT = 256, MAP_TOKENS = 2048;      // the mapping launch: tokens a CTA
 
 // n / d for 0 <= n < 2^31, 1 <= d < 2^31, as a product and a shift.
@@ -82,16 +81,17 @@ __device__ __forceinline__ int find_request(const int32_t *first, int lo, int hi
     return lo;
 }
 
-// All that the cluster's CTAs have written is visible to all of them.
-__device__ __forceinline__ void cluster_sync(bool alone)
+// All that the CTAs have written is visible to all of them.
+template <int CTAS>
+__device__ __forceinline__ void all_sync()
 {
-    if (alone) {
+    if (CTAS == 1) {
         __syncthreads();
-    } else {
-        __syncwarp();
-        asm volatile("barrier.cluster.arrive.release.aligned;\n"
-                     "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        return;
     }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 struct Sums {
@@ -110,7 +110,8 @@ __device__ __forceinline__ Sums shfl_up(const Sums &x, int d)
             __shfl_up_sync(0xffffffffu, x.tokens, d)};
 }
 
-// Exclusive sums over the CTA's threads, and all of them in *total.
+// Exclusive sums over the CTA's threads (at most 32 warps), and all of them in *total.
+template <int WARPS>
 __device__ Sums scan(const Sums &x, Sums *warp_sums, Sums *total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -123,37 +124,49 @@ __device__ Sums scan(const Sums &x, Sums *warp_sums, Sums *total)
     if (lane == 31) warp_sums[warp] = y;
     __syncthreads();
     if (warp == 0) {
-        Sums w = warp_sums[lane];
+        Sums w = {0, 0, 0};
+        if (lane < WARPS) w = warp_sums[lane];
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const Sums z = shfl_up(w, d);
             if (lane >= d) w = plus(w, z);
         }
-        warp_sums[lane] = w;
+        if (lane < WARPS) warp_sums[lane] = w;
     }
     __syncthreads();
-    *total = warp_sums[TB_WARPS - 1];
+    *total = warp_sums[WARPS - 1];
     const Sums z = shfl_up(y, 1);
     Sums before = {0, 0, 0};
     if (warp > 0) before = warp_sums[warp - 1];
     return lane > 0 ? plus(before, z) : before;
 }
 
-// Pages j of the call from j0 on in steps: eight at a time, so that their loads do not
-// wait for one another.
+// Pages [0, end) of a call, j of them before request r being first[r]: neighbours, which
+// are mostly one request's, a warp, up to eight a lane at a time, so that their loads do
+// not wait for one another.
 template <class Load, class Store>
-__device__ __forceinline__ void move_pages(int32_t j0, int32_t step, int32_t end, Load load, Store store)
+__device__ __forceinline__ void move_pages(const int32_t *first, int requests, int warp, int warps, int32_t end, Load load, Store store)
 {
     constexpr int AT_ONCE = 8;
-    for (int32_t j = j0; j < end; j += AT_ONCE * step) {
+    const int lane = threadIdx.x & 31;
+    const int32_t a_warp = min((end + warps * 32 - 1) / (warps * 32), AT_ONCE) * 32;
+    for (int64_t j0 = (int64_t)warp * a_warp; j0 < end; j0 += (int64_t)warps * a_warp) {
+        const int32_t last = (int32_t)min(j0 + a_warp, (int64_t)end) - 1;
+        int lo = 0, hi = requests - 1;
+        if (a_warp > 32) {
+            lo = find_request(first, 0, requests - 1, (int32_t)j0);
+            hi = find_request(first, lo, requests - 1, last);
+        }
         int32_t page[AT_ONCE];
         int64_t to[AT_ONCE];
 #pragma unroll
-        for (int k = 0; k < AT_ONCE; ++k)
-            if ((int64_t)j + (int64_t)k * step < end) load(j + k * step, page[k], to[k]);
+        for (int k = 0; k < AT_ONCE; ++k) {
+            const int64_t j = j0 + k * 32 + lane;
+            if (j <= last) load(find_request(first, lo, hi, (int32_t)j), (int32_t)j, page[k], to[k]);
+        }
 #pragma unroll
         for (int k = 0; k < AT_ONCE; ++k)
-            if ((int64_t)j + (int64_t)k * step < end) store(page[k], to[k]);
+            if (j0 + k * 32 + lane <= last) store(page[k], to[k]);
     }
 }
 
@@ -174,21 +187,23 @@ struct Requests {
 };
 size_t requests_bytes(int R, bool map) { return ((size_t)R * (map ? 6 : 4) + 1) * 4; }
 
-template <bool MAP>
-__global__ void __launch_bounds__(TB_NT, 1) tables_kernel(const __grid_constant__ TablesLaunch a, const __grid_constant__ Divider by)
+template <int CTAS, int NT, bool MAP>
+__global__ void __launch_bounds__(NT, 1) tables_kernel(const __grid_constant__ TablesLaunch a, const __grid_constant__ Divider by)
 {
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ Sums warp_sums[TB_WARPS];
+    constexpr int WARPS = NT / 32;
+    static_assert(WARPS <= 32, "scan");
+    __shared__ Sums warp_sums[WARPS];
     __shared__ int32_t taken;
     const Requests q(smem, a.R);
     const int tid = threadIdx.x, lane = tid & 31;
-    const int rank = blockIdx.x, ctas = gridDim.x;
-    const bool alone = ctas == 1;
+    const int rank = blockIdx.x;
     if (tid == 0) taken = 0;
     after_launch_before();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");      // (map_kernel waits itself)
 
     // ---- sums over the requests -------------------------------------------------
-    const int per = (a.R + TB_NT - 1) / TB_NT, r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+    const int per = (a.R + NT - 1) / NT, r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
     auto own = [&](int32_t n) { return max(n - a.shared_count, 0); };      // of n entries
     Sums mine = {0, 0, 0};
     for (int r = r0; r < r1; ++r) {
@@ -211,7 +226,7 @@ __global__ void __launch_bounds__(TB_NT, 1) tables_kernel(const __grid_constant_
     }
     const int32_t count = min(max(*a.free_count, 0), a.free_capacity);
     Sums total;
-    Sums at = scan(mine, warp_sums, &total);
+    Sums at = scan<WARPS>(mine, warp_sums, &total);
     // (a list without room for all that comes back keeps as much as it holds)
     const int32_t there = (int32_t)min((int64_t)count + total.freed, (int64_t)a.free_capacity);
     for (int r = r0; r < r1; ++r) {
@@ -250,11 +265,10 @@ __global__ void __launch_bounds__(TB_NT, 1) tables_kernel(const __grid_constant_
     __syncthreads();
 
     // ---- pages given back: the j-th of all is request r's (j - freed[r])-th -----------------
-    const int32_t j0 = rank * TB_NT + tid, step = ctas * TB_NT;
+    const int warp = rank * WARPS + (tid >> 5), warps = CTAS * WARPS;
     move_pages(
-        j0, step, total.freed,
-        [&](int32_t j, int32_t &page, int64_t &to) {
-            const int r = find_request(q.freed, 0, a.R - 1, j);
+        q.freed, a.R, warp, warps, total.freed,
+        [&](int r, int32_t j, int32_t &page, int64_t &to) {
             int32_t *entry = a.tables + (int64_t)r * a.tables_stride + max(q.need[r], a.shared_count) + (j - q.freed[r]);
             page = *entry;
             *entry = -1;
@@ -266,7 +280,7 @@ __global__ void __launch_bounds__(TB_NT, 1) tables_kernel(const __grid_constant_
     // entries of the shared prefix, a warp a request
     auto shared_entries = [&](bool back) {
         if (a.shared_count == 0) return;
-        for (int r = rank * TB_WARPS + (tid >> 5); r < a.R; r += ctas * TB_WARPS) {
+        for (int r = warp; r < a.R; r += warps) {
             const int32_t held = q.held[r], need = q.need[r];
             if (need < 0) continue;
             int32_t *row = a.tables + (int64_t)r * a.tables_stride;
@@ -276,30 +290,29 @@ __global__ void __launch_bounds__(TB_NT, 1) tables_kernel(const __grid_constant_
     };
     shared_entries(true);
     // (also: every CTA has read the lengths and counts that are written below)
-    cluster_sync(alone);
+    all_sync<CTAS>();
 
     // ---- pages taken -----------------------------------------------------------------
     const int32_t takes = taken;
     move_pages(
-        j0, step, takes,
-        [&](int32_t j, int32_t &page, int64_t &to) {
-            const int r = find_request(q.grown, 0, a.R - 1, j);
+        q.grown, a.R, warp, warps, takes,
+        [&](int r, int32_t j, int32_t &page, int64_t &to) {
             to = (int64_t)r * a.tables_stride + max(q.held[r], a.shared_count) + (j - q.grown[r]);
             page = a.free_list[there - 1 - j];
         },
         [&](int32_t page, int64_t to) { a.tables[to] = page; });
     shared_entries(false);
     if (rank == 0) {
-        for (int r = tid; r < a.R; r += TB_NT)
+        for (int r = tid; r < a.R; r += NT)
             if (q.need[r] >= 0 && q.need[r] != q.held[r]) a.held[r] = q.need[r];
         if (tid == 0) *a.free_count = there - takes;
     }
 
     // ---- slots -----------------------------------------------------------------------
     if (MAP) {
-        cluster_sync(alone);
+        all_sync<CTAS>();
         const int32_t end = min(q.first[a.R], a.tokens);
-        for (int32_t i = j0; i < a.tokens; i += step) {
+        for (int32_t i = rank * NT + tid; i < a.tokens; i += CTAS * NT) {
             const int r = i < end ? find_request(q.first, 0, a.R - 1, i) : 0;
             const int32_t start = i < end ? q.start[r] : LEFT;
             map_token(a, by, r, start == LEFT ? -1 : start + (i - q.first[r]), i);
@@ -310,13 +323,31 @@ __global__ void __launch_bounds__(TB_NT, 1) tables_kernel(const __grid_constant_
 // The slots of many tokens, behind tables_kernel: MAP_TOKENS of them a CTA.
 __global__ void __launch_bounds__(MAP_NT) map_kernel(const __grid_constant__ TablesLaunch a, const __grid_constant__ Divider by)
 {
-    after_launch_before();
+    __shared__ int32_t sums[2][MAP_NT / 32];
     const int32_t begin = blockIdx.x * MAP_TOKENS, last = min(a.tokens - begin, MAP_TOKENS) - 1 + begin;
+    after_launch_before();
     const int32_t end = min(a.offsets[a.R], a.tokens);
+    // The requests of the first and the last token: as many as begin at or before them,
+    // counted by all threads at once (a search: 9 to 13 loads one behind the other).
     int lo = 0, hi = 0;
-    if (begin < end) {
-        lo = find_request(a.offsets, 0, a.R - 1, begin);
-        hi = find_request(a.offsets, lo, a.R - 1, min(last, end - 1));
+#pragma unroll 4
+    for (int r = threadIdx.x; r < a.R; r += MAP_NT) {
+        const int32_t first = a.offsets[r];
+        lo += first <= begin;
+        hi += first <= min(last, end - 1);
+    }
+    lo = __reduce_add_sync(0xffffffffu, lo);
+    hi = __reduce_add_sync(0xffffffffu, hi);
+    if ((threadIdx.x & 31) == 0) {
+        sums[0][threadIdx.x >> 5] = lo;
+        sums[1][threadIdx.x >> 5] = hi;
+    }
+    __syncthreads();
+    lo = hi = -1;
+#pragma unroll
+    for (int k = 0; k < MAP_NT / 32; ++k) {
+        lo += sums[0][k];
+        hi += sums[1][k];
     }
     auto look = [&](int r) {
         const int32_t start = first_position(a, a.lens[r], a.held[r], a.new_tokens[r]);
@@ -341,19 +372,31 @@ __global__ void __launch_bounds__(MAP_NT) map_kernel(const __grid_constant__ Tab
 
 }  // namespace
 
+template <int CTAS, int NT, bool MAP>
+static cudaError_t launch_tables(const TablesLaunch &a, const Divider &by, cudaStream_t s)
+{
+    const size_t smem = requests_bytes(a.R, MAP);
+    if (smem > 40000) {
+        const cudaError_t e = cudaFuncSetAttribute(tables_kernel<CTAS, NT, MAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_behind(tables_kernel<CTAS, NT, MAP>, dim3(CTAS), NT, smem, CTAS, s, a, by);
+}
+
 cudaError_t launch_page_tables(const TablesLaunch &a, cudaStream_t s)
 {
     const Divider by(a.bs);
+    // Few slots in the same launch (1.0 M in one: 69 us for 256 requests, 25 in two).
     const bool map = a.new_tokens && a.tokens <= 16384;
-    const unsigned ctas = a.R > 32 ? 8 : 1;
-    const size_t smem = requests_bytes(a.R, map);
-    auto kernel = map ? tables_kernel<true> : tables_kernel<false>;
-    if (smem > 40000) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    const cudaError_t e = launch_behind(kernel, dim3(ctas), TB_NT, smem, ctas, s, a, by);
-    if (e != cudaSuccess || !a.new_tokens || map) return e;
+    // One CTA for what a decode step moves (32 requests, 4 drafts each: 7.0 us for a call
+    // there and one back, 8.5 with a cluster), a cluster of eight where whole prompts come
+    // and go (128 requests of 2,048 to 81,920 tokens: 22.6 us, 90 with one CTA).  What a call
+    // moves is known on the device alone: a step has few tokens, and where none are
+    // placed, few requests.
+    const bool step = a.new_tokens ? a.R <= 256 && a.tokens <= 4096 : a.R <= 32;
+    const cudaError_t e = step ? map ? launch_tables<1, 256, true>(a, by, s) : launch_tables<1, 256, false>(a, by, s)
+                               : map ? launch_tables<8, 1024, true>(a, by, s) : launch_tables<8, 1024, false>(a, by, s);
+    if (e != cudaSuccess || !a.new_tokens || map || a.tokens == 0) return e;
     return launch_behind(map_kernel, dim3((a.tokens + MAP_TOKENS - 1) / MAP_TOKENS), MAP_NT, 0, 1, s, a, by);
 }
 

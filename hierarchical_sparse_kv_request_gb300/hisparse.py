@@ -757,25 +757,18 @@ def evict_select(weights, slot2tok, seq_lens, out_slots, out_counts, keep_recent
 
 # -- resident pages (include/hisparse_pages.h) ------------------------------
 
-def _here(device: int, **tensors) -> None:
-    """Tensors (None: not there) are on the current device."""
-    for name, x in tensors.items():
-        if x is not None and x.get_device() != device:
-            raise ValueError(f"{name} is not on the current device, {device}")
-
-
-def _reachable(device: int, **tensors) -> None:
-    """Tensors (None: not there) are on the current device or in pinned memory."""
-    for name, x in tensors.items():
-        if x is not None and x.get_device() != device and not (x.get_device() == -1 and x.is_pinned()):
-            raise ValueError(f"{name} is neither on the current device, {device}, nor pinned")
+def _reachable(x, device: int, what: str) -> None:
+    """x (None: not there) is on the current device or in pinned memory."""
+    if x is not None and x.get_device() != device and not (x.get_device() == -1 and x.is_pinned()):
+        raise ValueError(f"{what} is neither on the current device, {device}, nor pinned")
 
 
 def _line(x, what: str) -> int:
     """Length of x, a contiguous int32 tensor of one dimension."""
-    if x.dtype is not (_torch or _load_torch()).int32 or len(x.shape) != 1 or not x.is_contiguous():
+    shape = x.shape
+    if x.dtype is not (_torch or _load_torch()).int32 or len(shape) != 1 or not x.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor of one dimension")
-    return x.shape[0]
+    return shape[0]
 
 
 def page_tables(lens, tables, held, free_list, free_count, block_size: int, shared=None,
@@ -794,29 +787,38 @@ def page_tables(lens, tables, held, free_list, free_count, block_size: int, shar
     if _line(held, "held") != R or _line(free_count, "free_count") != 1:
         raise ValueError(f"held must have {R} entries and free_count one")
     capacity = _line(free_list, "free_list")
-    prefix = 0 if shared is None else _line(shared, "shared")
-    tokens = 0
+    prefix = tokens = 0
+    prefix_at = new_at = offsets_at = slots_at = positions_at = 0
+    device = _current_device()
+    here = (tables.get_device() == device and held.get_device() == device and free_list.get_device() == device
+            and free_count.get_device() == device)
+    _reachable(lens, device, "lens")
+    if shared is not None:
+        prefix, prefix_at = _line(shared, "shared"), shared.data_ptr()
+        _reachable(shared, device, "shared")
     if new_tokens is not None:
-        if _line(new_tokens, "new_tokens") != R:
-            raise ValueError(f"new_tokens must have {R} entries")
         if offsets is None or slots is None:
             raise ValueError("new_tokens need offsets and slots")
         tokens = _line(slots, "slots")
-        if _line(offsets, "offsets") != R + 1 or positions is not None and _line(positions, "positions") != tokens:
-            raise ValueError(f"offsets must have {R + 1} entries, and positions as many as slots")
+        if _line(new_tokens, "new_tokens") != R or _line(offsets, "offsets") != R + 1:
+            raise ValueError(f"new_tokens must have {R} entries and offsets {R + 1}")
+        new_at, offsets_at, slots_at = new_tokens.data_ptr(), offsets.data_ptr(), slots.data_ptr()
+        _reachable(new_tokens, device, "new_tokens")
+        here = here and offsets.get_device() == device and slots.get_device() == device
+        if positions is not None:
+            if _line(positions, "positions") != tokens:
+                raise ValueError("positions and slots differ in length")
+            positions_at = positions.data_ptr()
+            here = here and positions.get_device() == device
     elif offsets is not None or slots is not None or positions is not None:
         raise ValueError("offsets, slots and positions need new_tokens")
     words = _words(status, R)
-    device = _current_device()
-    _here(device, tables=tables, held=held, free_list=free_list, free_count=free_count, offsets=offsets,
-          slots=slots, positions=positions, status=None if isinstance(status, int) else status)
-    _reachable(device, lens=lens, new_tokens=new_tokens, shared=shared)
-    at = _addr
-    args = _pack_page_tables_args(
+    if not here or words and status is not words and status.get_device() != device:
+        raise ValueError(f"only lens, new_tokens and shared may be outside the current device, {device}")
+    _check((_lib or load_library()).hisparse_page_tables(_pack_page_tables_args(
         R, blocks, block_size, prefix, lens.data_ptr(), tables.data_ptr(), stride, held.data_ptr(),
-        free_list.data_ptr(), capacity, free_count.data_ptr(), at(shared) or 0, at(new_tokens) or 0,
-        at(offsets) or 0, at(slots) or 0, at(positions) or 0, tokens, words)
-    _check((_lib or load_library()).hisparse_page_tables(args, _stream(stream)), "hisparse_page_tables")
+        free_list.data_ptr(), capacity, free_count.data_ptr(), prefix_at, new_at, offsets_at, slots_at,
+        positions_at, tokens, words), _stream(stream)), "hisparse_page_tables")
 
 
 def _format_rows(rows, what: str):
@@ -842,7 +844,10 @@ def _row_values(values, rows, slots):
             raise ValueError(f"slots must have {n} entries")
     elif count < n:
         raise ValueError("more values than rows")
-    _reachable(_current_device(), values=values, rows=rows, slots=slots)
+    device = _current_device()
+    _reachable(values, device, "values")
+    _reachable(rows, device, "rows")
+    _reachable(slots, device, "slots")
     return dt, n, strides[0] if n > 1 else ROW4_VALUES, count, stride, row_bytes
 
 
@@ -853,13 +858,15 @@ def norm_rows(values, rows, slots=None, weight=None, eps: float = 1e-6, stream=N
     in the rows' format.  slots int32 [n] (negative: not stored) or None: row i.
     On the current device or in pinned host memory."""
     dt, n, vs, count, rs, row_bytes = _row_values(values, rows, slots)
+    weight_at = None
     if weight is not None:
         if weight.dtype is not values.dtype or weight.shape != (ROW4_LATENT,) or not weight.is_contiguous():
             raise ValueError(f"weight must be a contiguous [{ROW4_LATENT}] of the values' type")
-        _reachable(_current_device(), weight=weight)
+        _reachable(weight, _current_device(), "weight")
+        weight_at = weight.data_ptr()
     _check((_lib or load_library()).hisparse_norm_rows(
-        values.data_ptr(), vs, dt, n, _addr(weight), eps, rows.data_ptr(), rs, row_bytes, count,
-        _addr(slots), _stream(stream)), "hisparse_norm_rows")
+        values.data_ptr(), vs, dt, n, weight_at, eps, rows.data_ptr(), rs, row_bytes, count,
+        None if slots is None else slots.data_ptr(), _stream(stream)), "hisparse_norm_rows")
 
 
 def gather_rows(rows, values, slots=None, stream=None) -> None:
@@ -867,8 +874,13 @@ def gather_rows(rows, values, slots=None, stream=None) -> None:
     rows[slots[i]] stands for; arguments as norm_rows()."""
     dt, n, vs, count, rs, row_bytes = _row_values(values, rows, slots)
     _check((_lib or load_library()).hisparse_gather_rows(
-        rows.data_ptr(), rs, row_bytes, count, _addr(slots), n, values.data_ptr(), vs, dt,
-        _stream(stream)), "hisparse_gather_rows")
+        rows.data_ptr(), rs, row_bytes, count, None if slots is None else slots.data_ptr(), n,
+        values.data_ptr(), vs, dt, _stream(stream)), "hisparse_gather_rows")
+
+
+def _sums(x, what: str, R: int, H: int) -> None:
+    if x.dtype is not _torch.float32 or x.shape != (R, H) or not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous float32 tensor of shape ({R}, {H})")
 
 
 def attend_prefix_workspace_bytes(num_requests: int, num_heads: int, prefix_len: int) -> int:
@@ -897,37 +909,46 @@ def attend_prefix(q, rows, table, block_size: int, prefix_len: int, out, scale: 
     if len(shape) != 3 or shape[2] != ROW4_VALUES or strides[2] != 1:
         raise ValueError(f"q must be [R][H][{ROW4_VALUES}] with contiguous heads")
     R, H = shape[0], shape[1]
-    places = []
-    for name, x in (("out", out), ("part", part)):
-        places.append((0, 0, 0))
-        if x is not None:
-            s = x.stride()
-            if x.dtype is not q.dtype or x.shape != (R, H, ROW4_LATENT) or s[2] != 1:
-                raise ValueError(f"{name} must be [{R}][{H}][{ROW4_LATENT}] of q's type with contiguous heads")
-            places[-1] = (x.data_ptr(), s[0], s[1])
-    for name, x in (("lse", lse), ("part_lse", part_lse)):
-        if x is not None and (x.dtype is not _torch.float32 or x.shape != (R, H) or not x.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous float32 tensor of shape ({R}, {H})")
-    if (part is None) != (part_lse is None):
-        raise ValueError("part and part_lse go together")
+    out_strides = out.stride()
+    if out.dtype is not q.dtype or out.shape != (R, H, ROW4_LATENT) or out_strides[2] != 1:
+        raise ValueError(f"out must be [{R}][{H}][{ROW4_LATENT}] of q's type with contiguous heads")
     count, row_stride, row_bytes = _format_rows(rows, "rows")
     if block_size < 1 or _line(table, "table") * block_size < prefix_len:
         raise ValueError(f"table names fewer than {prefix_len} tokens")
     words = _words(status, R)
     device = _current_device()
-    _here(device, q=q, rows=rows, out=out, part=part, lse=lse, part_lse=part_lse, workspace=workspace,
-          status=None if isinstance(status, int) else status)
-    _reachable(device, table=table)
+    here = q.get_device() == device and rows.get_device() == device and out.get_device() == device
+    lse_at = part_at = part_lse_at = 0
+    part_strides = (0, 0)
+    if lse is not None:
+        _sums(lse, "lse", R, H)
+        lse_at = lse.data_ptr()
+        here = here and lse.get_device() == device
+    if part is not None:
+        part_strides = part.stride()
+        if part.dtype is not q.dtype or part.shape != (R, H, ROW4_LATENT) or part_strides[2] != 1:
+            raise ValueError(f"part must be [{R}][{H}][{ROW4_LATENT}] of q's type with contiguous heads")
+        if part_lse is None:
+            raise ValueError("part needs part_lse")
+        _sums(part_lse, "part_lse", R, H)
+        part_at, part_lse_at = part.data_ptr(), part_lse.data_ptr()
+        here = here and part.get_device() == device and part_lse.get_device() == device
+    elif part_lse is not None:
+        raise ValueError("part_lse needs part")
+    if (not here or workspace is not None and workspace.get_device() != device
+            or words and status is not words and status.get_device() != device):
+        raise ValueError(f"only table may be outside the current device, {device}")
+    _reachable(table, device, "table")
     launch_stream = _stream(stream)
     if workspace is None:
         workspace = _allocate(attend_prefix_workspace_bytes(R, H, prefix_len), q.device, stream, launch_stream)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    args = _pack_attend_prefix_args(
+    _check((_lib or load_library()).hisparse_attend_prefix(_pack_attend_prefix_args(
         R, H, dt, row_bytes, q.data_ptr(), strides[0], strides[1], rows.data_ptr(), row_stride, count,
-        table.data_ptr(), block_size, prefix_len, scale, *places[1], 0 if part_lse is None else part_lse.data_ptr(),
-        *places[0], 0 if lse is None else lse.data_ptr(), words, workspace.data_ptr(), workspace.nbytes)
-    _check((_lib or load_library()).hisparse_attend_prefix(args, launch_stream), "hisparse_attend_prefix")
+        table.data_ptr(), block_size, prefix_len, scale, part_at, part_strides[0], part_strides[1], part_lse_at,
+        out.data_ptr(), out_strides[0], out_strides[1], lse_at, words, workspace.data_ptr(),
+        workspace.nbytes), launch_stream), "hisparse_attend_prefix")
 
 
 # -- measurement kernels (include/hisparse_measure.h) -----------------------
