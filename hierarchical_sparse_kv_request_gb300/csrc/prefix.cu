@@ -105,7 +105,7 @@ __host__ __device__ __forceinline__ int pair_of(const PrefixParts &w, int64_t un
 // 16-byte units of a head's 128 bytes swizzled.  Where values 4 n to 4 n + 3 of head i
 // of the pair's 128 are.
 constexpr int PART_IMAGE = 32 * 128;
-__device__ __forceinline__ int part_at(int i, int n)
+__host__ __device__ __forceinline__ int part_at(int i, int n)
 {
     const int warp = (i >> 6) * 4 + (n >> 6) * 2 + (i >> 5 & 1), h = i & 31;
     return (warp * 8 + (n >> 3 & 7)) * PART_IMAGE + h * 128 + (((n ^ h) & 7) << 4);

@@ -90,8 +90,8 @@ typedef struct hisparse_page_tables_args {
  *     requests that are left as they are, of entries that are negative, and at
  *     all places behind the last token.
  * Held entries have to be pages (or shared ones) and each page held or free once.
- * A call with other lengths followed by one with the old ones puts tables and
- * free list back as they were (unless a request went without).
+ * A call with other lengths followed by one with the old ones puts the tables and
+ * the list's free pages back as they were (unless a request went without).
  * Data errors, by status: BAD_SEQ_LEN (lens[r] beyond max_blocks pages), BAD_INDEX
  * (held[r] outside [0, max_blocks]): the request is left as it is; BAD_POSITION
  * (new_tokens[r] negative, which counts as 0, or above lens[r]: its tokens get
@@ -101,8 +101,9 @@ typedef struct hisparse_page_tables_args {
  * that the list has no room for are dropped.
  * One launch, or two with many tokens; capturable.  lens, new_tokens and shared
  * may not overlap what the call writes.
- * Errors: INVALID_ARG, UNSUPPORTED (R above HISPARSE_MAX_REQUESTS, max_blocks,
- * block_size above HISPARSE_RESIDENT_FLAG), CUDA.
+ * Errors: INVALID_ARG, UNSUPPORTED (R above HISPARSE_MAX_REQUESTS, max_blocks above
+ * its limit, R * max_blocks above 2^31 - 1, block_size above
+ * HISPARSE_RESIDENT_FLAG), CUDA.
  */
 int hisparse_page_tables(const hisparse_page_tables_args *args, void *stream);
 
@@ -192,12 +193,18 @@ typedef struct hisparse_attend_prefix_args {
  *   lse[r][h] = ln l
  * without the terms of `part` if that is NULL.  part and part_lse may be out and
  * lse themselves: hisparse_attend over a request's own rows, then this call on
- * its results.  If there is nothing at all, out = 0 and lse = -inf.
+ * its results (they may not overlap in any other way).  Where part_lse is -inf,
+ * part's values are not looked at.  If there is nothing at all, out = 0 and lse =
+ * -inf.
  * Products accumulate in 32 bits.  Latent values are used in `dtype`: exact but
  * as hisparse_gather_rows says.  Probabilities enter the second product in
  * `dtype`, relative to a running maximum; everything else of the softmax is
- * 32-bit; out is rounded once.  Results repeat bit for bit.
- * Several launches, capturable.  Errors: INVALID_ARG, UNSUPPORTED (R, H or
+ * 32-bit; out is rounded once.  Results repeat bit for bit.  A NaN scale gives NaN
+ * wherever a token is named.
+ * A bounded wait of the kernel's that runs out (not expected) leaves status
+ * ATTEND_TIMEOUT with every request; with status NULL neither that nor
+ * BAD_RESIDENT leaves a trace.
+ * One to three launches, capturable.  Errors: INVALID_ARG, UNSUPPORTED (R, H or
  * prefix_len beyond the limits), ALIGNMENT (q, rows, part, out or workspace not
  * 16-byte aligned), CAPACITY (workspace too small), CUDA.
  */

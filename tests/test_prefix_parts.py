@@ -1,0 +1,113 @@
+"""How attend_prefix cuts its work up, checked on the host: every tile of every group
+of heads belongs to one pair of CTAs, a pair has at most two parts of groups and each
+of them a place of its own in the workspace, the join finds those and no others, and
+every value of a part has a place inside it.  A place outside would be a write past the
+workspace on the GPU; this finds it without one.  The check compiles the kernel's source
+file into a host program (nvcc; no GPU needed)."""
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "hierarchical_sparse_kv_request_gb300", "csrc")
+
+PROGRAM = r"""
+#include "prefix.cu"
+#include <cstdio>
+#include <map>
+#include <vector>
+int main()
+{
+    using namespace hs;
+    long bad = 0, n = 0;
+    const int heads[] = {1, 64, 127, 128, 129, 512, 1480, 4096, 9728, 9729, 25600, 1 << 20};
+    for (int h : heads)
+        for (int len = 1; len <= 1 << 20; len = len < 700 ? len + 61 : len * 3) {
+            if ((int64_t)h * len > 40000000) continue;
+            int64_t bytes;
+            const PrefixParts w = lay_out(h > 1024 ? h / 1024 : 1, h > 1024 ? 1024 : h, len, nullptr, &bytes);
+            const int groups = ((h > 1024 ? h / 1024 * 1024 : h) + 127) / 128;
+            bad += w.tiles != (len + 127) / 128 || w.groups != groups || w.units != (int64_t)w.tiles * groups;
+            bad += w.pairs < 1 || w.pairs > MAX_PAIRS || first_unit(w, 0) != 0 || first_unit(w, w.pairs) != w.units;
+            // the workspace's pieces, one behind the other
+            const int64_t o = (int64_t)(uintptr_t)w.o, ml = (int64_t)(uintptr_t)w.ml, there = (int64_t)(uintptr_t)w.there,
+                          image = (int64_t)(uintptr_t)w.image;
+            bad += o < 0 || o % 16 || ml < o + (int64_t)w.pairs * 2 * 128 * 512 * 4 || ml % 8;
+            bad += there < ml + (int64_t)w.pairs * 2 * 128 * 8 || there % 16 || image < there + (int64_t)w.tiles * 16 || image % 16;
+            bad += bytes < image + (int64_t)w.tiles * TILE_BYTES;
+            std::map<int64_t, std::vector<int64_t>> parts;      // of a group: places
+            std::vector<int> used(w.pairs * 2, 0);
+            for (int p = 0; p < w.pairs; ++p) {
+                const int64_t u0 = first_unit(w, p), u1 = first_unit(w, p + 1);
+                bad += u1 <= u0;                            // no pair without work
+                for (int64_t u = u0; u < u1;) {             // as prefix_kernel goes through them
+                    const int64_t group = u / w.tiles, t0 = u - group * w.tiles;
+                    const int64_t t1 = t0 + (u1 - u) < w.tiles ? t0 + (u1 - u) : w.tiles;
+                    ++n;
+                    bad += pair_of(w, u) != p || pair_of(w, u + (t1 - t0) - 1) != p;
+                    u += t1 - t0;
+                    const bool whole = t0 == 0 && t1 == w.tiles;
+                    const int64_t place = (int64_t)p * 2 + (t0 == 0);
+                    if (!whole && used[place]++) ++bad;
+                    parts[group].push_back(whole ? -1 : place);
+                }
+            }
+            bad += (int64_t)parts.size() != w.groups;
+            for (auto &g : parts) {                         // as join_kernel does
+                const int64_t begin = g.first * w.tiles;
+                const int p0 = pair_of(w, begin), count = pair_of(w, begin + w.tiles - 1) - p0 + 1;
+                bad += count != (int)g.second.size() || (count == 1) != (g.second[0] < 0);
+                if (count == 1) continue;
+                for (int k = 0; k < count && k < (int)g.second.size(); ++k) {
+                    const int64_t first = (int64_t)p0 * 2 + (first_unit(w, p0) <= begin);
+                    bad += g.second[k] != (k == 0 ? first : (int64_t)(p0 + k) * 2);
+                }
+                bad += count > MAX_PAIRS;
+            }
+        }
+    // a part's values: heads by fours of values
+    std::vector<int> at(128 * 512 / 4, 0);
+    for (int i = 0; i < 128; ++i)
+        for (int v = 0; v < 128; ++v) {
+            const int x = part_at(i, v);
+            if (x % 16 || x < 0 || x / 16 >= (int)at.size() || at[x / 16]++) ++bad;
+            // as the softmax warps write them: warp (half of the values, heads' half), image of 32
+            // columns, lane, unit
+            const int rank = i / 64, lane = i % 32, warp = (v / 64) * 2 + i / 32 % 2, c = v / 8 % 8, unit = v % 8;
+            bad += x != ((rank * 4 + warp) * 8 + c) * PART_IMAGE + lane * 128 + ((unit ^ (lane & 7)) << 4);
+        }
+    // the blocks of a half tile: each once, the rope part last, X and Y of 128 values in turn
+    int seen = 0;
+    for (int k = 0; k < 9; ++k) seen |= 1 << block_at(k);
+    bad += seen != 511 || block_at(8) != 8;
+    for (int k = 0; k < 8; ++k) {
+        const int h = k / 4, y = k / 2 % 2;
+        bad += block_at(k) != y * 4 + h * 2 + k % 2;
+    }
+    for (int u = 0; u < 64; ++u)      // where expand_kernel puts unit u
+        bad += block_at((u % 32 / 16) * 4 + (u % 32 / 8 & 1) + (u >= 32 ? 2 : 0)) != u / 8;
+    bad += MISC_AT % 1024 != 0 || sizeof(PrefixSmem) + MISC_AT > 232448 || ROPE_AT != SLOTS * SLOT || SLOT != 4 * BLOCK;
+    bad += Q_SMEM * BLOCK < 8 * PART_IMAGE || P_AT + 4 * PART_IMAGE > MISC_AT || T_Q + Q_TMEM * 32 > 512 || T_S + 128 > T_Q;
+    std::printf("%ld parts, %ld wrong\n", n, bad);
+    return bad != 0;
+}
+"""
+
+
+def test_every_tile_and_part_has_one_place(tmp_path):
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    if not os.path.exists(nvcc):
+        pytest.skip("nvcc not found")
+    src = tmp_path / "parts_check.cu"
+    src.write_text(PROGRAM)
+    exe = tmp_path / "parts_check"
+    res = subprocess.run([nvcc, "-std=c++17", "-O1", "-gencode", "arch=compute_103a,code=sm_103a",
+                          "-I" + CSRC, "-I" + os.path.join(ROOT, "include"), str(src), "-o", str(exe)],
+                         capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+    run = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert run.returncode == 0, run.stdout + run.stderr
+    assert " 0 wrong" in run.stdout
