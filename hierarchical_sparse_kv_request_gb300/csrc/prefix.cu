@@ -38,7 +38,7 @@
 //   warp 4     brings keys in, warp 5 the values of the other CTA's keys;
 //   warp 6     of the first CTA issues the MMAs of S, up to two tiles ahead of warp 7,
 //              which issues those of O; those of the second say what has come in there.
-// The heads' tiles in a row are cut evenly among the pairs, wherever a head ends.
+// The groups' tiles in a row are shared out evenly among the pairs, wherever a group ends.
 #include <atomic>
 #include <mutex>
 
@@ -80,25 +80,42 @@ static_assert(PX_SMEM <= 232448, "shared memory of a CTA");
 // The latent block (of 64 values; 8: the rope part) at place n of a half tile.
 __host__ __device__ constexpr int block_at(int n) { return n == 8 ? 8 : (n >> 2) * 2 + (n >> 1 & 1) * 4 + (n & 1); }
 
-// How a call is cut up, and its workspace.
+// How a call is cut up, and its workspace.  Pair p has the tiles from start[p] to
+// start[p + 1], in the order of groups and tiles.
 struct PrefixParts {
     int tiles;               // of 128 keys
     int groups;              // of 128 heads
     int pairs;
-    int64_t units;           // tiles * groups; pair p takes units p * units / pairs to (p + 1) * units / pairs
+    struct Place {
+        int32_t group, tile;
+    } start[MAX_PAIRS + 1];
     uint8_t *image;          // [tiles][2] half tiles
     uint32_t *there;         // [tiles][4] a bit a key
-    uint8_t *o;              // [pairs][2] parts of O of 128 heads that a pair does not have whole (see part_at)
+    uint8_t *o;              // [pairs][2] parts of O of 128 heads that a pair does not have whole (see
+                             // part_at): of a group that it begins in the middle, of one from its start
     float2 *ml;              // [pairs][2][128] reference and sum
+    int2 *joins;             // [groups] of a group: see joined_pairs
 };
 
-__host__ __device__ __forceinline__ int64_t first_unit(const PrefixParts &w, int pair) { return w.units * pair / w.pairs; }
-
-// The pair that has a unit.
-__host__ __device__ __forceinline__ int pair_of(const PrefixParts &w, int64_t unit)
+// The pairs that have some of a group: the first, which has its first tile, and how many;
+// the others begin in the middle of it.
+__host__ __device__ __forceinline__ int2 joined_pairs(const PrefixParts &w, int group)
 {
-    int p = (int)(((unit + 1) * w.pairs - 1) / w.units);
-    return p;
+    // of the pairs that begin at (g, t) or before it, the last
+    auto last = [&](int g, int t) {
+        int lo = 0, hi = w.pairs - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            const PrefixParts::Place at = w.start[mid];
+            if (at.group < g || (at.group == g && at.tile <= t))
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        return lo;
+    };
+    const int p = last(group, 0);
+    return make_int2(p, last(group, w.tiles) - p + 1);
 }
 
 // A part of O: per CTA and warp of 32 heads by 256 values, 8 images of 32 values, the
@@ -127,6 +144,8 @@ __global__ void __launch_bounds__(EX_NT) expand_kernel(const __grid_constant__ P
     // prefix_kernel may be placed now: after this wait, as it reads its queries ahead of
     // its own
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // (for join_kernel, which has many threads to look that up)
+    for (int g = blockIdx.x * EX_NT + threadIdx.x; g < w.groups; g += gridDim.x * EX_NT) w.joins[g] = joined_pairs(w, g);
     const int t0 = blockIdx.x * EX_KEYS + warp * EX_ROWS;
     int64_t row = -1;
     if (lane < EX_ROWS && t0 + lane < a.len) {
@@ -278,8 +297,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
     const uint32_t base = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
-    const int64_t u0 = first_unit(w, pair), u1 = first_unit(w, pair + 1);
-    const int count = (int)(u1 - u0);      // tiles of this pair, over all its groups of heads
+    const PrefixParts::Place begin = w.start[pair], end = w.start[pair + 1];
+    // tiles of this pair, over all its groups of heads
+    const int count = (end.group - begin.group) * w.tiles + end.tile - begin.tile;
     auto bar = [](const uint64_t &b) { return smem_u32(&b); };
 
     if (warp == MMA_WARP) {
@@ -411,16 +431,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
             }
         };
         int n = 0;
-        int64_t u = u0;
-        for (bool begins = true; u < u1; begins = false) {
+        for (int group = begin.group, t0 = begin.tile; n < count; ++group, t0 = 0) {
             if (!(ok = meet_all(ok))) break;      // (P's place is free, too)
-            const int group = (int)(u / w.tiles), t0 = (int)(u - (int64_t)group * w.tiles);
-            const int t1 = (int)min((int64_t)w.tiles, t0 + (u1 - u));
-            u += t1 - t0;
+            const int t1 = group == end.group ? end.tile : w.tiles;
             const int head = group * PAIR_HEADS + rank * CTA_HEADS + i;
             const bool on = head < a.R * a.H;
             place_queries(group);
-            if (begins) after_launch_before();
+            if (group == begin.group) after_launch_before();
             float m = -INFINITY, l = 0.0f;
             const uint32_t *there = w.there + half * 2;
             uint2 next = *reinterpret_cast<const uint2 *>(there + (int64_t)t0 * 4);
@@ -573,7 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
         }
     } else if (warp == KEY_WARP) {
         // ---- this CTA's keys of every tile ------------------------------------------
-        int slot = 0, tile = (int)(u0 % w.tiles);
+        int slot = 0, tile = begin.tile;
         uint32_t slot_phase = 1;      // (nothing to wait for the first time round)
         for (int n = 0; ok && n < count; ++n) {
             const uint8_t *src = w.image + ((int64_t)tile * 2 + rank) * HALF_TILE;
@@ -591,7 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
         }
     } else if (warp == VALUE_WARP) {
         // ---- the other CTA's keys, for this one's values --------------------------------
-        int slot = 0, tile = (int)(u0 % w.tiles);
+        int slot = 0, tile = begin.tile;
         const uint32_t to = rank == 0 ? PART : 0;      // Y or X
         auto rope = [&](int tile) {
             if (elect_one()) {
@@ -643,7 +660,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
         // in short loops.  A thread's waits, and the fences behind them, take some hundred
         // cycles, in which the other's MMAs go on. -----------------------------------------
         auto wait = [&](const uint64_t &b, uint32_t phase) { return ok = ok && mbar_wait(bar(b), phase, gave_up); };
-        int slot = 0, tile = (int)(u0 % w.tiles);
+        int slot = 0, tile = begin.tile;
         bool begins = true;      // a group of heads
         if (warp == MMA_WARP) {
             constexpr uint32_t qk = mma_desc(128, KEYS, DT == kBf16, false);
@@ -746,16 +763,10 @@ __global__ void __launch_bounds__(JOIN_NT) join_kernel(const __grid_constant__ P
     const int tid = threadIdx.x, lane = tid & 31, head = blockIdx.x;
     const HeadPlace at(a, head);
     const int group = head / PAIR_HEADS, i = head % PAIR_HEADS;
-    const int64_t begin = (int64_t)group * w.tiles;
-    int p0 = 0, parts = 0;
-    if (w.units > 0) {
-        p0 = pair_of(w, begin);
-        parts = pair_of(w, begin + w.tiles - 1) - p0 + 1;
-        if (parts == 1) return;      // (that pair has written it)
-    }
-    // (a pair's second place is for the group that it begins with)
-    const int64_t first = (int64_t)p0 * 2 + (first_unit(w, p0) <= begin);
-    auto place = [&](int p) { return p == 0 ? first : (int64_t)(p0 + p) * 2; };
+    const int2 join = w.pairs > 0 ? w.joins[group] : make_int2(0, 0);
+    const int p0 = join.x, parts = join.y;
+    if (parts == 1) return;      // (that pair has written it)
+    auto place = [&](int p) { return (int64_t)(p0 + p) * 2 + (p == 0); };
     const uint8_t *src = w.o + part_at(i, tid);
     auto values = [&](int p) { return *reinterpret_cast<const float4 *>(src + place(p) * (PAIR_HEADS * kLatent * 4)); };
     float other = -INFINITY;
@@ -826,18 +837,63 @@ __global__ void __launch_bounds__(JOIN_NT) join_kernel(const __grid_constant__ P
 
 // ---- host ------------------------------------------------------------------------------
 
+// What a group of heads that a pair begins costs it beside its tiles (queries, O out; 10
+// to 13 thousand cycles), and a tile (2,650), in eighths of a tile.  Measured with 0, 16,
+// 29 and 40: 37 x 40 heads over 5,003 rows 34.9, 29.8, 30.0 and 29.7 us, 32 x 128 over
+// 8,192 69.5, 66.2, 66.4 and 64.7, 256 x 16 over 40,000 232.5, 230.1, 229.4 and 226.8.
+constexpr int GROUP_COST = 40, TILE_COST = 8;
+
+// Cuts the tiles so that no pair costs more than `most` (but one tile a pair at
+// least); whether MAX_PAIRS are enough.
+bool cut(PrefixParts &w, int64_t most)
+{
+    int group = 0, tile = 0;
+    for (w.pairs = 0; group < w.groups; ++w.pairs) {
+        if (w.pairs == MAX_PAIRS) return false;
+        w.start[w.pairs] = {group, tile};
+        int64_t left = most;
+        for (bool first = true; group < w.groups; first = false) {
+            int64_t n = (left - GROUP_COST) / TILE_COST;
+            if (n < 1) {
+                if (!first) break;
+                n = 1;
+            }
+            if (n < w.tiles - tile) {
+                tile += (int)n;
+                break;
+            }
+            left -= GROUP_COST + (int64_t)(w.tiles - tile) * TILE_COST;
+            ++group;
+            tile = 0;
+        }
+    }
+    w.start[w.pairs] = {group, 0};
+    return true;
+}
+
+// Cuts the tiles evenly: nearly the least cost a pair for which there are enough pairs.
+void cut_evenly(PrefixParts &w)
+{
+    const int64_t all = (int64_t)w.tiles * w.groups * TILE_COST;
+    // every pair begins a group, and every group is begun
+    int64_t most = (all + (int64_t)GROUP_COST * (w.groups > MAX_PAIRS ? w.groups : MAX_PAIRS)) / MAX_PAIRS;
+    most = most > GROUP_COST + TILE_COST ? most : GROUP_COST + TILE_COST;
+    while (!cut(w, most)) most += TILE_COST / 2 + most / 32;
+}
+
 PrefixParts lay_out(int32_t R, int32_t H, int32_t len, uint8_t *ws, int64_t *bytes)
 {
-    PrefixParts w = {};
+    PrefixParts w;
     w.tiles = (len + KEYS - 1) / KEYS;
     w.groups = (int)(((int64_t)R * H + PAIR_HEADS - 1) / PAIR_HEADS);
-    w.units = (int64_t)w.tiles * w.groups;
-    w.pairs = (int)(w.units < MAX_PAIRS ? w.units : MAX_PAIRS);
+    w.pairs = (int)((int64_t)w.tiles * w.groups < MAX_PAIRS ? (int64_t)w.tiles * w.groups : MAX_PAIRS);      // at most
     int64_t n = 16;      // never empty
     w.o = ws + n;
     n += (int64_t)w.pairs * 2 * PAIR_HEADS * kLatent * 4;
     w.ml = reinterpret_cast<float2 *>(ws + n);
     n += (int64_t)w.pairs * 2 * PAIR_HEADS * 8;
+    w.joins = reinterpret_cast<int2 *>(ws + n);
+    n += ((int64_t)w.groups + 1) / 2 * 16;
     w.there = reinterpret_cast<uint32_t *>(ws + n);
     n += (int64_t)w.tiles * 16;
     n = (n + 127) / 128 * 128;
@@ -868,14 +924,14 @@ cudaError_t prepare_device()
 template <int DT>
 cudaError_t launch(const PrefixLaunch &a, const PrefixParts &w, cudaStream_t s)
 {
-    if (w.units > 0) {
+    if (w.pairs > 0) {
         auto expand = a.row_bytes == kRow4 ? expand_kernel<DT, kRow4> : a.row_bytes == kRow8 ? expand_kernel<DT, kRow8> : expand_kernel<DT, kRow16>;
         cudaError_t e = launch_behind(expand, dim3(w.tiles * (KEYS / EX_KEYS)), EX_NT, 0, 1, s, a, w);
         if (e != cudaSuccess) return e;
         e = launch_behind(prefix_kernel<DT>, dim3(w.pairs * 2), PX_NT, PX_SMEM, 2, s, a, w);
         if (e != cudaSuccess) return e;
         bool split = false;
-        for (int p = 1; p < w.pairs; ++p) split = split || first_unit(w, p) % w.tiles != 0;
+        for (int p = 1; p < w.pairs; ++p) split = split || w.start[p].tile != 0;
         if (!split) return e;
     }
     return launch_behind(join_kernel<DT>, dim3(a.R * a.H), JOIN_NT, 0, 1, s, a, w);
@@ -890,7 +946,8 @@ cudaError_t launch_attend_prefix(const PrefixLaunch &a, cudaStream_t s)
     const cudaError_t e = prepare_device();
     if (e != cudaSuccess) return e;
     int64_t bytes;
-    const PrefixParts w = lay_out(a.R, a.H, a.len, a.workspace, &bytes);
+    PrefixParts w = lay_out(a.R, a.H, a.len, a.workspace, &bytes);
+    if (w.pairs > 0) cut_evenly(w);
     return a.dtype == kBf16 ? launch<kBf16>(a, w, s) : launch<kF16>(a, w, s);
 }
 

@@ -17,7 +17,6 @@ CSRC = os.path.join(ROOT, "hierarchical_sparse_kv_request_gb300", "csrc")
 PROGRAM = r"""
 #include "prefix.cu"
 #include <cstdio>
-#include <map>
 #include <vector>
 int main()
 {
@@ -28,44 +27,52 @@ int main()
         for (int len = 1; len <= 1 << 20; len = len < 700 ? len + 61 : len * 3) {
             if ((int64_t)h * len > 40000000) continue;
             int64_t bytes;
-            const PrefixParts w = lay_out(h > 1024 ? h / 1024 : 1, h > 1024 ? 1024 : h, len, nullptr, &bytes);
-            const int groups = ((h > 1024 ? h / 1024 * 1024 : h) + 127) / 128;
-            bad += w.tiles != (len + 127) / 128 || w.groups != groups || w.units != (int64_t)w.tiles * groups;
-            bad += w.pairs < 1 || w.pairs > MAX_PAIRS || first_unit(w, 0) != 0 || first_unit(w, w.pairs) != w.units;
+            PrefixParts w = lay_out(h > 1024 ? h / 1024 : 1, h > 1024 ? 1024 : h, len, nullptr, &bytes);
+            const int groups = ((h > 1024 ? h / 1024 * 1024 : h) + 127) / 128, most = w.pairs;
+            bad += w.tiles != (len + 127) / 128 || w.groups != groups;
+            bad += most < 1 || most > MAX_PAIRS;
             // the workspace's pieces, one behind the other
             const int64_t o = (int64_t)(uintptr_t)w.o, ml = (int64_t)(uintptr_t)w.ml, there = (int64_t)(uintptr_t)w.there,
                           image = (int64_t)(uintptr_t)w.image;
-            bad += o < 0 || o % 16 || ml < o + (int64_t)w.pairs * 2 * 128 * 512 * 4 || ml % 8;
-            bad += there < ml + (int64_t)w.pairs * 2 * 128 * 8 || there % 16 || image < there + (int64_t)w.tiles * 16 || image % 16;
+            bad += o < 0 || o % 16 || ml < o + (int64_t)most * 2 * 128 * 512 * 4 || ml % 8;
+            const int64_t joins = (int64_t)(uintptr_t)w.joins;
+            bad += joins < ml + (int64_t)most * 2 * 128 * 8 || joins % 8;
+            bad += there < joins + (int64_t)groups * 8 || there % 16 || image < there + (int64_t)w.tiles * 16 || image % 16;
             bad += bytes < image + (int64_t)w.tiles * TILE_BYTES;
-            std::map<int64_t, std::vector<int64_t>> parts;      // of a group: places
-            std::vector<int> used(w.pairs * 2, 0);
+            cut_evenly(w);
+            bad += w.pairs < 1 || w.pairs > most;
+            bad += w.start[0].group != 0 || w.start[0].tile != 0 || w.start[w.pairs].group != groups || w.start[w.pairs].tile != 0;
+            std::vector<std::vector<int64_t>> parts(groups);    // of a group: places
+            std::vector<int> used(most * 2, 0);
+            int64_t all = 0;
             for (int p = 0; p < w.pairs; ++p) {
-                const int64_t u0 = first_unit(w, p), u1 = first_unit(w, p + 1);
-                bad += u1 <= u0;                            // no pair without work
-                for (int64_t u = u0; u < u1;) {             // as prefix_kernel goes through them
-                    const int64_t group = u / w.tiles, t0 = u - group * w.tiles;
-                    const int64_t t1 = t0 + (u1 - u) < w.tiles ? t0 + (u1 - u) : w.tiles;
+                const auto begin = w.start[p], end = w.start[p + 1];
+                bad += begin.group >= groups || begin.tile >= w.tiles || begin.tile < 0;
+                const int64_t count = (int64_t)(end.group - begin.group) * w.tiles + end.tile - begin.tile;
+                bad += count < 1 || count > INT32_MAX;      // no pair without work
+                all += count;
+                int64_t n1 = 0;
+                int group = begin.group, t0 = begin.tile;
+                for (; n1 < count; ++group, t0 = 0) {        // as prefix_kernel goes through them
+                    const int t1 = group == end.group ? end.tile : w.tiles;
                     ++n;
-                    bad += pair_of(w, u) != p || pair_of(w, u + (t1 - t0) - 1) != p;
-                    u += t1 - t0;
+                    n1 += t1 - t0;
+                    bad += t1 <= t0 || group >= groups;
                     const bool whole = t0 == 0 && t1 == w.tiles;
                     const int64_t place = (int64_t)p * 2 + (t0 == 0);
                     if (!whole && used[place]++) ++bad;
                     parts[group].push_back(whole ? -1 : place);
                 }
+                bad += n1 != count;
             }
-            bad += (int64_t)parts.size() != w.groups;
-            for (auto &g : parts) {                         // as join_kernel does
-                const int64_t begin = g.first * w.tiles;
-                const int p0 = pair_of(w, begin), count = pair_of(w, begin + w.tiles - 1) - p0 + 1;
-                bad += count != (int)g.second.size() || (count == 1) != (g.second[0] < 0);
+            bad += all != (int64_t)w.tiles * groups;
+            for (int g = 0; g < groups; ++g) {                  // as join_kernel does
+                const int2 join = joined_pairs(w, g);
+                const int p0 = join.x, count = join.y;
+                bad += count != (int)parts[g].size() || (count == 1) != (parts[g][0] < 0) || count > MAX_PAIRS;
                 if (count == 1) continue;
-                for (int k = 0; k < count && k < (int)g.second.size(); ++k) {
-                    const int64_t first = (int64_t)p0 * 2 + (first_unit(w, p0) <= begin);
-                    bad += g.second[k] != (k == 0 ? first : (int64_t)(p0 + k) * 2);
-                }
-                bad += count > MAX_PAIRS;
+                for (int k = 0; k < count && k < (int)parts[g].size(); ++k)
+                    bad += parts[g][k] != (int64_t)(p0 + k) * 2 + (k == 0);
             }
         }
     // a part's values: heads by fours of values
