@@ -1,22 +1,27 @@
 // rows.cu -- KV rows normalised and stored by slot, and read back
 // (include/hisparse_pages.h, hisparse_norm_rows, hisparse_gather_rows).
 //
-// The mathematics.  y = x w / sqrt(mean x^2 + eps): the product x w of two
-// 16-bit values is exact in 32 bits, so y has one rounding of its own and those
-// of the one factor 1 / sqrt.  Then per group of 128 values a power of two and
-// e4m3 codes, per group of 16 an e4m3 scale and e2m1 codes, or y in 16 bits.
+// The mathematics.  y = x w / sqrt(mean x^2 + eps): the product t = x w of two 16-bit
+// values is exact in 32 bits, so y = t f has one rounding of its own and those of the one
+// factor f = 1 / sqrt, and the largest |y| of a group is that of t, times f.  Then per
+// group of 128 values a power of two s and e4m3 codes of t (f / s), per group of 16 an
+// e4m3 scale and e2m1 codes, or y in 16 bits.
 //
-// Bound by HBM: 1,152 bytes of values and 416 to 1,152 of row, each moved once;
-// nothing is kept between rows.  A warp works on a whole row: a lane holds 8
-// neighbouring values of each half of the latent part, so every load and store of
-// the warp is contiguous (512 bytes of values, 256 of e4m3 codes), a group of 16
-// is two neighbouring lanes, one of 128 half a warp.
+// Bound by HBM: 1,152 bytes of values and 416 to 1,152 of row, each moved once; nothing
+// is kept between rows.  (With y worked out before the groups' largest, and a division
+// and a root in f, the instructions of 4-bit rows took longer than their bytes: 28 us for
+// 70,001 rows.)  A warp works on a whole row: a lane holds 8 neighbouring values of each
+// half of the latent part, so every load and store of the warp is contiguous (512 bytes
+// of values, 256 of e4m3 codes), a group of 16 is two neighbouring lanes, one of 128 half
+// a warp.  262,144 rows of 656 bytes there and back, at slots in no order: 157 us, 0.89
+// of the copy rate.
 #include "pages.cuh"
 
 namespace hs {
 namespace {
 
-constexpr int ROWS_NT = 128, ROWS_CTAS = 14;     // threads a CTA, CTAs an SM
+constexpr int ROWS_NT = 128;                     // threads a CTA
+constexpr int NORM_CTAS = 14, GATHER_CTAS = 16;  // CTAs an SM (norm: 12 164 us, 14 and 16 157)
 constexpr int ROWS_A_CTA = ROWS_NT / 32;
 
 template <int DT>
@@ -37,21 +42,23 @@ __device__ __forceinline__ uint4 pack16(const float (&x)[8])
     return make_uint4(floats_to_pair<DT>(x[0], x[1]), floats_to_pair<DT>(x[2], x[3]), floats_to_pair<DT>(x[4], x[5]), floats_to_pair<DT>(x[6], x[7]));
 }
 
-// Largest magnitude of the 8 values of `lanes` neighbouring lanes; NaN if one is
-// (as integers, a NaN's magnitude is the largest).
+// Largest magnitude of the 8 values of LANES neighbouring lanes; NaN if one is.
 template <int LANES>
-__device__ __forceinline__ uint32_t top_bits(const float (&y)[8])
+__device__ __forceinline__ float largest(const float (&t)[8])
 {
-    uint32_t m = 0;
+    auto max_nan = [](float x, float y) {
+        float z;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(fabsf(x)), "f"(fabsf(y)));
+        return z;
+    };
+    float m = max_nan(max_nan(max_nan(t[0], t[1]), max_nan(t[2], t[3])), max_nan(max_nan(t[4], t[5]), max_nan(t[6], t[7])));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(y[j]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int d = 1; d < LANES; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    for (int d = 1; d < LANES; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
     return m;
 }
 
-// The exponent k of the least power of two with m <= 448 2^k = 1.75 2^(k + 8),
-// from the bits of m; -126 at least.
+// The exponent k of the least power of two with m <= 448 2^k = 1.75 2^(k + 8), from the
+// bits of m; -126 at least.
 __device__ __forceinline__ int scale_exponent(uint32_t m)
 {
     return max((int)(m >> 23) - 127 - 8 + ((m & 0x7FFFFFu) > 0x600000u), -126);
@@ -67,37 +74,49 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// 8 values to a row: those from 256 half + 8 lane on.
-__device__ __forceinline__ void store8(uint8_t *dst, const float (&y)[8], int half, int lane)
+// Values t f, those from 256 half + 8 lane on, to a row.
+__device__ __forceinline__ void store8(uint8_t *dst, const float (&t)[8], float f, int half, int lane)
 {
-    const uint32_t m = top_bits<16>(y);
+    const float top = largest<16>(t) * f;
+    const uint32_t m = __float_as_uint(top);
     // infinities have the exponent of 2^128: 2^120, and their codes clip to 448
     const int k = scale_exponent(min(m, 0x7F800000u));
-    const float inv = power_of_two(-k);
-    const bool nan = m > 0x7F800000u;
+    float by = f * power_of_two(-k), u[8];      // (exact: a power of two)
+    const bool far = !(by <= FLT_MAX);          // a group of zeros, or next to it
+    if (far) by = power_of_two(-k);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = t[j];
+    if (far) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] *= f;
+    }
     *reinterpret_cast<uint2 *>(dst + half * 256 + lane * 8) =
-        make_uint2(e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                   e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+        make_uint2(e4m3x4(u[0] * by, u[1] * by, u[2] * by, u[3] * by), e4m3x4(u[4] * by, u[5] * by, u[6] * by, u[7] * by));
     if ((lane & 15) == 0)
-        *reinterpret_cast<float *>(dst + kRow8ScaleAt + (half * 2 + (lane >> 4)) * 4) = nan ? __uint_as_float(0x7FC00000u) : power_of_two(k);
+        *reinterpret_cast<float *>(dst + kRow8ScaleAt + (half * 2 + (lane >> 4)) * 4) = top != top ? top : power_of_two(k);
 }
 
-// normed: y is any 32-bit number, and y * (1 / scale) as good as the quotient;
-// else it has a 16-bit type's value, and may lie on a border between two codes:
-// then the product's rounding is taken out (see rows4.cu), which would move
-// numbers next to a border onto it.
-__device__ __forceinline__ void store4(uint8_t *dst, const float (&y)[8], int half, int lane, bool normed)
+// NORM: t f is any 32-bit number, and t (f / scale) as good as the quotient; else f is 1
+// and t has a 16-bit type's value, and may lie on a border between two codes: then the
+// product's rounding is taken out (see rows4.cu), which would move numbers next to a
+// border onto it.
+template <bool NORM>
+__device__ __forceinline__ void store4(uint8_t *dst, const float (&t)[8], float f, int half, int lane)
 {
-    const float top = __uint_as_float(top_bits<2>(y));
+    const float top = largest<2>(t) * f;
     uint16_t e8;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e8) : "f"(0.0f), "f"(__fdiv_rn(top, 6.0f)));
     const float scale = __low2float(scale_half2(e8 & 0xFFu));
-    const float inv = scale == 0.0f ? 0.0f : __frcp_rn(scale);
+    const float inv = scale == 0.0f ? 0.0f : __frcp_rn(scale), by = f * inv;
     float q[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float t = normed ? y[j] * inv : __fadd_rn(__fmaf_rn(y[j], inv, 48.0f), -48.0f);
-        q[j] = __uint_as_float((__float_as_uint(t) & 0x7FFFFFFFu) | (__float_as_uint(y[j]) & 0x80000000u));
+        if (NORM) {
+            q[j] = t[j] * by;
+        } else {
+            const float x = __fadd_rn(__fmaf_rn(t[j], inv, 48.0f), -48.0f);
+            q[j] = __uint_as_float((__float_as_uint(x) & 0x7FFFFFFFu) | (__float_as_uint(t[j]) & 0x80000000u));
+        }
     }
     uint32_t out;
     asm("{\n"
@@ -114,6 +133,14 @@ __device__ __forceinline__ void store4(uint8_t *dst, const float (&y)[8], int ha
     if (!(lane & 1)) dst[kScaleAt + half * 16 + (lane >> 1)] = (uint8_t)e8;
 }
 
+// 1 / sqrt(v), by one step of Newton's method from the approximate root, off by about
+// 2^-23; 0 for infinity.
+__device__ __forceinline__ float inverse_root(float v)
+{
+    const float r = rsqrtf(v), e = fmaf(-v * r, r, 1.0f);
+    return v <= FLT_MAX ? fmaf(0.5f * r, e, r) : r;
+}
+
 // The row that value i goes to or comes from; -1: none.
 __device__ __forceinline__ int64_t row_of_value(const RowsLaunch &a, int64_t i)
 {
@@ -121,54 +148,57 @@ __device__ __forceinline__ int64_t row_of_value(const RowsLaunch &a, int64_t i)
     return s < a.num_rows ? s : -1;
 }
 
-template <int DT, int ROW>
-__global__ void __launch_bounds__(ROWS_NT, ROWS_CTAS) norm_kernel(const __grid_constant__ RowsLaunch a)
+template <int DT, int ROW, bool NORM>
+__global__ void __launch_bounds__(ROWS_NT, NORM_CTAS) norm_kernel(const __grid_constant__ RowsLaunch a)
 {
     after_launch_before();
     const int lane = threadIdx.x & 31;
     const int64_t i = (int64_t)blockIdx.x * ROWS_A_CTA + (threadIdx.x >> 5);
     if (i >= a.n) return;      // the same for the whole warp
-    const int64_t row = row_of_value(a, i);
-    if (row < 0) return;
     const uint8_t *src = a.values + i * a.value_stride;
-    uint8_t *dst = a.rows + row * a.row_stride;
+    // (ahead of the slot, which would be one more wait)
     const uint4 v[2] = {ld_dev_v4(src + lane * 16), ld_dev_v4(src + 512 + lane * 16)};
     uint4 rope;
     if (lane < 8) rope = ld_dev_v4(src + kLatent * 2 + lane * 16);
-    float y[2][8];
-    unpack16<DT>(v[0], y[0]);
-    unpack16<DT>(v[1], y[1]);
-    if (a.weight) {
+    const int64_t row = row_of_value(a, i);
+    if (row < 0) return;
+    uint8_t *dst = a.rows + row * a.row_stride;
+    float t[2][8], f = 1.0f;
+    unpack16<DT>(v[0], t[0]);
+    unpack16<DT>(v[1], t[1]);
+    if (NORM) {
         float sum = 0.0f;
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(y[half][j], y[half][j], sum);
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const float f = __frcp_rn(__fsqrt_rn(fmaf(sum, 1.0f / kLatent, a.eps)));
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             float w[8];
             unpack16<DT>(ld_dev_v4(a.weight + half * 512 + lane * 16), w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[half][j] = y[half][j] * w[j] * f;
+            for (int j = 0; j < 8; ++j) {
+                sum = fmaf(t[half][j], t[half][j], sum);
+                t[half][j] *= w[j];
+            }
         }
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        f = inverse_root(fmaf(sum, 1.0f / kLatent, a.eps));
     }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        if (ROW == kRow16)
-            st_v4(dst + half * 512 + lane * 16, pack16<DT>(y[half]));
-        else if (ROW == kRow8)
-            store8(dst, y[half], half, lane);
-        else
-            store4(dst, y[half], half, lane, a.weight != nullptr);
+        if (ROW == kRow16) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[half][j] *= f;
+            st_v4(dst + half * 512 + lane * 16, pack16<DT>(t[half]));
+        } else if (ROW == kRow8) {
+            store8(dst, t[half], f, half, lane);
+        } else {
+            store4<NORM>(dst, t[half], f, half, lane);
+        }
     }
     if (lane < 8) st_v4(dst + rope_at(ROW) + lane * 16, rope);
 }
 
 template <int DT, int ROW>
-__global__ void __launch_bounds__(ROWS_NT, ROWS_CTAS) gather_kernel(const __grid_constant__ RowsLaunch a)
+__global__ void __launch_bounds__(ROWS_NT, GATHER_CTAS) gather_kernel(const __grid_constant__ RowsLaunch a)
 {
     after_launch_before();
     const int lane = threadIdx.x & 31;
@@ -196,12 +226,18 @@ cudaError_t launch(Kernel kernel, const RowsLaunch &a, cudaStream_t s)
 
 }  // namespace
 
+template <int DT, int ROW>
+static cudaError_t launch_norm(const RowsLaunch &a, cudaStream_t s)
+{
+    return a.weight ? launch(norm_kernel<DT, ROW, true>, a, s) : launch(norm_kernel<DT, ROW, false>, a, s);
+}
+
 cudaError_t launch_norm_rows(const RowsLaunch &a, cudaStream_t s)
 {
     const bool b = a.dtype == kBf16;
-    if (a.row_bytes == kRow4) return b ? launch(norm_kernel<kBf16, kRow4>, a, s) : launch(norm_kernel<kF16, kRow4>, a, s);
-    if (a.row_bytes == kRow8) return b ? launch(norm_kernel<kBf16, kRow8>, a, s) : launch(norm_kernel<kF16, kRow8>, a, s);
-    return b ? launch(norm_kernel<kBf16, kRow16>, a, s) : launch(norm_kernel<kF16, kRow16>, a, s);
+    if (a.row_bytes == kRow4) return b ? launch_norm<kBf16, kRow4>(a, s) : launch_norm<kF16, kRow4>(a, s);
+    if (a.row_bytes == kRow8) return b ? launch_norm<kBf16, kRow8>(a, s) : launch_norm<kF16, kRow8>(a, s);
+    return b ? launch_norm<kBf16, kRow16>(a, s) : launch_norm<kF16, kRow16>(a, s);
 }
 
 cudaError_t launch_gather_rows(const RowsLaunch &a, cudaStream_t s)
