@@ -59,7 +59,8 @@ int hisparse_page_tables(const hisparse_page_tables_args *p, void *stream)
     if (a.num_requests > 1 && a.tables_stride < a.max_blocks) return HISPARSE_ERR_INVALID_ARG;
     if (a.new_tokens && (a.num_tokens < 0 || !a.offsets || (a.num_tokens > 0 && !a.slots))) return HISPARSE_ERR_INVALID_ARG;
     if (a.num_requests > HISPARSE_MAX_REQUESTS || a.max_blocks > HISPARSE_MAX_TABLE_BLOCKS ||
-        a.block_size > HISPARSE_RESIDENT_FLAG || (int64_t)a.num_requests * a.max_blocks > INT32_MAX)
+        a.block_size > HISPARSE_RESIDENT_FLAG || (a.new_tokens && a.num_tokens > HISPARSE_RESIDENT_FLAG) ||
+        (int64_t)a.num_requests * a.max_blocks > INT32_MAX)
         return HISPARSE_ERR_UNSUPPORTED;
     hs::TablesLaunch l;
     l.R = a.num_requests;

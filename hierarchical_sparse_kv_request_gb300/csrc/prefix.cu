@@ -38,7 +38,23 @@
 //   warp 4     brings keys in, warp 5 the values of the other CTA's keys;
 //   warp 6     of the first CTA issues the MMAs of S, up to two tiles ahead of warp 7,
 //              which issues those of O; those of the second say what has come in there.
-// The groups' tiles in a row are shared out evenly among the pairs, wherever a group ends.
+// The groups' tiles in a row are shared out among the pairs, wherever a group ends, so that
+// each has as much to do, its groups' starts and ends counted.
+//
+// What bounds it.  With much to do, shared memory: a tile of 128 keys moves some 330 KB
+// through each SM's (operands of S 112, of O 96, keys and values coming in 106, P 16) in
+// 2,650 cycles, 125 of its 128 bytes a cycle, where the products alone take 2,184.  Without
+// the copies a tile takes 2,330.  With little, a pair's start (1 thousand cycles, queries
+// 4) and end (5 to 7 for O, at some 25 bytes a cycle that an SM stores) and the launches
+// around it.  Measured on GB300, GPU time of a call: 256 requests of 16 heads over 40,000
+// rows 227 us (1,572 TFLOP/s, 0.82 of cuBLAS's best); 32 of 128 heads over 8,192 64; 32 of
+// 16 over 8,192 29; 37 of 40 over 5,003 29; 4 of 16 over 2,048 13.
+// Rounding.  Latent values of 4-bit rows, and of 8-bit rows with powers of two as scales,
+// are exact in both types, and so are queries.  P is rounded to the model's type (half a
+// step: 2^-8 of a probability in bf16), which the product's two operands share; out's error
+// against 64 bits is 1.6 to 2.0 x 10^-3 in bf16 (the plain 32-bit form's: 1.6) and 2.4 x
+// 10^-4 in f16 (2.1).  Scores, references, sums and O are 32-bit, and sums add up a tile at
+// a time.
 #include <atomic>
 #include <mutex>
 
@@ -86,6 +102,7 @@ struct PrefixParts {
     int tiles;               // of 128 keys
     int groups;              // of 128 heads
     int pairs;
+    bool split;              // join_kernel follows
     struct Place {
         int32_t group, tile;
     } start[MAX_PAIRS + 1];
@@ -144,8 +161,6 @@ __global__ void __launch_bounds__(EX_NT) expand_kernel(const __grid_constant__ P
     // prefix_kernel may be placed now: after this wait, as it reads its queries ahead of
     // its own
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // (for join_kernel, which has many threads to look that up)
-    for (int g = blockIdx.x * EX_NT + threadIdx.x; g < w.groups; g += gridDim.x * EX_NT) w.joins[g] = joined_pairs(w, g);
     const int t0 = blockIdx.x * EX_KEYS + warp * EX_ROWS;
     int64_t row = -1;
     if (lane < EX_ROWS && t0 + lane < a.len) {
@@ -181,7 +196,12 @@ __global__ void __launch_bounds__(EX_NT) expand_kernel(const __grid_constant__ P
         st_v4(half + (place + 2) * BLOCK + i * 128 + u, v[j][1]);
         if (lane < 8) st_v4(half + 8 * BLOCK + i * 128 + u, rope[j]);
     }
-    if (lane == 0) atomicOr(&there, named << (warp * EX_ROWS));
+    if (lane == 0) {
+        atomicOr(&there, named << (warp * EX_ROWS));
+        // For join_kernel, where each head's threads would have to look.  (A group a warp:
+        // the threads of one would read 32 places of `start` one behind the other.)
+        for (int g = blockIdx.x * (EX_NT / 32) + warp; g < w.groups; g += gridDim.x * (EX_NT / 32)) w.joins[g] = joined_pairs(w, g);
+    }
     __syncthreads();
     if (threadIdx.x == 0) w.there[blockIdx.x] = there;
     if (bad && a.status)
@@ -335,7 +355,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
     cluster_wait();      // the other CTA's mbarriers are there, and its tensor memory
     // (the softmax warps read the queries ahead of this wait: see expand_kernel)
     if (warp >= SOFTMAX) after_launch_before();
-    if (warp == MMA_WARP) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");      // (join_kernel waits itself)
+    // join_kernel may be placed now, as it waits before it does anything.  (Not so the
+    // caller's next launch, where no join follows: see hisparse_set_programmatic_launch.)
+    if (w.split && warp == MMA_WARP) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp < SOFTMAX) {
         // ---- softmax: a thread has head (warp % 2) 32 + lane of the CTA's, and half of
@@ -431,8 +453,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
             }
         };
         int n = 0;
-        for (int group = begin.group, t0 = begin.tile; n < count; ++group, t0 = 0) {
-            if (!(ok = meet_all(ok))) break;      // (P's place is free, too)
+        const int last_group = end.tile > 0 ? end.group : end.group - 1;
+        for (int group = begin.group, t0 = begin.tile; group <= last_group; ++group, t0 = 0) {
+            // (all four warps come here as often, whatever has gone wrong; P's place is free)
+            if (!(ok = meet_all(ok))) break;
             const int t1 = group == end.group ? end.tile : w.tiles;
             const int head = group * PAIR_HEADS + rank * CTA_HEADS + i;
             const bool on = head < a.R * a.H;
@@ -868,6 +892,8 @@ bool cut(PrefixParts &w, int64_t most)
         }
     }
     w.start[w.pairs] = {group, 0};
+    w.split = false;
+    for (int p = 1; p < w.pairs; ++p) w.split = w.split || w.start[p].tile != 0;
     return true;
 }
 
@@ -930,9 +956,7 @@ cudaError_t launch(const PrefixLaunch &a, const PrefixParts &w, cudaStream_t s)
         if (e != cudaSuccess) return e;
         e = launch_behind(prefix_kernel<DT>, dim3(w.pairs * 2), PX_NT, PX_SMEM, 2, s, a, w);
         if (e != cudaSuccess) return e;
-        bool split = false;
-        for (int p = 1; p < w.pairs; ++p) split = split || w.start[p].tile != 0;
-        if (!split) return e;
+        if (!w.split) return e;
     }
     return launch_behind(join_kernel<DT>, dim3(a.R * a.H), JOIN_NT, 0, 1, s, a, w);
 }

@@ -9,10 +9,17 @@
 // g_r <= count'.  So no page waits for another request's; only what is given back
 // has to be there before anything is taken, and the tables before the slots.
 //
-// One cluster of CTAs.  Each works out the sums over all requests for itself (in
-// shared memory, a thread having up to 8 requests), then the warps of the cluster
-// share the requests, a lane an entry, with a cluster barrier between giving back,
+// One CTA, or one cluster of them.  Each works out the sums over all requests for itself
+// (in shared memory, a thread having up to 8 requests), then the warps share the pages
+// that come back or go, whichever request's they are, with a barrier between giving back,
 // taking and mapping.
+//
+// Bound by latency: a call's chain is lengths, sums, entries given back, list, entries
+// taken and read again for the slots, some 0.4 us each, and the barriers (a cluster's 0.7
+// us).  Measured on GB300, GPU time of two calls, one there and one back: 32 requests, up
+// to 4 drafted tokens each 6.6 us; 256 requests, 38 of them admitted and 38 finished (some
+// 27 thousand pages each way, places for 1.0 M tokens) 24; 128 requests of 2,048 to 81,920
+// tokens admitted and finished (43 thousand pages, 2.8 M slots) 22.
 #include <climits>
 
 #include "pages.cuh"
@@ -20,17 +27,21 @@
 namespace hs {
 namespace {
 
-constexpr int MAP_NT = 256, MAP_TOKENS = 2048;      // the mapping launch: tokens a CTA
+constexpr int MAP_NT = 256, MAP_TOKENS = 1024;      // the mapping launch: tokens a CTA (256
+                                                    // requests, mixed: 24 us, 31 with 4,096)
 
-// n / d for 0 <= n < 2^31, 1 <= d < 2^31, as a product and a shift.
+// n / d for 0 <= n < 2^31, 1 <= d <= 2^30, as a product and a shift; and the last page
+// whose rows end below the flag bit.
 struct Divider {
     uint32_t mul, shift, d;
+    int32_t last_page;
     explicit Divider(int32_t by)
     {
         d = (uint32_t)by;
         shift = 0;
         while ((1ull << shift) < d) ++shift;
         mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+        last_page = kResidentFlag / by - 1;
     }
     __device__ __forceinline__ int32_t over(int32_t n) const { return (int32_t)((__umulhi(mul, (uint32_t)n) + (uint32_t)n) >> shift); }
 };
@@ -51,14 +62,15 @@ __device__ __forceinline__ int32_t first_position(const TablesLaunch &a, int32_t
     return len >= 0 && n <= len && held >= 0 && held <= a.W && (int64_t)held * a.bs >= len ? len - max(n, 0) : LEFT;
 }
 
-// The slot and position of token p of request r (p below 0: none), to place i.
-__device__ __forceinline__ void map_token(const TablesLaunch &a, const Divider &by, int r, int32_t p, int32_t i)
+// The slot and position of token p of request r (p below 0: none), whose table is row,
+// to place i.
+__device__ __forceinline__ void map_token(const TablesLaunch &a, const Divider &by, int r, const int32_t *row, int32_t p, int32_t i)
 {
     int32_t slot = -1, pos = -1;
     if (p >= 0) {
-        const int32_t b = by.over(p), page = a.tables[(int64_t)r * a.tables_stride + b];
-        if (page >= 0 && ((int64_t)page + 1) * a.bs <= kResidentFlag) {
-            slot = page * a.bs + (p - b * a.bs);
+        const int32_t b = by.over(p), page = row[b];
+        if ((uint32_t)page <= (uint32_t)by.last_page) {
+            slot = p + (page - b) * (int32_t)by.d;
             pos = p;
         } else if (page >= 0 && a.status) {
             record_status(a.status, r, kStatusBadResident);
@@ -149,7 +161,7 @@ __device__ __forceinline__ void move_pages(const int32_t *first, int requests, i
 {
     constexpr int AT_ONCE = 8;
     const int lane = threadIdx.x & 31;
-    const int32_t a_warp = min((end + warps * 32 - 1) / (warps * 32), AT_ONCE) * 32;
+    const int32_t a_warp = (int32_t)min(((int64_t)end + warps * 32 - 1) / (warps * 32), (int64_t)AT_ONCE) * 32;
     for (int64_t j0 = (int64_t)warp * a_warp; j0 < end; j0 += (int64_t)warps * a_warp) {
         const int32_t last = (int32_t)min(j0 + a_warp, (int64_t)end) - 1;
         int lo = 0, hi = requests - 1;
@@ -200,7 +212,10 @@ __global__ void __launch_bounds__(NT, 1) tables_kernel(const __grid_constant__ T
     const int rank = blockIdx.x;
     if (tid == 0) taken = 0;
     after_launch_before();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");      // (map_kernel waits itself)
+    // map_kernel may be placed now, as it waits before it does anything.  (Not so the
+    // caller's next launch, where none follows: a swap-in may read its resident tables
+    // ahead of its wait, see hisparse_set_programmatic_launch.)
+    if (!MAP && a.new_tokens) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- sums over the requests -------------------------------------------------
     const int per = (a.R + NT - 1) / NT, r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
@@ -315,7 +330,7 @@ __global__ void __launch_bounds__(NT, 1) tables_kernel(const __grid_constant__ T
         for (int32_t i = rank * NT + tid; i < a.tokens; i += CTAS * NT) {
             const int r = i < end ? find_request(q.first, 0, a.R - 1, i) : 0;
             const int32_t start = i < end ? q.start[r] : LEFT;
-            map_token(a, by, r, start == LEFT ? -1 : start + (i - q.first[r]), i);
+            map_token(a, by, r, a.tables + (int64_t)r * a.tables_stride, start == LEFT ? -1 : start + (i - q.first[r]), i);
         }
     }
 }
@@ -355,17 +370,18 @@ __global__ void __launch_bounds__(MAP_NT) map_kernel(const __grid_constant__ Tab
     };
     if (lo == hi && begin < end) {      // one request (or none behind the last token)
         const int32_t start = look(lo);
+        const int32_t *row = a.tables + (int64_t)lo * a.tables_stride;
 #pragma unroll
         for (int k = 0; k < MAP_TOKENS / MAP_NT; ++k) {
             const int32_t i = begin + k * MAP_NT + threadIdx.x;
-            if (i <= last) map_token(a, by, lo, i < end && start != LEFT ? start + i : -1, i);
+            if (i <= last) map_token(a, by, lo, row, i < end && start != LEFT ? start + i : -1, i);
         }
     } else {
 #pragma unroll 4
         for (int32_t i = begin + threadIdx.x; i <= last; i += MAP_NT) {
             const int r = i < end ? find_request(a.offsets, lo, hi, i) : 0;
             const int32_t start = i < end ? look(r) : LEFT;
-            map_token(a, by, r, start == LEFT ? -1 : start + i, i);
+            map_token(a, by, r, a.tables + (int64_t)r * a.tables_stride, start == LEFT ? -1 : start + i, i);
         }
     }
 }

@@ -102,7 +102,7 @@ typedef struct hisparse_page_tables_args {
  * One launch, or two with many tokens; capturable.  lens, new_tokens and shared
  * may not overlap what the call writes.
  * Errors: INVALID_ARG, UNSUPPORTED (R above HISPARSE_MAX_REQUESTS, max_blocks above
- * its limit, R * max_blocks above 2^31 - 1, block_size above
+ * its limit, R * max_blocks above 2^31 - 1, block_size or num_tokens above
  * HISPARSE_RESIDENT_FLAG), CUDA.
  */
 int hisparse_page_tables(const hisparse_page_tables_args *args, void *stream);

@@ -133,3 +133,41 @@ def test_a_decode_loop_behind_a_shared_prefix(captured):
             assert (np.abs(got - want) <= tol).all(), (s, r, np.abs(got - want).max())
             assert (np.abs(lse[r].double().cpu().numpy() - w_lse) <= ds + 2000 * U32).all()
     hs.close()
+
+
+@pytest.mark.parametrize("new_tokens", [False, True])
+def test_tables_changed_between_programmatic_swap_ins(new_tokens):
+    """A swap-in that reads ahead of its wait, its handle's last launch having been on
+    another layer: the resident tables that page_tables has written in between are those
+    it finds."""
+    R, k, D, bs, blocks, cap = 64, 64, 128, 16, 60, 1024
+    rng = np.random.default_rng(5)
+    hs = H.HiSparse(R, 2, H.ROW4_BYTES, k, D, host_to_device_ratio=8, host_capacity=[cap] * R)
+    hs.set_programmatic_launch(True)
+    lens = torch.full((R,), 800, dtype=torch.int32, device="cuda")
+    hs.prefill(lens)
+    tables = torch.full((R, blocks), -1, dtype=torch.int32, device="cuda")
+    held = torch.zeros(R, dtype=torch.int32, device="cuda")
+    pages = torch.from_numpy(rng.permutation(R * blocks).astype(np.int32)).cuda()
+    count = torch.tensor([R * blocks], dtype=torch.int32, device="cuda")
+    topk = torch.from_numpy(np.stack([rng.permutation(800)[:k] for _ in range(R)]).astype(np.int32)).cuda()
+    outs = [torch.empty((R, k), dtype=torch.int32, device="cuda") for _ in range(40)]
+    covered = [torch.full((R,), int(n), dtype=torch.int32, device="cuda") for n in rng.integers(1, 800, 40)]
+    new = torch.ones(R, dtype=torch.int32, device="cuda")
+    more = dict(new_tokens=new, offsets=torch.empty(R + 1, dtype=torch.int32, device="cuda"),
+                slots=torch.empty(1 << 15, dtype=torch.int32, device="cuda")) if new_tokens else {}
+    seen = []
+    for n in range(40):
+        H.page_tables(covered[n], tables, held, pages, count, bs, **more)
+        seen.append(tables.clone() if n % 2 else None)      # (half of them with no other kernel in between)
+        hs.swap_in_resident(n & 1, topk, lens, tables, bs, outs[n])
+    torch.cuda.synchronize()
+    assert (hs.status() == 0).all()
+    t = topk.cpu().numpy()
+    for n in range(40):
+        ids, resident = outs[n].cpu().numpy(), t < -(-int(covered[n][0]) // bs) * bs
+        assert np.array_equal((ids & H.RESIDENT_FLAG) != 0, resident), n
+        if seen[n] is not None:
+            page = np.take_along_axis(seen[n].cpu().numpy(), t // bs, 1)
+            assert np.array_equal(ids[resident], (H.RESIDENT_FLAG | (page * bs + t % bs))[resident])
+    hs.close()

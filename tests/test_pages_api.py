@@ -58,6 +58,7 @@ WITH_TOKENS = dict(new_tokens=A, offsets=A, slots=A, positions=A, num_tokens=10)
     (dict(max_blocks=(1 << 20) + 1, tables_stride=1 << 21), H.ERR_UNSUPPORTED),
     (dict(num_requests=4096, max_blocks=1 << 20, tables_stride=1 << 20), H.ERR_UNSUPPORTED),
     (dict(block_size=(1 << 30) + 1), H.ERR_UNSUPPORTED),
+    (dict(WITH_TOKENS, num_tokens=(1 << 30) + 1), H.ERR_UNSUPPORTED),
 ])
 def test_page_tables_refuses(lib, change, code):
     a = tables_args(**change)

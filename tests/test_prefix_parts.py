@@ -53,7 +53,8 @@ int main()
                 all += count;
                 int64_t n1 = 0;
                 int group = begin.group, t0 = begin.tile;
-                for (; n1 < count; ++group, t0 = 0) {        // as prefix_kernel goes through them
+                const int last_group = end.tile > 0 ? end.group : end.group - 1;
+                for (; group <= last_group; ++group, t0 = 0) {        // as prefix_kernel goes through them
                     const int t1 = group == end.group ? end.tile : w.tiles;
                     ++n;
                     n1 += t1 - t0;
@@ -66,6 +67,9 @@ int main()
                 bad += n1 != count;
             }
             bad += all != (int64_t)w.tiles * groups;
+            bool split = false;
+            for (auto &g : parts) split = split || g.size() > 1;
+            bad += split != w.split;
             for (int g = 0; g < groups; ++g) {                  // as join_kernel does
                 const int2 join = joined_pairs(w, g);
                 const int p0 = join.x, count = join.y;
