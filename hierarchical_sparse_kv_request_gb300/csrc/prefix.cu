@@ -47,8 +47,8 @@
 // the copies a tile takes 2,330.  With little, a pair's start (1 thousand cycles, queries
 // 4) and end (5 to 7 for O, at some 25 bytes a cycle that an SM stores) and the launches
 // around it.  Measured on GB300, GPU time of a call: 256 requests of 16 heads over 40,000
-// rows 227 us (1,572 TFLOP/s, 0.82 of cuBLAS's best); 32 of 128 heads over 8,192 64; 32 of
-// 16 over 8,192 29; 37 of 40 over 5,003 29; 4 of 16 over 2,048 13.
+// rows 225 us (1,582 TFLOP/s, 0.82 of cuBLAS's best); 32 of 128 heads over 8,192 63; 32 of
+// 16 over 8,192 25; 37 of 40 over 5,003 30; 4 of 16 over 2,048 12.
 // Rounding.  Latent values of 4-bit rows, and of 8-bit rows with powers of two as scales,
 // are exact in both types, and so are queries.  P is rounded to the model's type (half a
 // step: 2^-8 of a probability in bf16), which the product's two operands share; out's error
@@ -102,38 +102,22 @@ struct PrefixParts {
     int tiles;               // of 128 keys
     int groups;              // of 128 heads
     int pairs;
-    bool split;              // join_kernel follows
+    int joins;               // groups that several pairs have some of
     struct Place {
         int32_t group, tile;
     } start[MAX_PAIRS + 1];
+    // pair `first` has the group's first tile, the parts - 1 that follow begin in the middle
+    // of it
+    struct Join {
+        int32_t group;
+        int16_t first, parts;
+    } join[MAX_PAIRS];
     uint8_t *image;          // [tiles][2] half tiles
     uint32_t *there;         // [tiles][4] a bit a key
     uint8_t *o;              // [pairs][2] parts of O of 128 heads that a pair does not have whole (see
                              // part_at): of a group that it begins in the middle, of one from its start
     float2 *ml;              // [pairs][2][128] reference and sum
-    int2 *joins;             // [groups] of a group: see joined_pairs
 };
-
-// The pairs that have some of a group: the first, which has its first tile, and how many;
-// the others begin in the middle of it.
-__host__ __device__ __forceinline__ int2 joined_pairs(const PrefixParts &w, int group)
-{
-    // of the pairs that begin at (g, t) or before it, the last
-    auto last = [&](int g, int t) {
-        int lo = 0, hi = w.pairs - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            const PrefixParts::Place at = w.start[mid];
-            if (at.group < g || (at.group == g && at.tile <= t))
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        return lo;
-    };
-    const int p = last(group, 0);
-    return make_int2(p, last(group, w.tiles) - p + 1);
-}
 
 // A part of O: per CTA and warp of 32 heads by 256 values, 8 images of 32 values, the
 // 16-byte units of a head's 128 bytes swizzled.  Where values 4 n to 4 n + 3 of head i
@@ -196,12 +180,7 @@ __global__ void __launch_bounds__(EX_NT) expand_kernel(const __grid_constant__ P
         st_v4(half + (place + 2) * BLOCK + i * 128 + u, v[j][1]);
         if (lane < 8) st_v4(half + 8 * BLOCK + i * 128 + u, rope[j]);
     }
-    if (lane == 0) {
-        atomicOr(&there, named << (warp * EX_ROWS));
-        // For join_kernel, where each head's threads would have to look.  (A group a warp:
-        // the threads of one would read 32 places of `start` one behind the other.)
-        for (int g = blockIdx.x * (EX_NT / 32) + warp; g < w.groups; g += gridDim.x * (EX_NT / 32)) w.joins[g] = joined_pairs(w, g);
-    }
+    if (lane == 0) atomicOr(&there, named << (warp * EX_ROWS));
     __syncthreads();
     if (threadIdx.x == 0) w.there[blockIdx.x] = there;
     if (bad && a.status)
@@ -357,7 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
     if (warp >= SOFTMAX) after_launch_before();
     // join_kernel may be placed now, as it waits before it does anything.  (Not so the
     // caller's next launch, where no join follows: see hisparse_set_programmatic_launch.)
-    if (w.split && warp == MMA_WARP) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (w.joins > 0 && warp == MMA_WARP) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp < SOFTMAX) {
         // ---- softmax: a thread has head (warp % 2) 32 + lane of the CTA's, and half of
@@ -775,88 +754,113 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
 // ---- join ------------------------------------------------------------------------------
 
 constexpr int JOIN_NT = 128;
+constexpr int JOIN_WIDE = 1024;      // heads that get four warps each
 
-// A CTA a head, four values a thread: its parts from the pairs that have some of its
-// tiles.  Bound by latency with few heads: so the parts' factors come first, and their
-// values, eight at a time, wait for nothing but their loads.
-template <int DT>
+// The parts of the heads of split groups, WARPS warps a head, a lane 16 / WARPS of its
+// values; or, where there is no prefix (pairs 0), the heads' own parts alone.  Bound by
+// latency: references and sums, and the values of the first parts, are loaded at once,
+// and the values wait for nothing else.
+template <int DT, int WARPS>
 __global__ void __launch_bounds__(JOIN_NT) join_kernel(const __grid_constant__ PrefixLaunch a, const __grid_constant__ PrefixParts w)
 {
-    __shared__ float factors[MAX_PAIRS];
+    constexpr int FOURS = 4 / WARPS, AT_ONCE = 16 / FOURS;      // of a lane's values; parts
+    constexpr int LANES = (MAX_PAIRS + 31) / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n = WARPS == 4 ? blockIdx.x : blockIdx.x * 4 + warp, four = WARPS == 4 ? threadIdx.x : lane;
+    PrefixParts::Join join = {n / PAIR_HEADS, 0, 0};
+    if (w.pairs > 0) join = w.join[n / PAIR_HEADS];
+    const int i = n % PAIR_HEADS, head = join.group * PAIR_HEADS + i;
+    const bool on = head < a.R * a.H;
+    const HeadPlace at(a, on ? head : 0);
+    // (a pair's second place is for the group that it has from its start)
+    auto place = [&](int p) { return (int64_t)(join.first + p) * 2 + (p == 0); };
+    auto values = [&](int p, int k) {
+        return *reinterpret_cast<const float4 *>(w.o + place(p) * (PAIR_HEADS * kLatent * 4) + part_at(i, four + 32 * k));
+    };
+    uint8_t *out = a.out + at.r * a.out_rs + at.h * a.out_hs + four * 8;
+    const uint8_t *own = a.part + at.r * a.part_rs + at.h * a.part_hs + four * 8;
     after_launch_before();
-    const int tid = threadIdx.x, lane = tid & 31, head = blockIdx.x;
-    const HeadPlace at(a, head);
-    const int group = head / PAIR_HEADS, i = head % PAIR_HEADS;
-    const int2 join = w.pairs > 0 ? w.joins[group] : make_int2(0, 0);
-    const int p0 = join.x, parts = join.y;
-    if (parts == 1) return;      // (that pair has written it)
-    auto place = [&](int p) { return (int64_t)(p0 + p) * 2 + (p == 0); };
-    const uint8_t *src = w.o + part_at(i, tid);
-    auto values = [&](int p) { return *reinterpret_cast<const float4 *>(src + place(p) * (PAIR_HEADS * kLatent * 4)); };
-    float other = -INFINITY;
-    uint2 part = make_uint2(0, 0);
+    if (!on) return;      // (all of the head's warps)
+    float4 v[AT_ONCE][FOURS];
+#pragma unroll
+    for (int p = 0; p < AT_ONCE; ++p)
+#pragma unroll
+        for (int k = 0; k < FOURS; ++k)
+            if (p < join.parts) v[p][k] = values(p, k);
+    float2 ml[LANES];
+    float m = -INFINITY, l = 0.0f, f[LANES], other = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < LANES; ++k) {
+        const int p = k * 32 + lane;
+        ml[k] = p < join.parts ? w.ml[place(p) * PAIR_HEADS + i] : make_float2(-INFINITY, 0.0f);
+    }
+    uint2 part[FOURS];
     if (a.part) {
         other = a.part_lse[head];
-        part = *reinterpret_cast<const uint2 *>(a.part + at.r * a.part_rs + at.h * a.part_hs + tid * 8);
-    }
-    float4 v[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (k < parts) v[k] = values(k);
-    // every warp for itself: reference and sum of all parts
-    float2 ml[(MAX_PAIRS + 31) / 32];
-    float m = -INFINITY, l = 0.0f;
-#pragma unroll
-    for (int k = 0; k < (MAX_PAIRS + 31) / 32; ++k) {
-        const int p = k * 32 + lane;
-        ml[k] = p < parts ? w.ml[place(p) * PAIR_HEADS + i] : make_float2(-INFINITY, 0.0f);
-        m = fmaxf(m, ml[k].x);
+        for (int k = 0; k < FOURS; ++k) part[k] = *reinterpret_cast<const uint2 *>(own + k * 256);
     }
+#pragma unroll
+    for (int k = 0; k < LANES; ++k) m = fmaxf(m, ml[k].x);
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
 #pragma unroll
-    for (int k = 0; k < (MAX_PAIRS + 31) / 32; ++k) {
-        const float f = ex2(ml[k].x - (m == -INFINITY ? 0.0f : m));
-        if (k * 32 + lane < parts && tid < 32) factors[k * 32 + lane] = f;
-        if (k * 32 + lane < parts) l = fmaf(f, ml[k].y, l);
+    for (int k = 0; k < LANES; ++k) {
+        f[k] = ex2(ml[k].x - (m == -INFINITY ? 0.0f : m));
+        if (k * 32 + lane < join.parts) l = fmaf(f[k], ml[k].y, l);
     }
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
-    __syncthreads();      // (also: part may be out, part_lse lse)
-    float o[4] = {};
-    for (int p = 0; p < parts; p += 8) {
-        if (p > 0) {
+    float o[FOURS][4] = {};
+#pragma unroll 1
+    for (int p0 = 0; p0 < join.parts; p0 += AT_ONCE) {
+        if (p0 > 0) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (p + k < parts) v[k] = values(p + k);
+            for (int p = 0; p < AT_ONCE; ++p)
+#pragma unroll
+                for (int k = 0; k < FOURS; ++k)
+                    if (p0 + p < join.parts) v[p][k] = values(p0 + p, k);
         }
+        // (AT_ONCE divides 32: the factors of a round are in one of f)
+        const float fs = p0 < 32 ? f[0] : p0 < 64 ? f[1] : f[2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (p + k < parts) {
-                const float f = factors[p + k];
-                o[0] = fmaf(f, v[k].x, o[0]);
-                o[1] = fmaf(f, v[k].y, o[1]);
-                o[2] = fmaf(f, v[k].z, o[2]);
-                o[3] = fmaf(f, v[k].w, o[3]);
+        for (int p = 0; p < AT_ONCE; ++p) {
+            const float by = __shfl_sync(0xffffffffu, fs, (p0 + p) & 31);
+            if (p0 + p < join.parts) {
+#pragma unroll
+                for (int k = 0; k < FOURS; ++k) {
+                    o[k][0] = fmaf(by, v[p][k].x, o[k][0]);
+                    o[k][1] = fmaf(by, v[p][k].y, o[k][1]);
+                    o[k][2] = fmaf(by, v[p][k].z, o[k][2]);
+                    o[k][3] = fmaf(by, v[p][k].w, o[k][3]);
+                }
             }
+        }
     }
     float weight = 0.0f, scale = 1.0f;
     if (a.part) scale = add_part(m, l, other, &weight);
     const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
     scale *= inv;
+    const float by = weight * inv;
+    // (part may be out, whose values are this lane's own; part_lse lse)
+    if (WARPS > 1)
+        __syncthreads();
+    else
+        __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] *= scale;
-    if (weight != 0.0f) {
-        weight *= inv;
-        const float2 x = pair_to_float<DT>(part.x), y = pair_to_float<DT>(part.y);
-        o[0] = fmaf(x.x, weight, o[0]);
-        o[1] = fmaf(x.y, weight, o[1]);
-        o[2] = fmaf(y.x, weight, o[2]);
-        o[3] = fmaf(y.y, weight, o[3]);
+    for (int k = 0; k < FOURS; ++k) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[k][j] *= scale;
+        if (weight != 0.0f) {
+            const float2 x = pair_to_float<DT>(part[k].x), y = pair_to_float<DT>(part[k].y);
+            o[k][0] = fmaf(x.x, by, o[k][0]);
+            o[k][1] = fmaf(x.y, by, o[k][1]);
+            o[k][2] = fmaf(y.x, by, o[k][2]);
+            o[k][3] = fmaf(y.y, by, o[k][3]);
+        }
+        *reinterpret_cast<uint2 *>(out + k * 256) = make_uint2(floats_to_pair<DT>(o[k][0], o[k][1]), floats_to_pair<DT>(o[k][2], o[k][3]));
     }
-    *reinterpret_cast<uint2 *>(a.out + at.r * a.out_rs + at.h * a.out_hs + tid * 8) =
-        make_uint2(floats_to_pair<DT>(o[0], o[1]), floats_to_pair<DT>(o[2], o[3]));
-    if (tid == 0 && a.lse) a.lse[head] = log2_sum(m, l) * kLn2;
+    if (four == 0 && a.lse) a.lse[head] = log2_sum(m, l) * kLn2;
 }
 
 // ---- host ------------------------------------------------------------------------------
@@ -892,8 +896,14 @@ bool cut(PrefixParts &w, int64_t most)
         }
     }
     w.start[w.pairs] = {group, 0};
-    w.split = false;
-    for (int p = 1; p < w.pairs; ++p) w.split = w.split || w.start[p].tile != 0;
+    w.joins = 0;
+    for (int p = 1; p < w.pairs; ++p) {
+        if (w.start[p].tile == 0) continue;
+        if (w.joins > 0 && w.join[w.joins - 1].group == w.start[p].group)
+            ++w.join[w.joins - 1].parts;
+        else
+            w.join[w.joins++] = {w.start[p].group, (int16_t)(p - 1), 2};
+    }
     return true;
 }
 
@@ -918,8 +928,6 @@ PrefixParts lay_out(int32_t R, int32_t H, int32_t len, uint8_t *ws, int64_t *byt
     n += (int64_t)w.pairs * 2 * PAIR_HEADS * kLatent * 4;
     w.ml = reinterpret_cast<float2 *>(ws + n);
     n += (int64_t)w.pairs * 2 * PAIR_HEADS * 8;
-    w.joins = reinterpret_cast<int2 *>(ws + n);
-    n += ((int64_t)w.groups + 1) / 2 * 16;
     w.there = reinterpret_cast<uint32_t *>(ws + n);
     n += (int64_t)w.tiles * 16;
     n = (n + 127) / 128 * 128;
@@ -956,9 +964,14 @@ cudaError_t launch(const PrefixLaunch &a, const PrefixParts &w, cudaStream_t s)
         if (e != cudaSuccess) return e;
         e = launch_behind(prefix_kernel<DT>, dim3(w.pairs * 2), PX_NT, PX_SMEM, 2, s, a, w);
         if (e != cudaSuccess) return e;
-        if (!w.split) return e;
+        if (w.joins == 0) return e;
     }
-    return launch_behind(join_kernel<DT>, dim3(a.R * a.H), JOIN_NT, 0, 1, s, a, w);
+    // Four warps a head where there are few, with many parts each (32 x 16 heads over 8,192
+    // rows: 25.0 us, with one 31.8), else one (32 x 128 heads, 2 or 3 parts each: 63.1 us,
+    // with four 66.8).
+    const int heads = (w.pairs > 0 ? w.joins : w.groups) * PAIR_HEADS;
+    if (heads <= JOIN_WIDE) return launch_behind(join_kernel<DT, 4>, dim3(heads), JOIN_NT, 0, 1, s, a, w);
+    return launch_behind(join_kernel<DT, 1>, dim3(heads / 4), JOIN_NT, 0, 1, s, a, w);
 }
 
 }  // namespace

@@ -35,9 +35,7 @@ int main()
             const int64_t o = (int64_t)(uintptr_t)w.o, ml = (int64_t)(uintptr_t)w.ml, there = (int64_t)(uintptr_t)w.there,
                           image = (int64_t)(uintptr_t)w.image;
             bad += o < 0 || o % 16 || ml < o + (int64_t)most * 2 * 128 * 512 * 4 || ml % 8;
-            const int64_t joins = (int64_t)(uintptr_t)w.joins;
-            bad += joins < ml + (int64_t)most * 2 * 128 * 8 || joins % 8;
-            bad += there < joins + (int64_t)groups * 8 || there % 16 || image < there + (int64_t)w.tiles * 16 || image % 16;
+            bad += there < ml + (int64_t)most * 2 * 128 * 8 || there % 16 || image < there + (int64_t)w.tiles * 16 || image % 16;
             bad += bytes < image + (int64_t)w.tiles * TILE_BYTES;
             cut_evenly(w);
             bad += w.pairs < 1 || w.pairs > most;
@@ -67,17 +65,19 @@ int main()
                 bad += n1 != count;
             }
             bad += all != (int64_t)w.tiles * groups;
-            bool split = false;
-            for (auto &g : parts) split = split || g.size() > 1;
-            bad += split != w.split;
+            int joins = 0;
             for (int g = 0; g < groups; ++g) {                  // as join_kernel does
-                const int2 join = joined_pairs(w, g);
-                const int p0 = join.x, count = join.y;
-                bad += count != (int)parts[g].size() || (count == 1) != (parts[g][0] < 0) || count > MAX_PAIRS;
-                if (count == 1) continue;
-                for (int k = 0; k < count && k < (int)parts[g].size(); ++k)
-                    bad += parts[g][k] != (int64_t)(p0 + k) * 2 + (k == 0);
+                bad += (parts[g].size() == 1) != (parts[g][0] < 0);
+                if (parts[g].size() == 1) continue;
+                if (joins >= w.joins || joins >= MAX_PAIRS) {
+                    ++bad;
+                    break;
+                }
+                const auto join = w.join[joins++];
+                bad += join.group != g || join.parts != (int)parts[g].size();
+                for (int k = 0; k < (int)parts[g].size(); ++k) bad += parts[g][k] != (int64_t)(join.first + k) * 2 + (k == 0);
             }
+            bad += joins != w.joins;
         }
     // a part's values: heads by fours of values
     std::vector<int> at(128 * 512 / 4, 0);
