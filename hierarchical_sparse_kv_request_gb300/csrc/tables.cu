@@ -10,7 +10,7 @@
 // has to be there before anything is taken, and the tables before the slots.
 //
 // One CTA, or one cluster of them.  Each works out the sums over all requests for itself
-// (in shared memory, a thread having up to 8 requests), then the warps share the pages
+// (in shared memory, a thread having up to 16 requests), then the warps share the pages
 // that come back or go, whichever request's they are, with a barrier between giving back,
 // taking and mapping.
 //
@@ -18,8 +18,9 @@
 // taken and read again for the slots, some 0.4 us each, and the barriers (a cluster's 0.7
 // us).  Measured on GB300, GPU time of two calls, one there and one back: 32 requests, up
 // to 4 drafted tokens each 6.6 us; 256 requests, 38 of them admitted and 38 finished (some
-// 27 thousand pages each way, places for 1.0 M tokens) 24; 128 requests of 2,048 to 81,920
-// tokens admitted and finished (43 thousand pages, 2.8 M slots) 22.
+// 27 thousand pages each way, places for 1.0 M tokens) 22; 128 requests of 2,048 to 81,920
+// tokens admitted and finished (43 thousand pages, 2.8 M slots) 21.
+#include <atomic>
 #include <climits>
 
 #include "pages.cuh"
@@ -27,8 +28,10 @@
 namespace hs {
 namespace {
 
+constexpr int kMostRequests = 8192;                 // HISPARSE_MAX_REQUESTS
 constexpr int MAP_NT = 256, MAP_TOKENS = 1024;      // the mapping launch: tokens a CTA (256
-                                                    // requests, mixed: 24 us, 31 with 4,096)
+                                                    // requests, mixed: 22 us; with a cluster of
+                                                    // eight 24, 31 with 4,096)
 
 // n / d for 0 <= n < 2^31, 1 <= d <= 2^30, as a product and a shift; and the last page
 // whose rows end below the flag bit.
@@ -388,30 +391,46 @@ __global__ void __launch_bounds__(MAP_NT) map_kernel(const __grid_constant__ Tab
 
 }  // namespace
 
+// Sets a kernel's attributes on the current device, once.
+template <int CTAS, int NT, bool MAP>
+static cudaError_t prepare_tables()
+{
+    constexpr int kDevices = 64;
+    static std::atomic<bool> known[kDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= kDevices) return cudaErrorInvalidDevice;
+    if (known[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    auto kernel = tables_kernel<CTAS, NT, MAP>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)requests_bytes(kMostRequests, MAP));
+    if (e == cudaSuccess && CTAS > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) known[dev].store(true, std::memory_order_release);
+    return e;
+}
+
 template <int CTAS, int NT, bool MAP>
 static cudaError_t launch_tables(const TablesLaunch &a, const Divider &by, cudaStream_t s)
 {
-    const size_t smem = requests_bytes(a.R, MAP);
-    if (smem > 40000) {
-        const cudaError_t e = cudaFuncSetAttribute(tables_kernel<CTAS, NT, MAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_behind(tables_kernel<CTAS, NT, MAP>, dim3(CTAS), NT, smem, CTAS, s, a, by);
+    const cudaError_t e = prepare_tables<CTAS, NT, MAP>();
+    if (e != cudaSuccess) return e;
+    return launch_behind(tables_kernel<CTAS, NT, MAP>, dim3(CTAS), NT, requests_bytes(a.R, MAP), CTAS, s, a, by);
 }
 
 cudaError_t launch_page_tables(const TablesLaunch &a, cudaStream_t s)
 {
     const Divider by(a.bs);
-    // Few slots in the same launch (1.0 M in one: 69 us for 256 requests, 25 in two).
+    // Few slots in the same launch (1.0 M in one: 69 us for 256 requests with a
+    // cluster of eight, 25 in two).
     const bool map = a.new_tokens && a.tokens <= 16384;
-    // One CTA for what a decode step moves (32 requests, 4 drafts each: 7.0 us for a call
-    // there and one back, 8.5 with a cluster), a cluster of eight where whole prompts come
-    // and go (128 requests of 2,048 to 81,920 tokens: 22.6 us, 90 with one CTA).  What a call
-    // moves is known on the device alone: a step has few tokens, and where none are
-    // placed, few requests.
+    // One CTA for what a decode step moves (32 requests, 4 drafts each: 6.6 us for a call
+    // there and one back, 8.5 with a cluster of eight), a cluster of sixteen where whole
+    // prompts come and go (128 requests of 2,048 to 81,920 tokens: 20.8 us, 23.2 with eight
+    // of 1,024 threads, 90 with one CTA).  What a call moves is known on the device alone: a
+    // step has few tokens, and where none are placed, few requests.
     const bool step = a.new_tokens ? a.R <= 256 && a.tokens <= 4096 : a.R <= 32;
     const cudaError_t e = step ? map ? launch_tables<1, 256, true>(a, by, s) : launch_tables<1, 256, false>(a, by, s)
-                               : map ? launch_tables<8, 1024, true>(a, by, s) : launch_tables<8, 1024, false>(a, by, s);
+                               : map ? launch_tables<16, 512, true>(a, by, s) : launch_tables<16, 512, false>(a, by, s);
     if (e != cudaSuccess || !a.new_tokens || map || a.tokens == 0) return e;
     return launch_behind(map_kernel, dim3((a.tokens + MAP_TOKENS - 1) / MAP_TOKENS), MAP_NT, 0, 1, s, a, by);
 }
