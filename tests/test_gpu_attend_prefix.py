@@ -139,9 +139,9 @@ def test_pages_and_holes(bs, holes):
 
 def test_nothing_to_attend_to():
     """No tokens, and only holes: the part alone; without one, zeros."""
-    for n, holes in ((0, 0.0), (300, 1.0)):
+    for heads, n, holes in ((33, 0, 0.0), (33, 300, 1.0), (400, 0, 0.0), (400, 1000, 1.0)):
         for part in (True, False):
-            q, rows, table, out, lse, p, pl = call(4, 33, n, seed=n, holes=holes, part=part)
+            q, rows, table, out, lse, p, pl = call(4, heads, n, seed=n, holes=holes, part=part)
             if part:
                 keep = [0, 1, 3]                # (request 2's part has no weight)
                 assert torch.equal(out[keep], p[keep])
