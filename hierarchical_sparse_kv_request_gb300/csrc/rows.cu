@@ -8,20 +8,22 @@
 // e4m3 scale and e2m1 codes, or y in 16 bits.
 //
 // Bound by HBM: 1,152 bytes of values and 416 to 1,152 of row, each moved once; nothing
-// is kept between rows.  (With y worked out before the groups' largest, and a division
-// and a root in f, the instructions of 4-bit rows took longer than their bytes: 28 us for
-// 70,001 rows.)  A warp works on a whole row: a lane holds 8 neighbouring values of each
-// half of the latent part, so every load and store of the warp is contiguous (512 bytes
-// of values, 256 of e4m3 codes), a group of 16 is two neighbouring lanes, one of 128 half
-// a warp.  262,144 rows of 656 bytes there and back, at slots in no order: 157 us, 0.89
-// of the copy rate.
+// is kept between rows; and, next to it, by instructions (of 4-bit rows 256 a row and
+// warp took 23 us for 70,001 rows, 16 for their bytes).  A warp works on a whole row.  For
+// codes a lane has 16 neighbouring values: a group of 16 is a lane's own, one of 128 eight
+// lanes', its scale worked out once a lane, and the codes' stores are contiguous (8 values
+// of each half a lane, whose loads are: 37.4 and 154.9 us for the two below, 37.2 and
+// 153.1 so).  Products of 16-bit pairs go straight into 32 bits.  Not kept: values read
+// with the hint that they leave L2 first (2 to 6 % less for 65,536 rows, 3 to 6 % more for
+// 16,384 and for 196,608 and up).  There and back, at slots in no order: 262,144 rows of 656
+// bytes 153 us, 0.92 of the copy rate; 70,001 of 416 37, 0.83.
 #include "pages.cuh"
 
 namespace hs {
 namespace {
 
 constexpr int ROWS_NT = 128;                     // threads a CTA
-constexpr int NORM_CTAS = 14, GATHER_CTAS = 16;  // CTAs an SM (norm: 12 164 us, 14 and 16 157)
+constexpr int NORM_CTAS = 14, GATHER_CTAS = 16;  // CTAs an SM (norm: 12 161 us, 14 and 16 154)
 constexpr int ROWS_A_CTA = ROWS_NT / 32;
 
 template <int DT>
@@ -42,18 +44,37 @@ __device__ __forceinline__ uint4 pack16(const float (&x)[8])
     return make_uint4(floats_to_pair<DT>(x[0], x[1]), floats_to_pair<DT>(x[2], x[3]), floats_to_pair<DT>(x[4], x[5]), floats_to_pair<DT>(x[6], x[7]));
 }
 
-// Largest magnitude of the 8 values of LANES neighbouring lanes; NaN if one is.
-template <int LANES>
-__device__ __forceinline__ float largest(const float (&t)[8])
+// sum + a[k] b[k], k = 0, 1, and a[k] b[k], of 16-bit pairs, in 32 bits.
+template <int DT>
+__device__ __forceinline__ float fma16(uint32_t a, uint32_t b, int k, float c)
 {
-    auto max_nan = [](float x, float y) {
-        float z;
-        asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(fabsf(x)), "f"(fabsf(y)));
-        return z;
+    const uint16_t x = (uint16_t)(a >> (16 * k)), y = (uint16_t)(b >> (16 * k));
+    float d;
+    if (DT == kBf16)
+        asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"(x), "h"(y), "f"(c));
+    else
+        asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(d) : "h"(x), "h"(y), "f"(c));
+    return d;
+}
+
+// Largest magnitude of the 16 values of LANES neighbouring lanes; NaN if one is.
+template <int LANES>
+__device__ __forceinline__ float largest(const float (&t)[16])
+{
+    auto max3 = [](float x, float y, float z) {
+        float m;
+        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(fabsf(x)), "f"(fabsf(y)), "f"(fabsf(z)));
+        return m;
     };
-    float m = max_nan(max_nan(max_nan(t[0], t[1]), max_nan(t[2], t[3])), max_nan(max_nan(t[4], t[5]), max_nan(t[6], t[7])));
+    float m = fabsf(t[15]);
 #pragma unroll
-    for (int d = 1; d < LANES; d *= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+    for (int j = 0; j < 14; j += 2) m = j ? max3(m, t[j], t[j + 1]) : max3(t[0], t[1], t[15]);
+    m = max3(m, t[14], t[14]);
+#pragma unroll
+    for (int d = 1; d < LANES; d *= 2) {
+        const float o = __shfl_xor_sync(0xffffffffu, m, d);
+        m = max3(m, o, o);
+    }
     return m;
 }
 
@@ -74,50 +95,29 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// Values t f, those from 256 half + 8 lane on, to a row.
-__device__ __forceinline__ void store8(uint8_t *dst, const float (&t)[8], float f, int half, int lane)
+// Values t f, those from 16 lane on, to a row.
+__device__ __forceinline__ void store8(uint8_t *dst, float (&t)[16], float f, int lane)
 {
-    const float top = largest<16>(t) * f;
+    const float top = largest<8>(t) * f;
     const uint32_t m = __float_as_uint(top);
     // infinities have the exponent of 2^128: 2^120, and their codes clip to 448
     const int k = scale_exponent(min(m, 0x7F800000u));
-    float by = f * power_of_two(-k), u[8];      // (exact: a power of two)
+    float by = f * power_of_two(-k);            // (exact: a power of two)
     const bool far = !(by <= FLT_MAX);          // a group of zeros, or next to it
-    if (far) by = power_of_two(-k);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = t[j];
     if (far) {
+        by = power_of_two(-k);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] *= f;
+        for (int j = 0; j < 16; ++j) t[j] *= f;
     }
-    *reinterpret_cast<uint2 *>(dst + half * 256 + lane * 8) =
-        make_uint2(e4m3x4(u[0] * by, u[1] * by, u[2] * by, u[3] * by), e4m3x4(u[4] * by, u[5] * by, u[6] * by, u[7] * by));
-    if ((lane & 15) == 0)
-        *reinterpret_cast<float *>(dst + kRow8ScaleAt + (half * 2 + (lane >> 4)) * 4) = top != top ? top : power_of_two(k);
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = e4m3x4(t[4 * j] * by, t[4 * j + 1] * by, t[4 * j + 2] * by, t[4 * j + 3] * by);
+    st_v4(dst + lane * 16, make_uint4(c[0], c[1], c[2], c[3]));
+    if ((lane & 7) == 0) *reinterpret_cast<float *>(dst + kRow8ScaleAt + (lane >> 3) * 4) = top != top ? top : power_of_two(k);
 }
 
-// NORM: t f is any 32-bit number, and t (f / scale) as good as the quotient; else f is 1
-// and t has a 16-bit type's value, and may lie on a border between two codes: then the
-// product's rounding is taken out (see rows4.cu), which would move numbers next to a
-// border onto it.
-template <bool NORM>
-__device__ __forceinline__ void store4(uint8_t *dst, const float (&t)[8], float f, int half, int lane)
+__device__ __forceinline__ uint32_t e2m1x8(const float (&q)[16], int j)
 {
-    const float top = largest<2>(t) * f;
-    uint16_t e8;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e8) : "f"(0.0f), "f"(__fdiv_rn(top, 6.0f)));
-    const float scale = __low2float(scale_half2(e8 & 0xFFu));
-    const float inv = scale == 0.0f ? 0.0f : __frcp_rn(scale), by = f * inv;
-    float q[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (NORM) {
-            q[j] = t[j] * by;
-        } else {
-            const float x = __fadd_rn(__fmaf_rn(t[j], inv, 48.0f), -48.0f);
-            q[j] = __uint_as_float((__float_as_uint(x) & 0x7FFFFFFFu) | (__float_as_uint(t[j]) & 0x80000000u));
-        }
-    }
     uint32_t out;
     asm("{\n"
         ".reg .b8 b0, b1, b2, b3;\n"
@@ -128,9 +128,41 @@ __device__ __forceinline__ void store4(uint8_t *dst, const float (&t)[8], float 
         "mov.b32 %0, {b0, b1, b2, b3};\n"
         "}"
         : "=r"(out)
-        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
-    *reinterpret_cast<uint32_t *>(dst + half * 128 + lane * 4) = out;
-    if (!(lane & 1)) dst[kScaleAt + half * 16 + (lane >> 1)] = (uint8_t)e8;
+        : "f"(q[j]), "f"(q[j + 1]), "f"(q[j + 2]), "f"(q[j + 3]), "f"(q[j + 4]), "f"(q[j + 5]), "f"(q[j + 6]), "f"(q[j + 7]));
+    return out;
+}
+
+// NORM: t f is any 32-bit number, and t (f / scale) as good as the quotient; else f is 1
+// and t has a 16-bit type's value, and may lie on a border between two codes: then the
+// product's rounding is taken out (see rows4.cu), which would move numbers next to a
+// border onto it.
+template <bool NORM>
+__device__ __forceinline__ void store4(uint8_t *dst, float (&t)[16], float f, int lane)
+{
+    const float top = largest<1>(t) * f;
+    uint16_t e8;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e8) : "f"(0.0f), "f"(__fdiv_rn(top, 6.0f)));
+    const float scale = __low2float(scale_half2(e8 & 0xFFu));
+    float inv;
+    if (NORM) {      // (approximate, and one step of Newton's method; scale >= 2^-9 or 0)
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+        inv = fmaf(inv, fmaf(-scale, inv, 1.0f), inv);
+    } else {
+        inv = __frcp_rn(scale);
+    }
+    inv = scale == 0.0f ? 0.0f : inv;
+    const float by = f * inv;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        if (NORM) {
+            t[j] *= by;
+        } else {
+            const float x = __fadd_rn(__fmaf_rn(t[j], inv, 48.0f), -48.0f);
+            t[j] = __uint_as_float((__float_as_uint(x) & 0x7FFFFFFFu) | (__float_as_uint(t[j]) & 0x80000000u));
+        }
+    }
+    *reinterpret_cast<uint2 *>(dst + lane * 8) = make_uint2(e2m1x8(t, 0), e2m1x8(t, 8));
+    dst[kScaleAt + lane] = (uint8_t)e8;
 }
 
 // 1 / sqrt(v), by one step of Newton's method from the approximate root, off by about
@@ -151,50 +183,59 @@ __device__ __forceinline__ int64_t row_of_value(const RowsLaunch &a, int64_t i)
 template <int DT, int ROW, bool NORM>
 __global__ void __launch_bounds__(ROWS_NT, NORM_CTAS) norm_kernel(const __grid_constant__ RowsLaunch a)
 {
+    // A lane's two pieces of 8 values: 16 neighbouring ones, or of each half of the row
+    constexpr int LANE = ROW == kRow16 ? 16 : 32, NEXT = ROW == kRow16 ? 512 : 16;
     after_launch_before();
     const int lane = threadIdx.x & 31;
     const int64_t i = (int64_t)blockIdx.x * ROWS_A_CTA + (threadIdx.x >> 5);
     if (i >= a.n) return;      // the same for the whole warp
     const uint8_t *src = a.values + i * a.value_stride;
     // (ahead of the slot, which would be one more wait)
-    const uint4 v[2] = {ld_dev_v4(src + lane * 16), ld_dev_v4(src + 512 + lane * 16)};
+    const uint4 v[2] = {ld_dev_v4(src + lane * LANE), ld_dev_v4(src + NEXT + lane * LANE)};
     uint4 rope;
     if (lane < 8) rope = ld_dev_v4(src + kLatent * 2 + lane * 16);
     const int64_t row = row_of_value(a, i);
     if (row < 0) return;
     uint8_t *dst = a.rows + row * a.row_stride;
-    float t[2][8], f = 1.0f;
-    unpack16<DT>(v[0], t[0]);
-    unpack16<DT>(v[1], t[1]);
+    if (lane < 8) st_v4(dst + rope_at(ROW) + lane * 16, rope);
+    float t[16], f = 1.0f;
     if (NORM) {
         float sum = 0.0f;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            float w[8];
-            unpack16<DT>(ld_dev_v4(a.weight + half * 512 + lane * 16), w);
+            const uint4 w4 = ld_dev_v4(a.weight + half * NEXT + lane * LANE);
+            const uint32_t x[4] = {v[half].x, v[half].y, v[half].z, v[half].w}, w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                sum = fmaf(t[half][j], t[half][j], sum);
-                t[half][j] *= w[j];
+                sum = fma16<DT>(x[j >> 1], x[j >> 1], j & 1, sum);
+                t[half * 8 + j] = fma16<DT>(x[j >> 1], w[j >> 1], j & 1, -0.0f);
             }
         }
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         f = inverse_root(fmaf(sum, 1.0f / kLatent, a.eps));
-    }
+    } else {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        if (ROW == kRow16) {
+        for (int half = 0; half < 2; ++half) {
+            float x[8];
+            unpack16<DT>(v[half], x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) t[half][j] *= f;
-            st_v4(dst + half * 512 + lane * 16, pack16<DT>(t[half]));
-        } else if (ROW == kRow8) {
-            store8(dst, t[half], f, half, lane);
-        } else {
-            store4<NORM>(dst, t[half], f, half, lane);
+            for (int j = 0; j < 8; ++j) t[half * 8 + j] = x[j];
         }
     }
-    if (lane < 8) st_v4(dst + rope_at(ROW) + lane * 16, rope);
+    if (ROW == kRow16) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = t[half * 8 + j] * f;
+            st_v4(dst + half * 512 + lane * 16, pack16<DT>(x));
+        }
+    } else if (ROW == kRow8) {
+        store8(dst, t, f, lane);
+    } else {
+        store4<NORM>(dst, t, f, lane);
+    }
 }
 
 template <int DT, int ROW>
