@@ -12,7 +12,8 @@
 // to the workspace in 16 bits, in the layout that the tensor cores read, so that
 // tiles come in as plain bulk copies whatever the format, the pages' size and the
 // strides; rows that are not there are 0, and a bit a row says so.  prefix_kernel
-// multiplies.  join_kernel adds up heads whose rows were split.
+// multiplies; its CTAs start beside expand_kernel's.  join_kernel adds up heads whose
+// rows were split.
 //
 // prefix_kernel.  O of 128 heads by 512 values would fill tensor memory and leave
 // nothing for S, and 64 heads a CTA run the tensor cores at half their rate (128
@@ -45,10 +46,11 @@
 // through each SM's (operands of S 112, of O 96, keys and values coming in 106, P 16) in
 // 2,650 cycles, 125 of its 128 bytes a cycle, where the products alone take 2,184.  Without
 // the copies a tile takes 2,330.  With little, a pair's start (1 thousand cycles, queries
-// 4) and end (5 to 7 for O, at some 25 bytes a cycle that an SM stores) and the launches
-// around it.  Measured on GB300, GPU time of a call: 256 requests of 16 heads over 40,000
-// rows 225 us (1,582 TFLOP/s, 0.82 of cuBLAS's best); 32 of 128 heads over 8,192 63; 32 of
-// 16 over 8,192 25; 37 of 40 over 5,003 30; 4 of 16 over 2,048 12.
+// 4, while the rows are expanded) and end (5 to 7 for O, at some 25 bytes a cycle that an
+// SM stores) and the launches around it.  Measured on GB300, GPU time of a call: 256
+// requests of 16 heads over 40,000 rows 225 us (1,582 TFLOP/s, 0.82 of cuBLAS's best); 32 of
+// 128 heads over 8,192 62; 32 of 16 over 8,192 22.5; 37 of 40 over 5,003 28; 4 of 16 over
+// 2,048 10.8.
 // Rounding.  Latent values of 4-bit rows, and of 8-bit rows with powers of two as scales,
 // are exact in both types, and so are queries.  P is rounded to the model's type (half a
 // step: 2^-8 of a probability in bf16), which the product's two operands share; out's error
@@ -113,7 +115,7 @@ struct PrefixParts {
         int16_t first, parts;
     } join[MAX_PAIRS];
     uint8_t *image;          // [tiles][2] half tiles
-    uint32_t *there;         // [tiles][4] a bit a key
+    uint8_t *there;          // [tiles][32] the low four bits: a bit a key
     uint8_t *o;              // [pairs][2] parts of O of 128 heads that a pair does not have whole (see
                              // part_at): of a group that it begins in the middle, of one from its start
     float2 *ml;              // [pairs][2][128] reference and sum
@@ -131,60 +133,68 @@ __host__ __device__ __forceinline__ int part_at(int i, int n)
 
 // ---- expand ------------------------------------------------------------------------
 
-constexpr int EX_NT = 256, EX_KEYS = 32, EX_ROWS = EX_KEYS / (EX_NT / 32);
+// Warps without a word to each other: a round of EX_ROWS rows, a byte of `there`, or, with
+// ROUNDS 2, another behind it, whose rows are called into L2 meanwhile.  64 registers, 7
+// warps and no shared memory: a CTA finds a place beside prefix_kernel's (192 registers,
+// and nearly all shared memory), which so has its tensor memory and its queries, 3 to 4 us,
+// by when the rows are there.
+constexpr int EX_NT = 224, EX_ROWS = 4;
 
-template <int DT, int ROW>
-__global__ void __launch_bounds__(EX_NT) expand_kernel(const __grid_constant__ PrefixLaunch a, const __grid_constant__ PrefixParts w)
+template <int DT, int ROW, int ROUNDS>
+__global__ void __maxnreg__(64) expand_kernel(const __grid_constant__ PrefixLaunch a, const __grid_constant__ PrefixParts w)
 {
-    __shared__ uint32_t there;
-    __shared__ int bad;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (threadIdx.x == 0) there = 0, bad = 0;
-    __syncthreads();
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) * gridDim.x + blockIdx.x, warps = EX_NT / 32 * gridDim.x;
+    const int rounds = w.tiles * (KEYS / EX_ROWS);
     after_launch_before();
     // prefix_kernel may be placed now: after this wait, as it reads its queries ahead of
     // its own
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int t0 = blockIdx.x * EX_KEYS + warp * EX_ROWS;
-    int64_t row = -1;
-    if (lane < EX_ROWS && t0 + lane < a.len) {
-        const int t = t0 + lane, b = t / a.bs;
+    const int ahead = lane / EX_ROWS, t = (warp + ahead * warps) * EX_ROWS + lane % EX_ROWS;
+    const uint8_t *mine = nullptr;
+    bool bad = false;
+    if (ahead < ROUNDS && t < a.len) {
+        const int b = t / a.bs;
         const int32_t page = a.table[b];
-        row = (int64_t)page * a.bs + (t - b * a.bs);
-        if (page < 0 || row >= a.num_rows) {
-            row = -1;
-            if (page != -1) bad = 1;
+        const int64_t row = (int64_t)page * a.bs + (t - b * a.bs);
+        if (page >= 0 && row < a.num_rows)
+            mine = a.rows + row * a.row_stride;
+        else
+            bad = page != -1;
+    }
+    if (ROUNDS > 1 && ahead == 1 && mine)      // (into L2)
+#pragma unroll
+        for (int x = 0; x < ROW; x += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(mine + x));
+    const uint32_t named = __ballot_sync(0xffffffffu, mine != nullptr);
+#pragma unroll 1
+    for (int k = 0; k < ROUNDS && warp + k * warps < rounds; ++k) {
+        const int n = warp + k * warps;
+        Latent8<ROW> v[EX_ROWS][2];
+        uint4 rope[EX_ROWS];
+#pragma unroll
+        for (int j = 0; j < EX_ROWS; ++j) {
+            const uint8_t *p = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), k * EX_ROWS + j));
+            rope[j] = make_uint4(0, 0, 0, 0);
+            if (p) {
+                v[j][0].fetch(p, lane);
+                v[j][1].fetch(p, lane + 32);
+                if (lane < 8) rope[j] = ld_dev_v4(p + rope_at(ROW) + lane * 16);
+            }
+        }
+        if (lane == 0) w.there[n] = (uint8_t)(named >> (k * EX_ROWS) & ((1u << EX_ROWS) - 1));
+        uint8_t *half = w.image + (int64_t)(n / (64 / EX_ROWS)) * HALF_TILE;
+#pragma unroll
+        for (int j = 0; j < EX_ROWS; ++j) {
+            const int i = n % (64 / EX_ROWS) * EX_ROWS + j;
+            const uint32_t x = ((lane & 7) ^ (i & 7)) << 4;
+            // unit lane + 32 k is in block lane / 8 + 4 k, which is at place 0 1 4 5, 2 3 6 7
+            const int place = (lane >> 4) * 4 + (lane >> 3 & 1);
+            st_v4(half + place * BLOCK + i * 128 + x, latent8<DT, ROW>(v[j][0]));
+            st_v4(half + (place + 2) * BLOCK + i * 128 + x, latent8<DT, ROW>(v[j][1]));
+            if (lane < 8) st_v4(half + 8 * BLOCK + i * 128 + x, rope[j]);
         }
     }
-    const uint32_t named = __ballot_sync(0xffffffffu, row >= 0);
-    uint4 v[EX_ROWS][2], rope[EX_ROWS];
-#pragma unroll
-    for (int j = 0; j < EX_ROWS; ++j) {
-        const int64_t n = __shfl_sync(0xffffffffu, row, j);
-        v[j][0] = v[j][1] = rope[j] = make_uint4(0, 0, 0, 0);
-        if (n >= 0) {
-            const uint8_t *p = a.rows + n * a.row_stride;
-            v[j][0] = load_latent8<DT, ROW>(p, lane);
-            v[j][1] = load_latent8<DT, ROW>(p, lane + 32);
-            if (lane < 8) rope[j] = ld_dev_v4(p + rope_at(ROW) + lane * 16);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < EX_ROWS; ++j) {
-        const int t = t0 + j, i = t & 63;
-        uint8_t *half = w.image + (int64_t)(t >> 6) * HALF_TILE;
-        const uint32_t u = ((lane & 7) ^ (i & 7)) << 4;
-        // unit lane + 32 k is in block lane / 8 + 4 k, which is at place 0 1 4 5, 2 3 6 7
-        const int place = (lane >> 4) * 4 + (lane >> 3 & 1);
-        st_v4(half + place * BLOCK + i * 128 + u, v[j][0]);
-        st_v4(half + (place + 2) * BLOCK + i * 128 + u, v[j][1]);
-        if (lane < 8) st_v4(half + 8 * BLOCK + i * 128 + u, rope[j]);
-    }
-    if (lane == 0) atomicOr(&there, named << (warp * EX_ROWS));
-    __syncthreads();
-    if (threadIdx.x == 0) w.there[blockIdx.x] = there;
-    if (bad && a.status)
-        for (int r = threadIdx.x; r < a.R; r += EX_NT) record_status(a.status, r, kStatusBadResident);
+    if (__any_sync(0xffffffffu, bad) && a.status)
+        for (int r = lane; r < a.R; r += 32) record_status(a.status, r, kStatusBadResident);
 }
 
 // ---- pairs of CTAs ---------------------------------------------------------------
@@ -264,6 +274,24 @@ __device__ __forceinline__ float add_part(float &m, float &l, float part_lse, fl
     return f;
 }
 
+// The bits of 32 keys, four a byte.
+__device__ __forceinline__ uint32_t bits_of(uint32_t x, uint32_t y)
+{
+    auto half = [](uint32_t z) {
+        z = (z | z >> 4) & 0x00FF00FFu;
+        return (z | z >> 8) & 0xFFFFu;
+    };
+    return half(x) | half(y) << 16;
+}
+
+// A CTA's heads of a group: all 64 but of the last, of which both have half, so that
+// neither brings in, keeps up and stores more than it must.
+__host__ __device__ __forceinline__ int heads_of_cta(int heads, int group)
+{
+    const int left = heads - group * PAIR_HEADS;
+    return left < PAIR_HEADS ? (left + 1) / 2 : CTA_HEADS;
+}
+
 // A head's request and number.  (At most 2^13 requests of 2^10 heads.)
 struct HeadPlace {
     int r, h;
@@ -288,7 +316,7 @@ __device__ __forceinline__ bool meet(int id, int threads, bool go)
 }
 
 template <int DT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
+__global__ void __cluster_dims__(2, 1, 1) __maxnreg__(192)
     prefix_kernel(const __grid_constant__ PrefixLaunch a, const __grid_constant__ PrefixParts w)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -357,14 +385,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
         // head's 128 bytes, all of it on its way at once; then through P's place, 16 KB at
         // a time, to a thread's lane.  (A thread its own head's, 16 bytes of 32 heads a
         // load: 11 thousand cycles against 5.)
+        const int heads = a.R * a.H;
         auto place_queries = [&](int group) {
+            const int share = heads_of_cta(heads, group), head0 = group * PAIR_HEADS + rank * share;
             const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, set = nan ? 0x7FFF7FFFu : 0u;
             const int unit = lane & 7, first = warp * 4 + (lane >> 3);      // heads first + 16 k
             uint4 v[9][4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int head = group * PAIR_HEADS + rank * CTA_HEADS + first + 16 * k;
-                const bool on = head < a.R * a.H;
+                const int head = head0 + first + 16 * k;
+                const bool on = first + 16 * k < share && head < heads;
                 const HeadPlace at(a, on ? head : 0);
                 const uint8_t *q = a.q + at.r * a.q_rs + at.h * a.q_hs + unit * 16;
 #pragma unroll
@@ -437,16 +467,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
             // (all four warps come here as often, whatever has gone wrong; P's place is free)
             if (!(ok = meet_all(ok))) break;
             const int t1 = group == end.group ? end.tile : w.tiles;
-            const int head = group * PAIR_HEADS + rank * CTA_HEADS + i;
-            const bool on = head < a.R * a.H;
+            const int share = heads_of_cta(heads, group), head = group * PAIR_HEADS + rank * share + i;
+            const bool on = i < share && head < heads;
+            const int here = __popc(__ballot_sync(0xffffffffu, on));      // of the warp's heads
             place_queries(group);
             if (group == begin.group) after_launch_before();
             float m = -INFINITY, l = 0.0f;
-            const uint32_t *there = w.there + half * 2;
-            uint2 next = *reinterpret_cast<const uint2 *>(there + (int64_t)t0 * 4);
+            const uint8_t *there = w.there + half * 16;
+            uint4 next = *reinterpret_cast<const uint4 *>(there + (int64_t)t0 * 32);
             for (int t = t0; t < t1; ++t, ++n) {
-                const uint2 named = next;
-                if (t + 1 < t1) next = *reinterpret_cast<const uint2 *>(there + (int64_t)(t + 1) * 4);
+                const uint4 named = next;
+                if (t + 1 < t1) next = *reinterpret_cast<const uint4 *>(there + (int64_t)(t + 1) * 32);
                 ok = ok && all(mbar_wait(bar(sm.scored[n & 1]), (n >> 1) & 1, gave_up));
                 tc_fence_after();
                 uint32_t v[2][32];
@@ -456,11 +487,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
                 tc_fence_before();
                 tell(read_at + (n & 1) * 8);
                 float (&x)[2][32] = reinterpret_cast<float (&)[2][32]>(v);
-                if ((named.x & named.y) != 0xFFFFFFFFu) {
+                if ((named.x & named.y & named.z & named.w) != 0x0F0F0F0Fu) {
+                    const uint32_t lo = bits_of(named.x, named.y), hi = bits_of(named.z, named.w);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        if (!(named.x >> j & 1u)) x[0][j] = -INFINITY;
-                        if (!(named.y >> j & 1u)) x[1][j] = -INFINITY;
+                        if (!(lo >> j & 1u)) x[0][j] = -INFINITY;
+                        if (!(hi >> j & 1u)) x[1][j] = -INFINITY;
                     }
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -543,7 +575,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
                 weight *= inv;
                 const unsigned long long to = reinterpret_cast<unsigned long long>(on ? a.out + at.r * a.out_rs + at.h * a.out_hs + half * 512 : nullptr);
                 const unsigned long long from = reinterpret_cast<unsigned long long>(part);
-                all_columns([&](int c, int k, uint4 o) {
+                if (here > 0) all_columns([&](int c, int k, uint4 o) {
                     const int h = k * 4 + (lane >> 3);
                     const float fo = __shfl_sync(0xffffffffu, scale, h), fp = __shfl_sync(0xffffffffu, weight, h);
                     uint8_t *dst = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, to, h));
@@ -570,7 +602,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
                 uint32_t o[32];
                 tmem_ld_32(lanes + T_O, o);
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; here > 0 && c < 8; ++c) {
                     const uint32_t image = c % 3 == 2 ? base + P_AT + warp * PART_IMAGE : base + Q_AT + (warp * 2 + c % 3) * PART_IMAGE;
                     if (c >= 3) asm volatile("cp.async.bulk.wait_group.read 2;" ::: "memory");      // (lane 0's)
                     __syncwarp();
@@ -584,7 +616,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PX_NT, 1)
                     if (lane == 0)
                         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n"
                                      "cp.async.bulk.commit_group;" ::"l"(to + c * PART_IMAGE),
-                                     "r"(image), "n"(PART_IMAGE)
+                                     "r"(image), "r"(here * 128)
                                      : "memory");
                 }
                 asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -761,7 +793,7 @@ constexpr int JOIN_WIDE = 1024;      // heads that get four warps each
 // latency: references and sums, and the values of the first parts, are loaded at once,
 // and the values wait for nothing else.
 template <int DT, int WARPS>
-__global__ void __launch_bounds__(JOIN_NT) join_kernel(const __grid_constant__ PrefixLaunch a, const __grid_constant__ PrefixParts w)
+__global__ void __launch_bounds__(JOIN_NT, 4) join_kernel(const __grid_constant__ PrefixLaunch a, const __grid_constant__ PrefixParts w)
 {
     constexpr int FOURS = 4 / WARPS, AT_ONCE = 16 / FOURS;      // of a lane's values; parts
     constexpr int LANES = (MAX_PAIRS + 31) / 32;
@@ -769,8 +801,10 @@ __global__ void __launch_bounds__(JOIN_NT) join_kernel(const __grid_constant__ P
     const int n = WARPS == 4 ? blockIdx.x : blockIdx.x * 4 + warp, four = WARPS == 4 ? threadIdx.x : lane;
     PrefixParts::Join join = {n / PAIR_HEADS, 0, 0};
     if (w.pairs > 0) join = w.join[n / PAIR_HEADS];
-    const int i = n % PAIR_HEADS, head = join.group * PAIR_HEADS + i;
+    const int head = join.group * PAIR_HEADS + n % PAIR_HEADS;
     const bool on = head < a.R * a.H;
+    const int share = heads_of_cta(a.R * a.H, join.group);
+    const int i = n % PAIR_HEADS < share ? n % PAIR_HEADS : n % PAIR_HEADS - share + CTA_HEADS;
     const HeadPlace at(a, on ? head : 0);
     // (a pair's second place is for the group that it has from its start)
     auto place = [&](int p) { return (int64_t)(join.first + p) * 2 + (p == 0); };
@@ -928,8 +962,8 @@ PrefixParts lay_out(int32_t R, int32_t H, int32_t len, uint8_t *ws, int64_t *byt
     n += (int64_t)w.pairs * 2 * PAIR_HEADS * kLatent * 4;
     w.ml = reinterpret_cast<float2 *>(ws + n);
     n += (int64_t)w.pairs * 2 * PAIR_HEADS * 8;
-    w.there = reinterpret_cast<uint32_t *>(ws + n);
-    n += (int64_t)w.tiles * 16;
+    w.there = ws + n;
+    n += (int64_t)w.tiles * 32;
     n = (n + 127) / 128 * 128;
     w.image = ws + n;
     n += (int64_t)w.tiles * TILE_BYTES;
@@ -949,26 +983,54 @@ cudaError_t prepare_device()
     if (!known[dev].load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(prefix_kernel<kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PX_SMEM);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(prefix_kernel<kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PX_SMEM);
+        auto beside = [&](auto kernel) {      // (see launch_expand)
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+        };
+        beside(expand_kernel<kBf16, kRow4, 2>), beside(expand_kernel<kBf16, kRow8, 2>), beside(expand_kernel<kBf16, kRow16, 2>);
+        beside(expand_kernel<kF16, kRow4, 2>), beside(expand_kernel<kF16, kRow8, 2>), beside(expand_kernel<kF16, kRow16, 2>);
         if (e != cudaSuccess) return e;
         known[dev].store(true, std::memory_order_release);
     }
     return cudaSuccess;
 }
 
+// Many rows: as many CTAs as there is work for, and L1 as large as it gets, which holds
+// what is on its way (256 x 16 heads over 40,000 rows of 16 bits: 226 us, 230 with the
+// other kernel's).  Few: shared memory as prefix_kernel wants it, as an SM changes that
+// only when it is idle; and one CTA an SM if most of its warps have two rounds then (32 x
+// 16 heads, 8,192 rows: 22.3 us, 23.1 with a round a warp; 37 x 40 heads, 5,003 rows, 27.9
+// and 27.4 the other way round).  (The kernel before, of 256 threads and 32 rows a CTA,
+// beside which there was no place: 25.0 and 29.8.)
+int expand_rounds(int tiles) { return tiles * (KEYS / EX_ROWS) <= 2 * 2 * MAX_PAIRS * (EX_NT / 32) ? 2 : 1; }      // at most
+
+int expand_ctas(int tiles)
+{
+    constexpr int SMS = 2 * MAX_PAIRS;
+    const int all = (tiles * (KEYS / EX_ROWS) + EX_NT / 32 - 1) / (EX_NT / 32);
+    return expand_rounds(tiles) == 2 && all > SMS + SMS / 2 ? SMS : all;
+}
+
+template <int DT, int ROW>
+cudaError_t launch_expand(const PrefixLaunch &a, const PrefixParts &w, cudaStream_t s)
+{
+    const dim3 ctas(expand_ctas(w.tiles));
+    if (expand_rounds(w.tiles) == 2) return launch_behind(expand_kernel<DT, ROW, 2>, ctas, EX_NT, 0, 1, s, a, w);
+    return launch_behind(expand_kernel<DT, ROW, 1>, ctas, EX_NT, 0, 1, s, a, w);
+}
+
 template <int DT>
 cudaError_t launch(const PrefixLaunch &a, const PrefixParts &w, cudaStream_t s)
 {
     if (w.pairs > 0) {
-        auto expand = a.row_bytes == kRow4 ? expand_kernel<DT, kRow4> : a.row_bytes == kRow8 ? expand_kernel<DT, kRow8> : expand_kernel<DT, kRow16>;
-        cudaError_t e = launch_behind(expand, dim3(w.tiles * (KEYS / EX_KEYS)), EX_NT, 0, 1, s, a, w);
+        cudaError_t e = a.row_bytes == kRow4 ? launch_expand<DT, kRow4>(a, w, s) : a.row_bytes == kRow8 ? launch_expand<DT, kRow8>(a, w, s) : launch_expand<DT, kRow16>(a, w, s);
         if (e != cudaSuccess) return e;
         e = launch_behind(prefix_kernel<DT>, dim3(w.pairs * 2), PX_NT, PX_SMEM, 2, s, a, w);
         if (e != cudaSuccess) return e;
         if (w.joins == 0) return e;
     }
     // Four warps a head where there are few, with many parts each (32 x 16 heads over 8,192
-    // rows: 25.0 us, with one 31.8), else one (32 x 128 heads, 2 or 3 parts each: 63.1 us,
-    // with four 66.8).
+    // rows: 25.0 us, with one 31.8, at the time), else one (32 x 128 heads, 2 or 3 parts each:
+    // 63.1 us, with four 66.8).
     const int heads = (w.pairs > 0 ? w.joins : w.groups) * PAIR_HEADS;
     if (heads <= JOIN_WIDE) return launch_behind(join_kernel<DT, 4>, dim3(heads), JOIN_NT, 0, 1, s, a, w);
     return launch_behind(join_kernel<DT, 1>, dim3(heads / 4), JOIN_NT, 0, 1, s, a, w);

@@ -123,6 +123,19 @@ def test_heads(R, heads):
          requests=None if R * heads < 2000 else [0, 1, R // 2, R - 1])
 
 
+@pytest.mark.parametrize("heads", [1, 2, 3, 31, 33, 34, 64, 65, 72, 96, 97, 130, 191, 193, 200])
+@pytest.mark.parametrize("n", [100, 1500])
+def test_the_last_heads_are_shared_out(heads, n):
+    """Groups of heads that are not full, in one pair and in parts."""
+    call(1, heads, n, M.ROW8, "bf16", seed=heads, part=heads % 2 == 0)
+
+
+@pytest.mark.parametrize("n", [4256, 4257, 6272, 6273, 8448, 8449])
+@pytest.mark.parametrize("row", ROWS)
+def test_lengths_where_the_rows_come_in_another_way(n, row):
+    call(2, 4, n, row, bs=64, seed=n, holes=0.1)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("row", ROWS)
 @pytest.mark.parametrize("R,heads,n", [(4, 16, 2048), (37, 40, 5003), (200, 128, 130), (9, 128, 9000)])

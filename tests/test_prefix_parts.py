@@ -102,6 +102,28 @@ int main()
         bad += block_at((u % 32 / 16) * 4 + (u % 32 / 8 & 1) + (u >= 32 ? 2 : 0)) != u / 8;
     bad += MISC_AT % 1024 != 0 || sizeof(PrefixSmem) + MISC_AT > 232448 || ROPE_AT != SLOTS * SLOT || SLOT != 4 * BLOCK;
     bad += Q_SMEM * BLOCK < 8 * PART_IMAGE || P_AT + 4 * PART_IMAGE > MISC_AT || T_Q + Q_TMEM * 32 > 512 || T_S + 128 > T_Q;
+    // the heads of both CTAs of every group: each once, 64 of a CTA at most
+    for (int heads = 1; heads < 400; ++heads) {
+        std::vector<int> had(heads, 0);
+        for (int g = 0; g * 128 < heads; ++g) {
+            const int share = heads_of_cta(heads, g);
+            bad += share < 1 || share > 64;
+            for (int rank = 0; rank < 2; ++rank)
+                for (int i = 0; i < share; ++i) {
+                    const int head = g * 128 + rank * share + i;      // as prefix_kernel
+                    if (head >= heads) continue;
+                    bad += head >= (g + 1) * 128 || had[head]++;
+                    const int h = head % 128;                         // as join_kernel
+                    bad += (h < share ? h : h - share + 64) != rank * 64 + i;
+                }
+        }
+        for (int n : had) bad += n != 1;
+    }
+    // the rounds of expand_kernel: none left out, whatever the length
+    for (int tiles = 1; tiles <= 8192; ++tiles) {
+        const int rounds = tiles * (KEYS / EX_ROWS), n = expand_rounds(tiles), warps = expand_ctas(tiles) * (EX_NT / 32);
+        bad += n < 1 || n > 2 || (int64_t)warps * n < rounds;
+    }
     std::printf("%ld parts, %ld wrong\n", n, bad);
     return bad != 0;
 }
