@@ -5,18 +5,20 @@
 // values is exact in 32 bits, so y = t f has one rounding of its own and those of the one
 // factor f = 1 / sqrt, and the largest |y| of a group is that of t, times f.  Then per
 // group of 128 values a power of two s and e4m3 codes of t (f / s), per group of 16 an
-// e4m3 scale and e2m1 codes, or y in 16 bits.
+// e4m3 scale and e2m1 codes, or y in 16 bits.  Codes and scales are those of unlimited
+// precision: worked out with f too small and too large by what it may be off, and, where
+// that makes a difference, with numbers of 47 bits.
 //
 // Bound by HBM: 1,152 bytes of values and 416 to 1,152 of row, each moved once; nothing
-// is kept between rows; and, next to it, by instructions (of 4-bit rows 256 a row and
-// warp took 23 us for 70,001 rows, 16 for their bytes).  A warp works on a whole row.  For
+// is kept between rows; and, next to it, by instructions.  A warp works on a whole row.  For
 // codes a lane has 16 neighbouring values: a group of 16 is a lane's own, one of 128 eight
 // lanes', its scale worked out once a lane, and the codes' stores are contiguous (8 values
 // of each half a lane, whose loads are: 37.4 and 154.9 us for the two below, 37.2 and
-// 153.1 so).  Products of 16-bit pairs go straight into 32 bits.  Not kept: values read
-// with the hint that they leave L2 first (2 to 6 % less for 65,536 rows, 3 to 6 % more for
-// 16,384 and for 196,608 and up).  There and back, at slots in no order: 262,144 rows of 656
-// bytes 153 us, 0.92 of the copy rate; 70,001 of 416 37, 0.83.
+// 153.1 so, both with codes of 32 bits).  Products of 16-bit pairs go straight into 32 bits.
+// Not kept: values read with the hint that they leave L2 first (2 to 6 % less for 65,536
+// rows, 3 to 6 % more for 16,384 and for 196,608 and up).  There and back, at slots in no
+// order: 262,144 rows of 656 bytes 156.5 us, 0.90 of the copy rate; 70,001 of 416 38.1, 0.81
+// (with codes of 32 bits 152.5 and 36.9).
 #include "pages.cuh"
 
 namespace hs {
@@ -95,8 +97,18 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// Values t f, those from 16 lane on, to a row.
-__device__ __forceinline__ void store8(uint8_t *dst, float (&t)[16], float f, int lane)
+// How far t f / scale may be from what it stands for: 13 roundings of 2^-24 (of the sum of
+// squares 10, of which the root halves what they come to; the mean, the root 2, 1 / scale 2,
+// the products 3).  Codes and scales that are the same this far to both sides are those of
+// unlimited precision; a row with others, one in a hundred, is done again with twice the
+// bits (exact_row).  (Without that some 40 of 10^9 codes and one of 10^6 scales are the next
+// one, as they are with 32 bits anywhere.)
+constexpr float LOW = 1.0f - 13.0f / (1 << 24), HIGH = 1.0f + 13.0f / (1 << 24);
+
+// Values t f, those from 16 lane on, to a row.  NORM: whether a code or scale may be the
+// one next to it; nothing is stored if the warp has one.
+template <bool NORM>
+__device__ __forceinline__ bool store8(uint8_t *dst, float (&t)[16], float f, int lane)
 {
     const float top = largest<8>(t) * f;
     const uint32_t m = __float_as_uint(top);
@@ -110,10 +122,23 @@ __device__ __forceinline__ void store8(uint8_t *dst, float (&t)[16], float f, in
         for (int j = 0; j < 16; ++j) t[j] *= f;
     }
     uint32_t c[4];
+    bool near = false;
+    if (NORM) {
+        const float low = by * LOW, high = by * HIGH;
+        near = scale_exponent(min(__float_as_uint(top * LOW), 0x7F800000u)) != scale_exponent(min(__float_as_uint(top * HIGH), 0x7F800000u));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = e4m3x4(t[4 * j] * by, t[4 * j + 1] * by, t[4 * j + 2] * by, t[4 * j + 3] * by);
+        for (int j = 0; j < 4; ++j) {
+            c[j] = e4m3x4(t[4 * j] * low, t[4 * j + 1] * low, t[4 * j + 2] * low, t[4 * j + 3] * low);
+            near |= c[j] != e4m3x4(t[4 * j] * high, t[4 * j + 1] * high, t[4 * j + 2] * high, t[4 * j + 3] * high);
+        }
+        if (__any_sync(0xffffffffu, near)) return true;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = e4m3x4(t[4 * j] * by, t[4 * j + 1] * by, t[4 * j + 2] * by, t[4 * j + 3] * by);
+    }
     st_v4(dst + lane * 16, make_uint4(c[0], c[1], c[2], c[3]));
     if ((lane & 7) == 0) *reinterpret_cast<float *>(dst + kRow8ScaleAt + (lane >> 3) * 4) = top != top ? top : power_of_two(k);
+    return false;
 }
 
 __device__ __forceinline__ uint32_t e2m1x8(const float (&q)[16], int j)
@@ -132,37 +157,48 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&q)[16], int j)
     return out;
 }
 
-// NORM: t f is any 32-bit number, and t (f / scale) as good as the quotient; else f is 1
-// and t has a 16-bit type's value, and may lie on a border between two codes: then the
-// product's rounding is taken out (see rows4.cu), which would move numbers next to a
-// border onto it.
+// The same.  Not NORM: f is 1 and t has a 16-bit type's value, and may lie on a border
+// between two codes: then the product's rounding is taken out (see rows4.cu), which would
+// move numbers next to a border onto it.
 template <bool NORM>
-__device__ __forceinline__ void store4(uint8_t *dst, float (&t)[16], float f, int lane)
+__device__ __forceinline__ bool store4(uint8_t *dst, float (&t)[16], float f, int lane)
 {
-    const float top = largest<1>(t) * f;
+    const float top = largest<1>(t) * f, sixth = __fdiv_rn(top, 6.0f);
     uint16_t e8;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e8) : "f"(0.0f), "f"(__fdiv_rn(top, 6.0f)));
+    bool near = false;
+    if (NORM) {
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e8) : "f"(sixth * LOW), "f"(sixth * HIGH));
+        near = (e8 & 0xFFu) != e8 >> 8;
+    } else {
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e8) : "f"(0.0f), "f"(sixth));
+    }
     const float scale = __low2float(scale_half2(e8 & 0xFFu));
-    float inv;
+    uint2 c;
     if (NORM) {      // (approximate, and one step of Newton's method; scale >= 2^-9 or 0)
+        float inv;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
         inv = fmaf(inv, fmaf(-scale, inv, 1.0f), inv);
-    } else {
-        inv = __frcp_rn(scale);
-    }
-    inv = scale == 0.0f ? 0.0f : inv;
-    const float by = f * inv;
+        const float by = f * (scale == 0.0f ? 0.0f : inv), low = by * LOW, high = by * HIGH;
+        float q[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        if (NORM) {
-            t[j] *= by;
-        } else {
+        for (int j = 0; j < 16; ++j) q[j] = t[j] * low;
+        c = make_uint2(e2m1x8(q, 0), e2m1x8(q, 8));
+#pragma unroll
+        for (int j = 0; j < 16; ++j) q[j] = t[j] * high;
+        near |= c.x != e2m1x8(q, 0) || c.y != e2m1x8(q, 8);
+        if (__any_sync(0xffffffffu, near)) return true;
+    } else {
+        const float inv = scale == 0.0f ? 0.0f : __frcp_rn(scale);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
             const float x = __fadd_rn(__fmaf_rn(t[j], inv, 48.0f), -48.0f);
             t[j] = __uint_as_float((__float_as_uint(x) & 0x7FFFFFFFu) | (__float_as_uint(t[j]) & 0x80000000u));
         }
+        c = make_uint2(e2m1x8(t, 0), e2m1x8(t, 8));
     }
-    *reinterpret_cast<uint2 *>(dst + lane * 8) = make_uint2(e2m1x8(t, 0), e2m1x8(t, 8));
+    *reinterpret_cast<uint2 *>(dst + lane * 8) = c;
     dst[kScaleAt + lane] = (uint8_t)e8;
+    return false;
 }
 
 // 1 / sqrt(v), by one step of Newton's method from the approximate root, off by about
@@ -173,11 +209,113 @@ __device__ __forceinline__ float inverse_root(float v)
     return v <= FLT_MAX ? fmaf(0.5f * r, e, r) : r;
 }
 
+// A sum of two numbers, the second less than half a step of the first: 47 bits or more.
+struct Twice {
+    float hi, lo;
+};
+
+// x + y, y small against x (infinities and NaN stay what they are).
+__device__ __forceinline__ Twice together(float x, float y)
+{
+    if (!(fabsf(x) <= FLT_MAX)) return {x, 0.0f};
+    const float h = __fadd_rn(x, y);
+    return {h, __fsub_rn(y, __fsub_rn(h, x))};
+}
+
+__device__ __forceinline__ Twice plus(const Twice &x, const Twice &y)
+{
+    const float s = __fadd_rn(x.hi, y.hi), b = __fsub_rn(s, x.hi);
+    return together(s, __fadd_rn(__fadd_rn(__fsub_rn(x.hi, __fsub_rn(s, b)), __fsub_rn(y.hi, b)), __fadd_rn(x.lo, y.lo)));
+}
+
+__device__ __forceinline__ Twice times(const Twice &x, float y)
+{
+    const float h = __fmul_rn(x.hi, y);
+    return together(h, __fmaf_rn(x.lo, y, __fmaf_rn(x.hi, y, -h)));
+}
+
+// 1 / x: what the approximate quotient leaves, once.
+__device__ __forceinline__ Twice over(const Twice &x, float y)
+{
+    const float inv = __frcp_rn(y), h = __fmul_rn(x.hi, inv);
+    return together(h, __fmul_rn(__fadd_rn(__fmaf_rn(-h, y, x.hi), x.lo), inv));
+}
+
+// 1 / sqrt(v): a step of Newton's method, its difference kept apart.
+__device__ __forceinline__ Twice inverse_root(const Twice &v)
+{
+    const float r = inverse_root(v.hi), p = __fmul_rn(r, r), pl = __fmaf_rn(r, r, -p);
+    const float e = __fsub_rn(__fmaf_rn(-v.hi, p, 1.0f), __fmaf_rn(v.hi, pl, __fmul_rn(v.lo, p)));
+    return together(r, __fmul_rn(__fmul_rn(0.5f, r), e));
+}
+
+// In 32 bits, cut off, with the last bit set if that is not exact: rounded again to fewer
+// bits it gives what x does.
+__device__ __forceinline__ float to_odd(const Twice &x)
+{
+    const uint32_t h = __float_as_uint(x.hi), l = __float_as_uint(x.lo);
+    return x.lo == 0.0f ? x.hi : __uint_as_float((h - ((h ^ l) >> 31)) | 1u);
+}
+
 // The row that value i goes to or comes from; -1: none.
 __device__ __forceinline__ int64_t row_of_value(const RowsLaunch &a, int64_t i)
 {
     const int64_t s = a.slots ? a.slots[i] : i;
     return s < a.num_rows ? s : -1;
+}
+
+// Codes and scales of the warp's row, normalised, with twice the bits.  (Its root is a
+// number: with another, codes are the same to both sides.)
+template <int DT, int ROW>
+__device__ __noinline__ void exact_row(const RowsLaunch &a)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t i = (int64_t)blockIdx.x * ROWS_A_CTA + (threadIdx.x >> 5);
+    const uint8_t *src = a.values + i * a.value_stride;
+    uint8_t *dst = a.rows + row_of_value(a, i) * a.row_stride;
+    float t[16];
+    Twice sums[4] = {};
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        float x[8], w[8];
+        unpack16<DT>(ld_dev_v4(src + half * 16 + lane * 32), x);
+        unpack16<DT>(ld_dev_v4(a.weight + half * 16 + lane * 32), w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            sums[j & 3] = plus(sums[j & 3], {x[j] * x[j], 0.0f});      // (exact)
+            t[half * 8 + j] = x[j] * w[j];
+        }
+    }
+    Twice sum = plus(plus(sums[0], sums[1]), plus(sums[2], sums[3]));
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2)
+        sum = plus(sum, {__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
+    const Twice f = inverse_root(plus({sum.hi / kLatent, sum.lo / kLatent}, {a.eps, 0.0f}));
+    const Twice top = times(f, largest<ROW == kRow8 ? 8 : 1>(t));
+    if (ROW == kRow8) {
+        // (448 is even: a top just above a border is above it when its last bit is set)
+        const int k = scale_exponent(min(__float_as_uint(to_odd(top)), 0x7F800000u));
+        const float by = power_of_two(-k);      // (f times this may be too much: see store8)
+        uint32_t c[4];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const Twice y = times(f, t[j]);
+            t[j] = to_odd({y.hi * by, y.lo * by});
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = e4m3x4(t[4 * j], t[4 * j + 1], t[4 * j + 2], t[4 * j + 3]);
+        st_v4(dst + lane * 16, make_uint4(c[0], c[1], c[2], c[3]));
+        if ((lane & 7) == 0) *reinterpret_cast<float *>(dst + kRow8ScaleAt + (lane >> 3) * 4) = top.hi != top.hi ? top.hi : power_of_two(k);
+    } else {
+        uint16_t e8;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e8) : "f"(0.0f), "f"(to_odd(over(top, 6.0f))));
+        const float scale = __low2float(scale_half2(e8 & 0xFFu));
+        const Twice g = scale == 0.0f ? Twice{0.0f, 0.0f} : over(f, scale);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) t[j] = to_odd(times(g, t[j]));
+        *reinterpret_cast<uint2 *>(dst + lane * 8) = make_uint2(e2m1x8(t, 0), e2m1x8(t, 8));
+        dst[kScaleAt + lane] = (uint8_t)e8;
+    }
 }
 
 template <int DT, int ROW, bool NORM>
@@ -200,17 +338,18 @@ __global__ void __launch_bounds__(ROWS_NT, NORM_CTAS) norm_kernel(const __grid_c
     if (lane < 8) st_v4(dst + rope_at(ROW) + lane * 16, rope);
     float t[16], f = 1.0f;
     if (NORM) {
-        float sum = 0.0f;
+        float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const uint4 w4 = ld_dev_v4(a.weight + half * NEXT + lane * LANE);
             const uint32_t x[4] = {v[half].x, v[half].y, v[half].z, v[half].w}, w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                sum = fma16<DT>(x[j >> 1], x[j >> 1], j & 1, sum);
+                sums[j & 3] = fma16<DT>(x[j >> 1], x[j >> 1], j & 1, sums[j & 3]);
                 t[half * 8 + j] = fma16<DT>(x[j >> 1], w[j >> 1], j & 1, -0.0f);
             }
         }
+        float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         f = inverse_root(fmaf(sum, 1.0f / kLatent, a.eps));
@@ -232,9 +371,9 @@ __global__ void __launch_bounds__(ROWS_NT, NORM_CTAS) norm_kernel(const __grid_c
             st_v4(dst + half * 512 + lane * 16, pack16<DT>(x));
         }
     } else if (ROW == kRow8) {
-        store8(dst, t, f, lane);
+        if (store8<NORM>(dst, t, f, lane)) exact_row<DT, ROW>(a);
     } else {
-        store4<NORM>(dst, t, f, lane);
+        if (store4<NORM>(dst, t, f, lane)) exact_row<DT, ROW>(a);
     }
 }
 

@@ -123,10 +123,11 @@ int hisparse_page_tables(const hisparse_page_tables_args *args, void *stream);
  *               whose slot is negative or not below num_rows is not stored.
  *               Of two values with one slot, either's bytes may stand in any
  *               part of the row.
- * With a weight, y = x / sqrt(mean of the 512 x^2 + eps) * weight, in 32 bits and
- * not rounded before it is stored (a mean that 32 bits do not hold gives 0);
- * else y = x.  Formats:
- *   1152  y rounded to `dtype`
+ * With a weight, y = x / sqrt(mean of the 512 x^2 + eps) * weight, not rounded
+ * before it is stored (a mean that 32 bits do not hold gives 0); else y = x.  Codes
+ * and scales are those of y's exact value, as long as the squares are normal numbers
+ * of 32 bits.  Formats:
+ *   1152  y, in 32 bits, rounded to `dtype`
  *    656  group scale: the least power of two, 2^-126 at least, that brings the
  *         group's largest magnitude to 448 or less (infinities: 2^120; NaN: NaN).
  *         A power of two loses nothing to any other scale but at the smallest

@@ -95,6 +95,62 @@ def test_rows_at_slots(n, dtype, row):
     assert np.array_equal(values[:, 512:].double().cpu().numpy(), rope)
 
 
+def nearest(v, table):
+    """The entries of table (rising; ties to the even one) nearest to v >= 0."""
+    hi = np.clip(np.searchsorted(table, v), 1, len(table) - 1)
+    a, b = v - table[hi - 1], table[hi] - v
+    return table[np.where((a < b) | ((a == b) & (hi % 2 == 1)), hi - 1, hi)]
+
+
+def exact_values(y, row):
+    """What codes and scales of unlimited precision stand for."""
+    group = 128 if row == M.ROW8 else 16
+    g = np.abs(y).reshape(len(y), -1, group)
+    top = g.max(2)
+    codes = M.E4M3[:127] if row == M.ROW8 else np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
+    scale = (M.scale8(top) if row == M.ROW8 else nearest(np.minimum(top / 6, 448.0), M.E4M3[:127]))[:, :, None]
+    q = np.minimum(g / np.where(scale > 0, scale, 1.0), codes[-1])
+    return np.where(scale > 0, nearest(q, codes) * scale, 0.0).reshape(y.shape) * np.sign(y)
+
+
+@pytest.mark.parametrize("row", [M.ROW4, M.ROW8])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("spread", [1.0, 2.0 ** -6])
+def test_codes_and_scales_are_those_of_unlimited_precision(dtype, row, spread):
+    """Every one of 10 million (4 million of them beside groups of zeros, whose scale is
+    far from the row's): one that 32 bits cannot tell is worked out with more."""
+    x, w = make(20000, dtype, 11, spread)
+    x[::5, 128:256] = 0
+    rows = torch.empty((20000, row), dtype=torch.uint8, device="cuda")
+    H.norm_rows(x, rows, weight=w, eps=1e-5)
+    y = M.norm(x[:, :512].double().cpu().numpy(), w.double().cpu().numpy(), float(np.float32(1e-5)))
+    got, _ = M.values_of_rows(rows.cpu().numpy(), dtype)
+    assert np.array_equal(got, exact_values(y, row))
+
+
+def test_infinities_and_nan_of_the_weight_stay_in_their_groups():
+    x, w = make(5000, "bf16", 12)
+    x[:, 40] = torch.where(x[:, 40] == 0, 1, x[:, 40])
+    w[40], w[200] = float("inf"), float("nan")
+    finite = w.double().cpu().numpy()
+    finite[[40, 200]] = 1.0
+    y = M.norm(x[:, :512].double().cpu().numpy(), finite, float(np.float32(1e-6)))
+    for row, group in ((M.ROW8, 128), (M.ROW4, 16)):
+        rows = torch.empty((5000, row), dtype=torch.uint8, device="cuda")
+        back = torch.empty((5000, 576), dtype=torch.bfloat16, device="cuda")
+        H.norm_rows(x, rows, weight=w)
+        H.gather_rows(rows, back)
+        got, want = back[:, :512].double().cpu().numpy(), exact_values(y, row)
+        of = np.arange(512) // group
+        there = (of != 40 // group) & (of != 200 // group)
+        assert np.array_equal(got[:, there], want[:, there])
+        assert np.isnan(got[:, of == 200 // group]).all()
+        most = float("inf") if row == M.ROW8 else 2688.0      # (448 * 2^120, beyond bf16; 6 * 448)
+        assert (np.abs(got[:, 40]) == most).all()
+        rest = (of == 40 // group) & (np.arange(512) != 40)
+        assert (got[:, rest] == 0).all()
+
+
 @pytest.mark.parametrize("row", ROWS)
 def test_slots_that_are_none(row):
     """Negative, and not below the number of rows: nothing is written, nothing read."""
