@@ -17,7 +17,7 @@
 // 153.1 so, both with codes of 32 bits).  Products of 16-bit pairs go straight into 32 bits.
 // Not kept: values read with the hint that they leave L2 first (2 to 6 % less for 65,536
 // rows, 3 to 6 % more for 16,384 and for 196,608 and up).  There and back, at slots in no
-// order: 262,144 rows of 656 bytes 156.5 us, 0.90 of the copy rate; 70,001 of 416 38.1, 0.81
+// order: 262,144 rows of 656 bytes 157 us, 0.89 of the copy rate; 70,001 of 416 38.7, 0.80
 // (with codes of 32 bits 152.5 and 36.9).
 #include "pages.cuh"
 
