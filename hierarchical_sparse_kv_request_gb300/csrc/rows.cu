@@ -241,9 +241,11 @@ __device__ __forceinline__ Twice over(const Twice &x, float y)
     return together(h, __fmul_rn(__fadd_rn(__fmaf_rn(-h, y, x.hi), x.lo), inv));
 }
 
-// 1 / sqrt(v): a step of Newton's method, its difference kept apart.
+// 1 / sqrt(v): a step of Newton's method, its difference kept apart.  (Below 2^-100 v.lo has
+// lost its bits, and r^2 may be too large.)
 __device__ __forceinline__ Twice inverse_root(const Twice &v)
 {
+    if (v.hi < 0x1p-100f) return {inverse_root(v.hi), 0.0f};
     const float r = inverse_root(v.hi), p = __fmul_rn(r, r), pl = __fmaf_rn(r, r, -p);
     const float e = __fsub_rn(__fmaf_rn(-v.hi, p, 1.0f), __fmaf_rn(v.hi, pl, __fmul_rn(v.lo, p)));
     return together(r, __fmul_rn(__fmul_rn(0.5f, r), e));

@@ -124,9 +124,9 @@ int hisparse_page_tables(const hisparse_page_tables_args *args, void *stream);
  *               Of two values with one slot, either's bytes may stand in any
  *               part of the row.
  * With a weight, y = x / sqrt(mean of the 512 x^2 + eps) * weight, not rounded
- * before it is stored (a mean that 32 bits do not hold gives 0); else y = x.  Codes
- * and scales are those of y's exact value, as long as the squares are normal numbers
- * of 32 bits.  Formats:
+ * before it is stored (a mean above what 32 bits hold gives 0; one that is 0 in them,
+ * with eps 0, NaN); else y = x.  Codes and scales are those of y's exact value where
+ * the mean is between 2^-100 and 2^100.  Formats:
  *   1152  y, in 32 bits, rounded to `dtype`
  *    656  group scale: the least power of two, 2^-126 at least, that brings the
  *         group's largest magnitude to 448 or less (infinities: 2^120; NaN: NaN).

@@ -246,6 +246,31 @@ def test_sizes_far_from_one(spread):
 
 
 @pytest.mark.parametrize("row", ROWS)
+@pytest.mark.parametrize("spread", [1e-15, 1e-18, 1e-19, 2e-20, 1e15])
+def test_means_next_to_what_32_bits_hold(row, spread):
+    """As many rows as have codes that take a second look: all of them numbers, and with
+    squares that are normal numbers none far off."""
+    x, w = make(3000, "bf16", 13, spread)
+    rows = torch.empty((3000, row), dtype=torch.uint8, device="cuda")
+    H.norm_rows(x, rows, weight=w, eps=0.0)
+    assert np.isfinite(M.values_of_rows(rows.cpu().numpy(), "bf16")[0]).all()
+    if spread in (1e-15, 1e15):
+        check(M.norm(x[:, :512].double().cpu().numpy(), w.double().cpu().numpy(), 0.0), x[:, 512:], rows, "bf16", row)
+
+
+@pytest.mark.parametrize("row", ROWS)
+def test_a_mean_of_zero_without_eps(row):
+    x, w = make(3, "bf16", 14)
+    x[0, :512], x[1, :512] = 0, 1e-25
+    rows = torch.empty((3, row), dtype=torch.uint8, device="cuda")
+    back = torch.empty((3, 576), dtype=torch.bfloat16, device="cuda")
+    H.norm_rows(x, rows, weight=w, eps=0.0)
+    H.gather_rows(rows, back)
+    assert torch.isnan(back[:2, :512]).all() and torch.isfinite(back[2]).all()
+    assert torch.equal(back[:, 512:], x[:, 512:])
+
+
+@pytest.mark.parametrize("row", ROWS)
 def test_strides_streams_and_graphs(row):
     n = 50
     x, w = make(n, "bf16", 8)
