@@ -1028,9 +1028,9 @@ cudaError_t launch(const PrefixLaunch &a, const PrefixParts &w, cudaStream_t s)
         if (e != cudaSuccess) return e;
         if (w.joins == 0) return e;
     }
-    // Four warps a head where there are few, with many parts each (32 x 16 heads over 8,192
-    // rows: 25.0 us, with one 31.8, at the time), else one (32 x 128 heads, 2 or 3 parts each:
-    // 63.1 us, with four 66.8).
+    // Four warps a head where there are few, with many parts each (8,192 rows and 32 x 16
+    // heads: 22.9 us, with one 23.4; 16 x 64: 29.5 and 31.5), else one (16 x 128: 39.6 us, with
+    // four 42.3).
     const int heads = (w.pairs > 0 ? w.joins : w.groups) * PAIR_HEADS;
     if (heads <= JOIN_WIDE) return launch_behind(join_kernel<DT, 4>, dim3(heads), JOIN_NT, 0, 1, s, a, w);
     return launch_behind(join_kernel<DT, 1>, dim3(heads / 4), JOIN_NT, 0, 1, s, a, w);

@@ -358,3 +358,19 @@ def test_the_longest_prefix():
     tol = HALF["bf16"] * np.abs(want) + (np.expm1(2 * ds) + HALF["bf16"] + 20000 * U32)[:, None] * sp["abs"]
     assert (np.abs(out[0].double().cpu().numpy() - want) <= tol).all()
     assert (np.abs(lse[0].double().cpu().numpy() - w_lse - np.log(256.0)) <= ds + 20000 * U32).all()
+
+
+def test_pages_past_two_gigabytes():
+    """2.4 GB of rows, the prefix's pages the last of them."""
+    n, bs, dtype = 300, 64, "bf16"
+    count = 2 ** 31 // M.ROW16 + 40 * bs
+    count -= count % bs
+    rows = torch.zeros((count, M.ROW16), dtype=torch.uint8, device="cuda")
+    last = make_rows(8 * bs, dtype, M.ROW16, 3)
+    rows[-8 * bs:] = last
+    table = torch.tensor([count // bs - 1 - k for k in range(5)], dtype=torch.int32, device="cuda")
+    q = make_q(2, 20, dtype, 4)
+    out, lse = torch.empty((2, 20, 512), dtype=TYPES[dtype], device="cuda"), torch.empty((2, 20), device="cuda")
+    H.attend_prefix(q, rows, table, bs, n, out, 576 ** -0.5, lse=lse)
+    near = torch.tensor([7 - k for k in range(5)], dtype=torch.int32, device="cuda")
+    check(q, named(last, near, bs, n), out, lse, float(np.float32(576 ** -0.5)), dtype)
