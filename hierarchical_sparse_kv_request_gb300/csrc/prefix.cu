@@ -298,6 +298,51 @@ struct HeadPlace {
     __device__ __forceinline__ HeadPlace(const PrefixLaunch &a, int head) : r(head / a.H), h(head - r * a.H) {}
 };
 
+// How scores are made: queries (two a word) are multiplied by `query`, the products by 4 if
+// `fourfold` and by f, positive, which makes base-2 scores.  The sign of the scale goes
+// into the queries, and in bf16, which has the range for it, its power of two: a product
+// is then about as large as the score, and beyond 32 bits only if that is.  (A query times
+// a power of two is exact from 2^-126 on.)  In f16 products are far within 32 bits, and
+// a factor of 4 comes off scales that log2(e) would take beyond them.
+template <int DT>
+struct ScoreFactors {
+    uint32_t query;
+    float f;
+    bool fourfold;
+    __device__ __forceinline__ explicit ScoreFactors(float scale)
+    {
+        const float size = fabsf(scale);
+        uint32_t by;
+        fourfold = false;
+        if (!(size <= FLT_MAX)) {
+            by = 0x7FFFu;      // NaN
+            f = 1.0f;
+        } else if (size == 0.0f) {
+            by = 0u;           // (f 0 would make NaN of the -inf of a row that is not there)
+            f = 1.0f;
+        } else if (DT == kBf16) {
+            const uint32_t bits = __float_as_uint(size), e = max(bits >> 23, 1u);
+            by = e << 7;
+            f = (bits >> 23 ? __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u) : size * 0x1p126f) * kLog2e;
+        } else {
+            by = 0x3C00u;
+            fourfold = size > 0x1p126f;
+            f = size * (fourfold ? 0.25f * kLog2e : kLog2e);
+        }
+        if (scale < 0.0f) by |= 0x8000u;
+        query = by * 0x10001u;
+    }
+    __device__ __forceinline__ uint32_t of(uint32_t x) const
+    {
+        uint32_t y;
+        if (DT == kBf16)
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(query));
+        else
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(query));
+        return y;
+    }
+};
+
 // Whether all threads that meet at a named barrier go on.  (Nothing limits this
 // wait: all of them come here, whatever has gone wrong.)
 __device__ __forceinline__ bool meet(int id, int threads, bool go)
@@ -378,17 +423,15 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(192)
         };
         auto meet_half = [&](bool go) { return meet(1 + (warp & 1), 64, go); };      // the warp with the heads' other half
         auto meet_all = [&](bool go) { return meet(3, SOFTMAX * 32, go); };
-        // (scale 0: not 0 times the -inf of a row that is not there)
-        const bool nan = a.scale != a.scale;
-        const float f = nan ? 1.0f : fmaxf(fabsf(a.scale) * kLog2e, FLT_MIN);
-        // The queries of a group, with the sign of the scale (or NaN): eight threads a
-        // head's 128 bytes, all of it on its way at once; then through P's place, 16 KB at
-        // a time, to a thread's lane.  (A thread its own head's, 16 bytes of 32 heads a
-        // load: 11 thousand cycles against 5.)
+        const ScoreFactors<DT> factors(a.scale);
+        const float f = factors.f;
+        // The queries of a group, times their factor: eight threads a head's 128 bytes, all
+        // of it on its way at once; then through P's place, 16 KB at a time, to a thread's
+        // lane.  (A thread its own head's, 16 bytes of 32 heads a load: 11 thousand cycles
+        // against 5.)
         const int heads = a.R * a.H;
         auto place_queries = [&](int group) {
             const int share = heads_of_cta(heads, group), head0 = group * PAIR_HEADS + rank * share;
-            const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, set = nan ? 0x7FFF7FFFu : 0u;
             const int unit = lane & 7, first = warp * 4 + (lane >> 3);      // heads first + 16 k
             uint4 v[9][4];
 #pragma unroll
@@ -408,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(192)
                 for (int k = 0; k < 4; ++k) {
                     const int h = first + 16 * k;
                     st_smem_v4(block + h * 128 + ((unit ^ (h & 7)) << 4),
-                               make_uint4((x[k].x ^ flip) | set, (x[k].y ^ flip) | set, (x[k].z ^ flip) | set, (x[k].w ^ flip) | set));
+                               make_uint4(factors.of(x[k].x), factors.of(x[k].y), factors.of(x[k].z), factors.of(x[k].w)));
                 }
             };
 #pragma unroll
@@ -487,6 +530,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(192)
                 tc_fence_before();
                 tell(read_at + (n & 1) * 8);
                 float (&x)[2][32] = reinterpret_cast<float (&)[2][32]>(v);
+                if (DT == kF16 && factors.fourfold)
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) x[j >> 5][j & 31] *= 4.0f;
                 if ((named.x & named.y & named.z & named.w) != 0x0F0F0F0Fu) {
                     const uint32_t lo = bits_of(named.x, named.y), hi = bits_of(named.z, named.w);
 #pragma unroll

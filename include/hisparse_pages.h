@@ -167,7 +167,7 @@ typedef struct hisparse_attend_prefix_args {
     const int32_t *table;          /* device-addressable [ceil(prefix_len / block_size)] */
     int32_t block_size;            /* tokens a page, >= 1 */
     int32_t prefix_len;            /* tokens, 0 .. HISPARSE_MAX_PREFIX */
-    float scale;                   /* of the scores, before the softmax */
+    float scale;                   /* of the scores, before the softmax; any, see below */
     const void *part;              /* device [R][H][512] of `dtype`, or NULL */
     int64_t part_request_stride;
     int64_t part_head_stride;
@@ -200,8 +200,10 @@ typedef struct hisparse_attend_prefix_args {
  * Products accumulate in 32 bits.  Latent values are used in `dtype`: exact but
  * as hisparse_gather_rows says.  Probabilities enter the second product in
  * `dtype`, relative to a running maximum; everything else of the softmax is
- * 32-bit; out is rounded once.  Results repeat bit for bit.  A NaN scale gives NaN
- * wherever a token is named.
+ * 32-bit; out is rounded once.  Results repeat bit for bit.  scale may
+ * be any number as long as the scores are below 2.3e38 (beyond it, NaN); in bf16 its
+ * power of two is multiplied into the queries, which loses bits of values that come
+ * below 2^-126 by it.  A NaN or infinite scale gives NaN wherever a token is named.
  * A bounded wait of the kernel's that runs out (not expected) leaves status
  * ATTEND_TIMEOUT with every request; with status NULL neither that nor
  * BAD_RESIDENT leaves a trace.
