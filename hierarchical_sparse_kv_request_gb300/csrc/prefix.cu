@@ -298,22 +298,21 @@ struct HeadPlace {
     __device__ __forceinline__ HeadPlace(const PrefixLaunch &a, int head) : r(head / a.H), h(head - r * a.H) {}
 };
 
-// How scores are made: queries (two a word) are multiplied by `query`, the products by 4 if
-// `fourfold` and by f, positive, which makes base-2 scores.  The sign of the scale goes
+// How scores are made: queries (two a word) are multiplied by `query`, the products by f,
+// positive, and `more`, which makes base-2 scores.  The sign of the scale goes
 // into the queries, and in bf16, which has the range for it, its power of two: a product
 // is then about as large as the score, and beyond 32 bits only if that is.  (A query times
 // a power of two is exact from 2^-126 on.)  In f16 products are far within 32 bits, and
-// a factor of 4 comes off scales that log2(e) would take beyond them.
+// a factor of 4 comes off f where log2(e) would take it beyond them.
 template <int DT>
 struct ScoreFactors {
     uint32_t query;
-    float f;
-    bool fourfold;
+    float f, more;
     __device__ __forceinline__ explicit ScoreFactors(float scale)
     {
         const float size = fabsf(scale);
         uint32_t by;
-        fourfold = false;
+        more = 1.0f;
         if (!(size <= FLT_MAX)) {
             by = 0x7FFFu;      // NaN
             f = 1.0f;
@@ -326,8 +325,8 @@ struct ScoreFactors {
             f = (bits >> 23 ? __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u) : size * 0x1p126f) * kLog2e;
         } else {
             by = 0x3C00u;
-            fourfold = size > 0x1p126f;
-            f = size * (fourfold ? 0.25f * kLog2e : kLog2e);
+            if (size > 0x1p126f) more = 4.0f;
+            f = size * (kLog2e / more);
         }
         if (scale < 0.0f) by |= 0x8000u;
         query = by * 0x10001u;
@@ -342,6 +341,14 @@ struct ScoreFactors {
         return y;
     }
 };
+
+// A reference is a rounded score, and the weights' exponents are differences from it that
+// leave that rounding out: half a step, from here on a sixteenth and more (at 2^29 a factor
+// of 2^32, at 2^31 beyond 32 bits).  Scores are then rounded too before the reference comes
+// off.  (In a branch of its own, as far as P's stores: with the exponents chosen in the
+// loop that all tiles go through 32 x 128 heads over 8,192 rows take 63.0 us instead of 62.0,
+// 61.6 with no such branch.)
+constexpr float kFarReference = 1 << 20;
 
 // Whether all threads that meet at a named barrier go on.  (Nothing limits this
 // wait: all of them come here, whatever has gone wrong.)
@@ -516,6 +523,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(192)
             place_queries(group);
             if (group == begin.group) after_launch_before();
             float m = -INFINITY, l = 0.0f;
+            bool far = factors.more != 1.0f;      // or one of the warp's references is: see kFarReference
             const uint8_t *there = w.there + half * 16;
             uint4 next = *reinterpret_cast<const uint4 *>(there + (int64_t)t0 * 32);
             for (int t = t0; t < t1; ++t, ++n) {
@@ -530,9 +538,6 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(192)
                 tc_fence_before();
                 tell(read_at + (n & 1) * 8);
                 float (&x)[2][32] = reinterpret_cast<float (&)[2][32]>(v);
-                if (DT == kF16 && factors.fourfold)
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) x[j >> 5][j & 31] *= 4.0f;
                 if ((named.x & named.y & named.z & named.w) != 0x0F0F0F0Fu) {
                     const uint32_t lo = bits_of(named.x, named.y), hi = bits_of(named.z, named.w);
 #pragma unroll
@@ -549,20 +554,62 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(192)
                     top[2] = fmaxf(top[2], x[1][j]);
                     top[3] = fmaxf(top[3], x[1][j + 1]);
                 }
-                float s = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
+                float s = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f * factors.more;
                 sm.top[n & 1][half][i] = s;
                 if (!(ok = meet_half(ok))) break;
                 s = fmaxf(s, sm.top[n & 1][half ^ 1][i]);
+                // P and O are free once the product before is done: O times d, and P in its place
+                auto add = [&](bool is_free, bool moves, float d) {
+                    if (!all(is_free) && !(ok = all(mbar_wait(bar(sm.added), (n - 1) & 1, gave_up)))) return;
+                    if (moves && t > t0) {
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 256; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld_32(lanes + T_O + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * d);
+                            tmem_st_32(lanes + T_O + c, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    const uint32_t p_at = base + P_AT + half * BLOCK + i * 128;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            st_smem_v4(p_at + (((k * 4 + y) ^ (i & 7)) << 4),
+                                       make_uint4(v[k][4 * y], v[k][4 * y + 1], v[k][4 * y + 2], v[k][4 * y + 3]));
+                    fence_async_smem();
+                    tc_fence_before();
+                    tell(weighed_at);
+                };
                 float d = 1.0f;
-                const bool moves = __any_sync(0xffffffffu, s > m + kMoveAbove);
+                // (m + 8 may round to the next number)
+                const bool moves = __any_sync(0xffffffffu, s - m > kMoveAbove || far);
                 if (moves) {
                     const float to = fmaxf(m, s);
                     d = to == -INFINITY ? 1.0f : ex2(m - to);
                     m = to;
                     l *= d;
+                    far = factors.more != 1.0f || __any_sync(0xffffffffu, fabsf(m) >= kFarReference && m != -INFINITY);
+                    if (far) {
+                        const float r = m == -INFINITY ? 0.0f : -m;
+                        auto weight = [&](float product) { return ex2(fmaf(__fmul_rn(product, f), factors.more, r)); };
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) {
+                                const float p0 = weight(x[k][j]), p1 = weight(x[k][j + 1]);
+                                l += p0 + p1;
+                                v[k][j >> 1] = floats_to_pair<DT>(p0, p1);
+                            }
+                        add(n == 0, true, d);
+                        continue;
+                    }
                 }
-                // P and O are free once the product before is done (asked ahead of the
-                // exponentials, which hide how long that takes)
+                // (asked ahead of the exponentials, which hide how long that takes)
                 const bool is_free = n == 0 || mbar_try(bar(sm.added), (n - 1) & 1);
                 const float r = m == -INFINITY ? 0.0f : -m;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -575,30 +622,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(192)
                         v[k][j >> 1] = floats_to_pair<DT>(p0, p1);
                     }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                if (!all(is_free) && !(ok = all(mbar_wait(bar(sm.added), (n - 1) & 1, gave_up)))) continue;
-                if (moves && t > t0) {
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < 256; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld_32(lanes + T_O + c, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * d);
-                        tmem_st_32(lanes + T_O + c, o);
-                    }
-                    tmem_wait_st();
-                }
-                const uint32_t p_at = base + P_AT + half * BLOCK + i * 128;
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        st_smem_v4(p_at + (((k * 4 + y) ^ (i & 7)) << 4),
-                                   make_uint4(v[k][4 * y], v[k][4 * y + 1], v[k][4 * y + 2], v[k][4 * y + 3]));
-                fence_async_smem();
-                tc_fence_before();
-                tell(weighed_at);
+                add(is_free, moves, d);
             }
             ok = ok && all(mbar_wait(bar(sm.added), (n - 1) & 1, gave_up));
             tc_fence_after();
