@@ -4,8 +4,8 @@
 // The mathematics.  The heads of all requests are the rows of one matrix Q (M = R
 // H rows of 576).  With s = scale * log2(e) * (q . row), a running reference m of
 // the row maximum, l = sum 2^(s - m) and O = sum 2^(s - m) * latent over the rows
-// seen so far; when s outgrows m by more than 8, m moves and l and O are
-// multiplied by 2^(m_old - m_new).  A part comes in as one more row of score
+// seen so far; when s outgrows m by more than 8 (f16: see kBelowF16), m moves and l
+// and O are multiplied by 2^(m_old - m_new).  A part comes in as one more row of score
 // part_lse * log2(e) and value part.  out = O / l, lse = (m + log2 l) ln 2.
 //
 // Three launches.  expand_kernel reads the prefix's pages once and writes its rows
@@ -350,6 +350,15 @@ struct ScoreFactors {
 // 61.6 with no such branch.)
 constexpr float kFarReference = 1 << 20;
 
+// In f16 weights below 2^-14 lose bits and those below 2^-25 are 0, however many they are: the
+// reference lies 2^7 below the largest score when it moves, and moves for one above 2^15 of it
+// (65,504 is f16's largest; a far reference, rounded to more than that, stays where the score
+// is, as its neighbours weigh nothing).  So at most 2^-32 of the largest weight is lost a
+// row, 2^-12 with the most rows, half of out's own half step.  (With 2^9 the reference moves
+// more often: 32 x 128 heads over 8,192 rows 63.3 us, 37 x 40 over 5,003 28.2; 2^7 62.4 and 27.8, as
+// with the reference at the largest score.)
+constexpr float kBelowF16 = 7.0f, kAboveF16 = 15.0f;
+
 // Whether all threads that meet at a named barrier go on.  (Nothing limits this
 // wait: all of them come here, whatever has gone wrong.)
 __device__ __forceinline__ bool meet(int id, int threads, bool go)
@@ -430,6 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(192)
         };
         auto meet_half = [&](bool go) { return meet(1 + (warp & 1), 64, go); };      // the warp with the heads' other half
         auto meet_all = [&](bool go) { return meet(3, SOFTMAX * 32, go); };
+        constexpr float BELOW = DT == kF16 ? kBelowF16 : 0.0f, ABOVE = DT == kF16 ? kAboveF16 : kMoveAbove;
         const ScoreFactors<DT> factors(a.scale);
         const float f = factors.f;
         // The queries of a group, times their factor: eight threads a head's 128 bytes, all
@@ -586,10 +596,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(192)
                     tell(weighed_at);
                 };
                 float d = 1.0f;
-                // (m + 8 may round to the next number)
-                const bool moves = __any_sync(0xffffffffu, s - m > kMoveAbove || far);
+                // (the difference: m + ABOVE may round to the next number)
+                const bool moves = __any_sync(0xffffffffu, s - m > ABOVE || far);
                 if (moves) {
-                    const float to = fmaxf(m, s);
+                    const float to = fmaxf(m, fabsf(s) < kFarReference ? s - BELOW : s);
                     d = to == -INFINITY ? 1.0f : ex2(m - to);
                     m = to;
                     l *= d;
