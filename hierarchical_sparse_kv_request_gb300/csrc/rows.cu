@@ -97,6 +97,12 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
+// x with the sign of y: of a 0, which sums and products of two numbers lose.
+__device__ __forceinline__ float signed_as(float x, float y)
+{
+    return __uint_as_float((__float_as_uint(x) & 0x7FFFFFFFu) | (__float_as_uint(y) & 0x80000000u));
+}
+
 // How far t f / scale may be from what it stands for: 13 roundings of 2^-24 (of the sum of
 // squares 10, of which the root halves what they come to; the mean, the root 2, 1 / scale 2,
 // the products 3).  Codes and scales that are the same this far to both sides are those of
@@ -191,8 +197,7 @@ __device__ __forceinline__ bool store4(uint8_t *dst, float (&t)[16], float f, in
         const float inv = scale == 0.0f ? 0.0f : __frcp_rn(scale);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            const float x = __fadd_rn(__fmaf_rn(t[j], inv, 48.0f), -48.0f);
-            t[j] = __uint_as_float((__float_as_uint(x) & 0x7FFFFFFFu) | (__float_as_uint(t[j]) & 0x80000000u));
+            t[j] = signed_as(__fadd_rn(__fmaf_rn(t[j], inv, 48.0f), -48.0f), t[j]);
         }
         c = make_uint2(e2m1x8(t, 0), e2m1x8(t, 8));
     }
@@ -302,7 +307,7 @@ __device__ __noinline__ void exact_row(const RowsLaunch &a)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
             const Twice y = times(f, t[j]);
-            t[j] = to_odd({y.hi * by, y.lo * by});
+            t[j] = signed_as(to_odd({y.hi * by, y.lo * by}), t[j]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) c[j] = e4m3x4(t[4 * j], t[4 * j + 1], t[4 * j + 2], t[4 * j + 3]);
@@ -314,7 +319,7 @@ __device__ __noinline__ void exact_row(const RowsLaunch &a)
         const float scale = __low2float(scale_half2(e8 & 0xFFu));
         const Twice g = scale == 0.0f ? Twice{0.0f, 0.0f} : over(f, scale);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) t[j] = to_odd(times(g, t[j]));
+        for (int j = 0; j < 16; ++j) t[j] = signed_as(to_odd(times(g, t[j])), t[j]);
         *reinterpret_cast<uint2 *>(dst + lane * 8) = make_uint2(e2m1x8(t, 0), e2m1x8(t, 8));
         dst[kScaleAt + lane] = (uint8_t)e8;
     }
