@@ -2,12 +2,13 @@
 // (include/hisparse_pages.h, hisparse_norm_rows, hisparse_gather_rows).
 //
 // The mathematics.  y = x w / sqrt(mean x^2 + eps): the product t = x w of two 16-bit
-// values is exact in 32 bits, so y = t f has one rounding of its own and those of the one
+// values is exact in 32 bits (as long as it is a normal number there), so y = t f has one rounding of its own and those of the one
 // factor f = 1 / sqrt, and the largest |y| of a group is that of t, times f.  Then per
 // group of 128 values a power of two s and e4m3 codes of t (f / s), per group of 16 an
 // e4m3 scale and e2m1 codes, or y in 16 bits.  Codes and scales are those of unlimited
-// precision: worked out with f too small and too large by what it may be off, and, where
-// that makes a difference, with numbers of 47 bits.
+// precision (a y within 2^-42 of a border between two counts as on it): worked out with f
+// too small and too large by what it may be off, and, where that makes a difference, with
+// pairs of numbers.
 //
 // Bound by HBM: 1,152 bytes of values and 416 to 1,152 of row, each moved once; nothing
 // is kept between rows; and, next to it, by instructions.  A warp works on a whole row.  For
@@ -239,7 +240,7 @@ __device__ __forceinline__ Twice times(const Twice &x, float y)
     return together(h, __fmaf_rn(x.lo, y, __fmaf_rn(x.hi, y, -h)));
 }
 
-// 1 / x: what the approximate quotient leaves, once.
+// x / y: what the approximate quotient leaves, once.
 __device__ __forceinline__ Twice over(const Twice &x, float y)
 {
     const float inv = __frcp_rn(y), h = __fmul_rn(x.hi, inv);
@@ -257,11 +258,14 @@ __device__ __forceinline__ Twice inverse_root(const Twice &v)
 }
 
 // In 32 bits, cut off, with the last bit set if that is not exact: rounded again to fewer
-// bits it gives what x does.
+// bits it gives what x does.  A pair here is off by 12 roundings of 2^-47 (of the sum of
+// squares 11, halved by the root; the mean, the root 2, the products 3): nearer than 2^-42 to a
+// number of 24 bits, which borders between codes are, x counts as that number.  (Without
+// that a y that lies on a border, as with rows of one magnitude and eps 0, got the code below.)
 __device__ __forceinline__ float to_odd(const Twice &x)
 {
     const uint32_t h = __float_as_uint(x.hi), l = __float_as_uint(x.lo);
-    return x.lo == 0.0f ? x.hi : __uint_as_float((h - ((h ^ l) >> 31)) | 1u);
+    return !(fabsf(x.lo) > fabsf(x.hi) * 0x1p-42f) ? x.hi : __uint_as_float((h - ((h ^ l) >> 31)) | 1u);
 }
 
 // The row that value i goes to or comes from; -1: none.
@@ -300,7 +304,7 @@ __device__ __noinline__ void exact_row(const RowsLaunch &a)
     const Twice f = inverse_root(plus({sum.hi / kLatent, sum.lo / kLatent}, {a.eps, 0.0f}));
     const Twice top = times(f, largest<ROW == kRow8 ? 8 : 1>(t));
     if (ROW == kRow8) {
-        // (448 is even: a top just above a border is above it when its last bit is set)
+        // (448 is even: a top above a border is above it when its last bit is set)
         const int k = scale_exponent(min(__float_as_uint(to_odd(top)), 0x7F800000u));
         const float by = power_of_two(-k);      // (f times this may be too much: see store8)
         uint32_t c[4];

@@ -125,8 +125,11 @@ int hisparse_page_tables(const hisparse_page_tables_args *args, void *stream);
  *               part of the row.
  * With a weight, y = x / sqrt(mean of the 512 x^2 + eps) * weight, not rounded
  * before it is stored (a mean above what 32 bits hold gives 0; one that is 0 in them,
- * with eps 0, NaN); else y = x.  Codes and scales are those of y's exact value where
- * the mean is between 2^-100 and 2^100.  Formats:
+ * with eps 0, NaN); else y = x.  Codes and scales are those of y's exact value, which
+ * counts as on a border between two if it is nearer to it than 2^-42 of itself, where
+ * the mean is between 2^-100 and 2^100 and the products x * weight are 0 or between
+ * 2^-126 and 3.4e38.  (Those that are not are taken as 32 bits have them: bf16's
+ * smallest lose bits, its largest are infinite.)  Formats:
  *   1152  y, in 32 bits, rounded to `dtype`
  *    656  group scale: the least power of two, 2^-126 at least, that brings the
  *         group's largest magnitude to 448 or less (infinities: 2^120; NaN: NaN).
