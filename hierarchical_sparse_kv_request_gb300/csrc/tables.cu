@@ -417,18 +417,28 @@ static cudaError_t launch_tables(const TablesLaunch &a, const Divider &by, cudaS
     return launch_behind(tables_kernel<CTAS, NT, MAP>, dim3(CTAS), NT, requests_bytes(a.R, MAP), CTAS, s, a, by);
 }
 
+// One CTA for a decode step, a cluster of sixteen where many pages may come and go.  What a
+// call moves is known on the device alone; on the host, that a step has few tokens (or, where
+// none are placed, few requests), and that it moves no more pages than the tables hold
+// behind the shared prefix.  GPU time of a call there and one back, one CTA and the cluster:
+// up to 4 tokens more for 32 requests of 626 pages each 7.9 and 9.0 us, for 256 of 626 9.0 and
+// 9.7; 4 of those 256 finished and back 15.7 and 12.5; all 32 finished and back 37 and
+// 10.7, 32 of 1,281 pages 64 and 11.6, of 81,921 3,495 and 162.  (Prompts: 128 requests of 2,048
+// to 81,920 tokens 90 us and 20.8, 23.2 with eight CTAs of 1,024 threads.)
+constexpr int64_t kStepPages = 32768;
+static bool one_cta(const TablesLaunch &a)
+{
+    if ((int64_t)a.R * (a.W - a.shared_count) > kStepPages) return false;
+    return a.new_tokens ? a.R <= 256 && a.tokens <= 4096 : a.R <= 32;
+}
+
 cudaError_t launch_page_tables(const TablesLaunch &a, cudaStream_t s)
 {
     const Divider by(a.bs);
     // Few slots in the same launch (1.0 M in one: 69 us for 256 requests with a
     // cluster of eight, 25 in two).
     const bool map = a.new_tokens && a.tokens <= 16384;
-    // One CTA for what a decode step moves (32 requests, 4 drafts each: 6.6 us for a call
-    // there and one back, 8.5 with a cluster of eight), a cluster of sixteen where whole
-    // prompts come and go (128 requests of 2,048 to 81,920 tokens: 20.8 us, 23.2 with eight
-    // of 1,024 threads, 90 with one CTA).  What a call moves is known on the device alone: a
-    // step has few tokens, and where none are placed, few requests.
-    const bool step = a.new_tokens ? a.R <= 256 && a.tokens <= 4096 : a.R <= 32;
+    const bool step = one_cta(a);
     const cudaError_t e = step ? map ? launch_tables<1, 256, true>(a, by, s) : launch_tables<1, 256, false>(a, by, s)
                                : map ? launch_tables<16, 512, true>(a, by, s) : launch_tables<16, 512, false>(a, by, s);
     if (e != cudaSuccess || !a.new_tokens || map || a.tokens == 0) return e;
