@@ -88,3 +88,52 @@ def test_largest_scales_in_f16(scale):
     assert torch.equal(out, rows[best, :512].expand_as(out))
     want = float(np.float32(scale)) * 2.0 ** -48 * best
     assert (lse.double() - want).abs().max() <= 4 * 2.0 ** -24 * abs(want) + 2.0 ** -20
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("order", ["rising", "falling", "shuffled"])
+@pytest.mark.parametrize("scale", [1e4, 3e6, 1e9, -1e9, 1e20, 3e38])
+def test_a_pair_goes_through_several_tiles(scale, order, dtype):
+    """Heads for all pairs, eight tiles each, the reference moving between them; joined with
+    parts far above (even heads), far below (odd ones), and of no weight."""
+    n, R, heads = 1000, 19, 512
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn((n, 576), generator=g, device="cuda")
+    x[:, 0] = (torch.arange(n, device="cuda") // 10) / 128.0 - 0.4       # tens of rows alike
+    x[-10:-1, 0], x[1:10, 0] = 0.3, -0.3                                 # but the largest and the smallest
+    x[:, 512:] = 0
+    x16 = x.to(TYPES[dtype])
+    rows = torch.empty((n, M.ROW16), dtype=torch.uint8, device="cuda")
+    H.norm_rows(x16, rows)
+    table = {"rising": torch.arange(n), "falling": torch.arange(n).flip(0),
+             "shuffled": torch.randperm(n, generator=torch.Generator().manual_seed(1))}[order].to(torch.int32).cuda()
+    q = torch.zeros((R, heads, 576), dtype=TYPES[dtype], device="cuda")
+    size = 2.0 ** -10 if abs(scale) > 1e38 else 1.0                      # (scores stay in range)
+    q[:, :, 0] = size * torch.where(torch.arange(heads, device="cuda") % 4 < 2, 1.0, -1.0).to(TYPES[dtype])
+    s32 = float(np.float32(scale))
+    score = s32 * q[0, :4, 0].double()[:, None] * x16[:, 0].double()[None]      # (the same for every fourth head)
+    top = score.amax(1)
+    part = torch.randn((R, heads, 512), generator=g, device="cuda").to(TYPES[dtype])
+    lse = (top.repeat(heads // 4) + torch.where(torch.arange(heads, device="cuda") % 2 == 0, 1.0, -1.0) * top.abs().max() / 4)
+    part_lse = lse.float().expand(R, heads).clone()
+    part_lse[5] = -float("inf")
+    part[5] = float("nan")
+    out, sums = torch.empty((R, heads, 512), dtype=TYPES[dtype], device="cuda"), torch.empty((R, heads), device="cuda")
+    alone, sums0 = torch.empty_like(out), torch.empty_like(sums)
+    H.attend_prefix(q, rows, table, 1, n, alone, scale, lse=sums0)
+    H.attend_prefix(q, rows, table, 1, n, out, scale, lse=sums, part=part, part_lse=part_lse)
+    # at 10^4 the next score is 10^4 / 256 or more away: what it weighs is below f16's step
+    weights = (score == top[:, None]).double()
+    weights /= weights.sum(1, keepdim=True)
+    want = (weights @ x16[:, :512].double()).repeat(heads // 4, 1)
+    spread = (weights @ x16[:, :512].double().abs()).repeat(heads // 4, 1)
+    tol = HALF[dtype] * want.abs() + (1 + HALF[dtype]) * (HALF[dtype] + 200 * U32) * spread + 2.0 ** -25 + 1e-12
+    assert ((alone.double() - want).abs() <= tol).all()
+    count = (score == top[:, None]).sum(1).double().log().repeat(heads // 4)
+    w = top.repeat(heads // 4) + count
+    assert ((sums0.double() - w).abs() <= 6 * U32 * w.abs() + 200 * U32).all()
+    rest = [r for r in range(R) if r != 5]
+    assert torch.equal(out[5], alone[5]) and torch.equal(sums[5], sums0[5])
+    assert torch.equal(out[rest][:, ::2], part[rest][:, ::2])
+    assert torch.equal(out[rest][:, 1::2], alone[rest][:, 1::2])
+    assert ((sums[rest][:, ::2] - part_lse[rest][:, ::2]).abs() <= 4 * U32 * part_lse[rest][:, ::2].abs()).all()
