@@ -48,17 +48,18 @@
 // the copies a tile takes 2,330.  With little, a pair's start (1 thousand cycles, queries
 // 4, while the rows are expanded) and end (5 to 7 for O, at some 25 bytes a cycle that an
 // SM stores) and the launches around it.  Measured on GB300, GPU time of a call: 256
-// requests of 16 heads over 40,000 rows 225 us (1,582 TFLOP/s, 0.82 of cuBLAS's best); 32 of
-// 128 heads over 8,192 62; 32 of 16 over 8,192 22.5; 37 of 40 over 5,003 28; 4 of 16 over
-// 2,048 10.8.
-// Rounding.  Latent values of 4-bit rows, and of 8-bit rows with powers of two as scales,
-// are exact in both types, and so are queries.  P is rounded to the model's type (half a
-// step: 2^-8 of a probability in bf16), which the product's two operands share; out's error
-// against 64 bits is 1.6 to 2.0 x 10^-3 in bf16 (the plain 32-bit form's: 1.6) and 2.4 x
-// 10^-4 in f16 (2.1).  Scores, references, sums and O are 32-bit, and sums add up a tile at
-// a time.
+// requests of 16 heads over 40,000 rows 228 us (1,564 TFLOP/s, 0.84 of cuBLAS's best), 241
+// in a long row of calls (1,479, 0.87 of its sustained rate: the power limit takes the clock
+// down); 32 of 128 heads over 8,192 62; 32 of 16 over 8,192 22.3; 37 of 40 over 5,003 27.7;
+// 4 of 16 over 2,048 11.
+// Rounding.  Queries are exact (see ScoreFactors), and latent values of 4-bit rows, and of
+// 8-bit rows with powers of two as scales, too, in f16 as far as they are among its normal
+// numbers.  P is rounded to the model's type (half a step: 2^-8 of a probability in bf16),
+// which the product's two operands share, and their sum l is of the unrounded ones, so that
+// lse does not feel it: out's error against 64 bits is 1.7 to 2.0 x 10^-3 in bf16 (the
+// plain 32-bit form's: 1.65) and 2.5 x 10^-4 in f16 (2.1).  Scores, references, sums and
+// O are 32-bit, and sums add up a tile at a time.
 #include <atomic>
-#include <mutex>
 
 #include "pages.cuh"
 
@@ -66,7 +67,7 @@ namespace hs {
 namespace {
 
 constexpr int PAIR_HEADS = 128, CTA_HEADS = 64, KEYS = 128;
-constexpr int MAX_PAIRS = 76;                    // pairs of SMs of a GB300
+constexpr int MAX_PAIRS = 76;                    // pairs of SMs of a GB300 (with fewer, in waves)
 constexpr uint32_t BLOCK = 64 * 128;             // 64 values of 64 keys, swizzled
 constexpr uint32_t PART = 2 * BLOCK, SLOT = 2 * PART;
 constexpr uint32_t HALF_TILE = 9 * BLOCK;        // 64 keys: X0 Y0 X1 Y1 rope, as they go into the slots
@@ -299,11 +300,11 @@ struct HeadPlace {
 };
 
 // How scores are made: queries (two a word) are multiplied by `query`, the products by f,
-// positive, and `more`, which makes base-2 scores.  The sign of the scale goes
-// into the queries, and in bf16, which has the range for it, its power of two: a product
-// is then about as large as the score, and beyond 32 bits only if that is.  (A query times
-// a power of two is exact from 2^-126 on.)  In f16 products are far within 32 bits, and
-// a factor of 4 comes off f where log2(e) would take it beyond them.
+// positive, and `more`, which makes base-2 scores.  The sign of the scale goes into the
+// queries, and in bf16, which has the range for it, its power of two: a product is then
+// about as large as the score, and beyond 32 bits only if that is.  (A query times a power
+// of two is exact from 2^-126 on.)  In f16 products are far within 32 bits, and a factor of
+// 4 comes off f where log2(e) would take it beyond them.
 template <int DT>
 struct ScoreFactors {
     uint32_t query;

@@ -14,19 +14,22 @@
 // is kept between rows; and, next to it, by instructions.  A warp works on a whole row.  For
 // codes a lane has 16 neighbouring values: a group of 16 is a lane's own, one of 128 eight
 // lanes', its scale worked out once a lane, and the codes' stores are contiguous (8 values
-// of each half a lane, whose loads are: 37.4 and 154.9 us for the two below, 37.2 and
-// 153.1 so, both with codes of 32 bits).  Products of 16-bit pairs go straight into 32 bits.
+// of each half a lane, whose loads are, took 1.5 us more for the first case below).  Products
+// of 16-bit pairs go straight into 32 bits.
 // Not kept: values read with the hint that they leave L2 first (2 to 6 % less for 65,536
-// rows, 3 to 6 % more for 16,384 and for 196,608 and up).  There and back, at slots in no
-// order: 262,144 rows of 656 bytes 157 us, 0.89 of the copy rate; 70,001 of 416 38.7, 0.80
-// (with codes of 32 bits 152.5 and 36.9).
+// rows, 3 to 6 % more for 16,384 and for 196,608 and up).  GPU time there and back, at slots
+// in no order: 262,144 rows of 656 bytes 157 us, 0.89 of the copy rate (152.3 without the
+// second look); 70,001 of 416 38.4, 0.80 (36.8).  norm_kernel and gather_kernel alone, 262,144
+// rows: of 416 bytes 71 and 69 us, of 656 83 and 75, of 1,152 89 and 89; without a weight
+// 66, 76 and 89.
 #include "pages.cuh"
 
 namespace hs {
 namespace {
 
 constexpr int ROWS_NT = 128;                     // threads a CTA
-constexpr int NORM_CTAS = 14, GATHER_CTAS = 16;  // CTAs an SM (norm: 12 161 us, 14 and 16 154)
+constexpr int NORM_CTAS = 14, GATHER_CTAS = 16;  // CTAs an SM (norm, 262,144 rows of 656
+                                                 // bytes: 12 90 us, 14 and 16 83)
 constexpr int ROWS_A_CTA = ROWS_NT / 32;
 
 template <int DT>
@@ -108,8 +111,9 @@ __device__ __forceinline__ float signed_as(float x, float y)
 // squares 10, of which the root halves what they come to; the mean, the root 2, 1 / scale 2,
 // the products 3).  Codes and scales that are the same this far to both sides are those of
 // unlimited precision; a row with others, one in a hundred, is done again with twice the
-// bits (exact_row).  (Without that some 40 of 10^9 codes and one of 10^6 scales are the next
-// one, as they are with 32 bits anywhere.)
+// bits (exact_row).  (Without that, counted over random rows as in perf/more_operators.py, 255
+// of 5.4 x 10^8 8-bit codes, 87 of 5.4 x 10^8 4-bit ones and 13 of 3.4 x 10^7 of their scales
+// are the next one.)
 constexpr float LOW = 1.0f - 13.0f / (1 << 24), HIGH = 1.0f + 13.0f / (1 << 24);
 
 // Values t f, those from 16 lane on, to a row.  NORM: whether a code or scale may be the

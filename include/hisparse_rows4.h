@@ -147,6 +147,8 @@ typedef struct hisparse_attend_args {
  * resident_count, BAD_POSITION for a named row's position outside
  * [0, weights_tokens) (its weight is dropped).  With status NULL
  * neither these nor ATTEND_TIMEOUT leave a trace.
+ * Scores of 2^25 and more in magnitude are beyond what the running maximum is kept
+ * in: out and lse may then be 0 or NaN.
  * A NaN scale gives NaN wherever a row is named.  One to four launches,
  * capturable.
  * Errors: INVALID_ARG, UNSUPPORTED (H or k beyond the limits), ALIGNMENT
